@@ -89,7 +89,10 @@ typedef enum qmm_status {
     QMM_ERR_WORKSPACE = 9,       /* workspace given but smaller than qmm_workspace_bytes() */
     QMM_ERR_UNSUPPORTED = 10,    /* current device is not compute capability 10.3, the path cannot take the shape,
                                     or a caller workspace is not device memory of the current device */
-    QMM_ERR_BAD_ID = 11          /* an expert id outside [0, n_experts) (reported by qmm_device_status) */
+    QMM_ERR_BAD_ID = 11,         /* an expert id outside [0, n_experts) (reported by qmm_device_status) */
+    QMM_ERR_BAD_PAGE = 12        /* a cache call met a page id outside the pool, a length beyond its page
+                                    table or a position beyond its rotary table (reported by
+                                    qmm_device_status) */
 } qmm_status;
 
 /* Kernel path selection for qmm_args.path. */
@@ -353,8 +356,9 @@ int qmm_dequant_affine(int fmt, const void *w, const void *scales, const void *b
 int qmm_check_bounded_wait(void *stream);
 
 /* Synchronizes `stream`, then reports whether any kernel enqueued so far
- * timed out on a pipeline barrier (QMM_ERR_DEVICE_TIMEOUT) or met an expert
- * id out of range (QMM_ERR_BAD_ID), and clears the flag; QMM_OK otherwise,
+ * timed out on a pipeline barrier (QMM_ERR_DEVICE_TIMEOUT), met an expert
+ * id out of range (QMM_ERR_BAD_ID) or a cache entry out of range
+ * (QMM_ERR_BAD_PAGE), and clears the flag; QMM_OK otherwise,
  * QMM_ERR_CUDA if the synchronize failed. Every
  * barrier wait in the kernels is bounded (about 2 s); on expiry the kernel
  * records the fault, stops its pipeline, releases its tensor memory and
@@ -380,6 +384,140 @@ int qmm_device_status(void *stream);
  * whose kernels can overlap on the GPU (different streams without ordering
  * between them) race on it. */
 int qmm_matmul_noalloc(const qmm_args *a);
+
+/* ---- Paged key-value cache and attention over it ------------------------
+ *
+ * The cache of a decoding model, kept in packed form and read in place. The
+ * products above turn activations into q, k and v rows (fp32); these calls
+ * rotate q and k, write k and v into the cache, attend to it, and read it
+ * back. A sequence's positions 0, 1, 2, ... live in the pages that its row of
+ * the page table lists: position p in page page_table[s][p / page_size].
+ *
+ * Memory of a page (qmm_kv_page_bytes bytes), as it is read by the attention:
+ *     [kv head][strip of 16 positions]{ K codes, K scales, V codes, V scales }
+ * F16, BF16: codes [head_dim / 16][16 positions][16 values], no scales.
+ * Q8_0: codes [head_dim / 32][16 positions][32 signed bytes], scales
+ *       [head_dim / 32][16 positions] f16; value = d * code.
+ * Q4_0: codes [head_dim / 32][16 positions][16 bytes] (byte i: dim 2i in the
+ *       low nibble, dim 2i + 1 in the high one), scales as for Q8_0;
+ *       value = d * (code - 8).
+ * Values are quantised over blocks of 32 dims of one position and head like
+ * the ggml formats of the same names, from the fp32 row x:
+ * Q8_0: d = f16(max|x| / 127), code = rint(x * (1 / d)) within +-127;
+ * Q4_0: m = the value of largest magnitude (the maximum, if the minimum is
+ *       no further from 0), d = f16(-m / 8), code = rint(x * (1 / d)) + 8
+ *       within 0..15. d = 0 gives codes of 0 (8). |d| saturates at 65504;
+ *       a block that holds an Inf or NaN gets d = NaN and reads back as NaN.
+ *
+ * New rows: a call that appends or attends works on the last n_new positions
+ * of every sequence; row i of sequence s is position lens[s] - n_new + i, and
+ * lens counts those positions already. Rows of negative position (sequences
+ * shorter than n_new, idle slots of length 0) are padding: nothing is written
+ * to the cache for them, and their outputs are zeros. q, k, v and outputs
+ * are fp32 [n_seqs * n_new][heads][head_dim] with a stride per row (so that
+ * they can be parts of one product's output rows).
+ *
+ * Checked on the device, since lengths and tables live there: a page id
+ * outside [0, n_pages), a length beyond max_pages * page_size, a position
+ * beyond the rotary table. Nothing out of range is read or written: such
+ * positions are left unwritten (append), read as zeros (read) or count as
+ * absent (attend), and qmm_device_status reports QMM_ERR_BAD_PAGE. */
+typedef struct qmm_kv_cache {
+    int fmt_k, fmt_v;          /* QMM_F16, QMM_BF16, QMM_Q8_0 or QMM_Q4_0: the same for both, or K Q8_0 with V Q4_0 */
+    void *pages;               /* device, n_pages * qmm_kv_page_bytes(), 16-byte aligned */
+    size_t pages_len;          /* bytes the caller holds at pages; 0 = not checked */
+    int64_t n_pages;           /* pages in the pool */
+    int64_t page_size;         /* positions per page: a multiple of 16, at most 65536 */
+    int64_t n_kv_heads;
+    int64_t head_dim;          /* a multiple of 32, at most 512 */
+    const int32_t *page_table; /* device, [n_seqs][table_stride] page ids; entries past a sequence's
+                                  length are not read */
+    int64_t table_stride;      /* int32 entries from one sequence's row to the next, >= max_pages */
+    int64_t max_pages;         /* entries of a row */
+    const int32_t *lens;       /* device, [n_seqs] positions held, the new ones included */
+    int64_t n_seqs;
+} qmm_kv_cache;
+
+/* Rotary pairing of qmm_kv_append. */
+typedef enum qmm_rope_style {
+    QMM_ROPE_HALF = 0,   /* dims a and a + n_rot / 2 form pair a */
+    QMM_ROPE_PAIRS = 1   /* dims 2a and 2a + 1 form pair a */
+} qmm_rope_style;
+
+typedef struct qmm_kv_append_args {
+    qmm_kv_cache cache;
+    int64_t n_new;             /* rows per sequence, >= 1 */
+    const float *k, *v;        /* device, row r at k + r * k_stride: [n_kv_heads][head_dim] */
+    int64_t k_stride, v_stride;/* floats, >= n_kv_heads * head_dim */
+    const float *q;            /* device, row r at q + r * q_stride: [n_heads][head_dim]; NULL: none */
+    float *q_out;              /* device, rotated q (zeros for padding rows); may be q itself */
+    int64_t q_stride, q_out_stride, n_heads;
+    const float *rope;         /* device, [rope_len][n_rot / 2][2]: cos and sin of each pair's angle at each
+                                  position, 16-byte aligned; NULL: nothing is rotated */
+    int64_t rope_len;
+    int64_t n_rot;             /* leading dims of a head that are rotated: a multiple of 8, at most head_dim */
+    int rope_style;            /* qmm_rope_style */
+    void *stream;
+    int flags;                 /* 0 */
+} qmm_kv_append_args;
+
+/* Bytes of one page; 0 when the formats, page size, head count or head_dim
+ * are not accepted. Host only. */
+size_t qmm_kv_page_bytes(int fmt_k, int fmt_v, int64_t page_size, int64_t n_kv_heads, int64_t head_dim);
+
+/* Appends n_new rows per sequence: k (rotated when rope is given) and v are
+ * packed into the cache at their positions, and q, when given, is rotated
+ * into q_out. With c and s the table's cos and sin of the row's position,
+ * a pair (x0, x1) becomes (x0 c - x1 s, x0 s + x1 c), every product and sum
+ * rounded to fp32. Two sequences must not share a page that is written. One
+ * launch; stream-ordered, no synchronization. */
+int qmm_kv_append(const qmm_kv_append_args *a);
+
+typedef struct qmm_kv_read_args {
+    qmm_kv_cache cache;
+    int64_t first;             /* first position read of every sequence, or -1: the last `count` positions */
+    int64_t count;             /* rows per sequence */
+    float *k, *v;              /* device, [n_seqs][count][n_kv_heads][head_dim] fp32; either may be NULL */
+    void *stream;
+    int flags;                 /* 0 */
+} qmm_kv_read_args;
+
+/* Reads the cache back as the fp32 values that its codes stand for (the
+ * product of code and scale is exact). Row i of sequence s is position
+ * first + i (first = -1: lens[s] - count + i); positions outside [0, lens[s])
+ * read as zeros. One launch, stream-ordered. */
+int qmm_kv_read(const qmm_kv_read_args *a);
+
+typedef struct qmm_attend_args {
+    qmm_kv_cache cache;        /* head_dim 64, 96, 128, 192 or 256 */
+    int64_t n_new;             /* query rows per sequence, >= 1 */
+    int64_t n_heads;           /* query heads: a multiple of n_kv_heads; head h reads kv head
+                                  h / (n_heads / n_kv_heads) */
+    const float *q;            /* device, row r at q + r * q_stride: [n_heads][head_dim] */
+    float *out;                /* device, row r at out + r * out_stride: [n_heads][head_dim] */
+    int64_t q_stride, out_stride; /* floats, >= n_heads * head_dim */
+    float scale;               /* multiplies q . k */
+    int64_t window;            /* 0: every position up to the row's own; else the last `window` of them */
+    void *workspace;           /* device scratch, 256-byte aligned, or NULL (library-owned grow-only buffer) */
+    size_t workspace_bytes;
+    void *stream;
+    int flags;                 /* 0 */
+} qmm_attend_args;
+
+/* Attention of the new rows over the cache, read in its packed form:
+ *     out[s][i][h] = sum_t softmax_t(scale * q[s][i][h] . k[s][t]) v[s][t],
+ * t over max(0, pos + 1 - window) .. pos of the row's position pos (the row's
+ * own position included, so its k and v are appended first). A row that sees
+ * no position gives zeros. Cache bytes outside the range, whatever they hold,
+ * do not reach the result. Sums, the softmax's maximum and its total are fp32;
+ * q and the weights enter the tensor cores as sums of 16-bit terms that keep
+ * at least 22 bits. The same call gives the same result each time. Scratch as
+ * for qmm_matmul_ex (calls that can run concurrently pass their own). */
+int qmm_attend(const qmm_attend_args *a);
+
+/* Device scratch bytes qmm_attend needs for *a; 0 when *a is not accepted.
+ * Host only (reads the device's SM count). */
+size_t qmm_attend_workspace_bytes(const qmm_attend_args *a);
 
 /* Message for the last non-OK status on this host thread ("" if none): the
  * text that the rullama matmul_* dispatchers (src/backend/matmul.rs) carry

@@ -7,7 +7,8 @@ functions carry the C names (``qmm_matmul``, ``qmm_matmul_ex``,
 ``qmm_dequant`` ...) and take plain integers / device pointers or torch
 tensors; ``matmul``, ``dequant``, ``matmul_backward_input``,
 ``matmul_experts``, ``matmul_affine``, ``dequant_affine`` and ``matmul_glu``
-are tensor-level conveniences over them.
+are tensor-level conveniences over them, and so are ``KvCache``,
+``kv_append``, ``kv_read`` and ``attend`` over the paged key-value cache.
 If ``libqmm.so`` has not been built, every call raises: there is no fallback.
 """
 from __future__ import annotations
@@ -27,14 +28,15 @@ FLAG_SPLIT_W = 4
 STATUS = {0: "QMM_OK", 1: "QMM_ERR_FORMAT", 2: "QMM_ERR_SHAPE", 3: "QMM_ERR_SIZE",
           4: "QMM_ERR_RANGE", 5: "QMM_ERR_NULL", 6: "QMM_ERR_ALIGN", 7: "QMM_ERR_CUDA",
           8: "QMM_ERR_DEVICE_TIMEOUT", 9: "QMM_ERR_WORKSPACE", 10: "QMM_ERR_UNSUPPORTED",
-          11: "QMM_ERR_BAD_ID"}
+          11: "QMM_ERR_BAD_ID", 12: "QMM_ERR_BAD_PAGE"}
 EXPORTS = ("qmm_weight_bytes", "qmm_matmul", "qmm_set_stream", "qmm_matmul_ex",
            "qmm_workspace_bytes", "qmm_select_path", "qmm_matmul_host", "qmm_dequant",
            "qmm_device_status", "qmm_last_error", "qmm_version", "qmm_matmul_noalloc",
            "qmm_matmul_backward_input", "qmm_backward_input_workspace_bytes",
            "qmm_matmul_experts", "qmm_matmul_affine", "qmm_dequant_affine", "qmm_matmul_glu",
            "qmm_glu_workspace_bytes", "qmm_check_bounded_wait", "qmm_matmul_experts_affine",
-           "qmm_experts_workspace_bytes")
+           "qmm_experts_workspace_bytes", "qmm_kv_page_bytes", "qmm_kv_append", "qmm_kv_read",
+           "qmm_attend", "qmm_attend_workspace_bytes")
 
 
 class QmmError(RuntimeError):
@@ -50,6 +52,39 @@ class qmm_args(ctypes.Structure):
                 ("j_end", ctypes.c_int64), ("accumulate", ctypes.c_int), ("path", ctypes.c_int),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
                 ("stream", ctypes.c_void_p), ("flags", ctypes.c_int)]
+
+
+class qmm_kv_cache(ctypes.Structure):
+    _fields_ = [("fmt_k", ctypes.c_int), ("fmt_v", ctypes.c_int), ("pages", ctypes.c_void_p),
+                ("pages_len", ctypes.c_size_t), ("n_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("n_kv_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("n_seqs", ctypes.c_int64)]
+
+
+class qmm_kv_append_args(ctypes.Structure):
+    _fields_ = [("cache", qmm_kv_cache), ("n_new", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64), ("n_heads", ctypes.c_int64),
+                ("rope", ctypes.c_void_p), ("rope_len", ctypes.c_int64), ("n_rot", ctypes.c_int64),
+                ("rope_style", ctypes.c_int), ("stream", ctypes.c_void_p), ("flags", ctypes.c_int)]
+
+
+class qmm_kv_read_args(ctypes.Structure):
+    _fields_ = [("cache", qmm_kv_cache), ("first", ctypes.c_int64), ("count", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("stream", ctypes.c_void_p),
+                ("flags", ctypes.c_int)]
+
+
+class qmm_attend_args(ctypes.Structure):
+    _fields_ = [("cache", qmm_kv_cache), ("n_new", ctypes.c_int64), ("n_heads", ctypes.c_int64),
+                ("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("window", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("stream", ctypes.c_void_p),
+                ("flags", ctypes.c_int)]
 
 
 _lib = None
@@ -89,6 +124,11 @@ def load(path: str = LIB_PATH):
         "qmm_check_bounded_wait": (i, [vp]),
         "qmm_matmul_experts_affine": (i, [pa, vp, i64, i64, vp, vp]),
         "qmm_dequant_affine": (i, [i, vp, vp, vp, i64, i64, vp, vp]),
+        "qmm_kv_page_bytes": (sz, [i, i, i64, i64, i64]),
+        "qmm_kv_append": (i, [ctypes.POINTER(qmm_kv_append_args)]),
+        "qmm_kv_read": (i, [ctypes.POINTER(qmm_kv_read_args)]),
+        "qmm_attend": (i, [ctypes.POINTER(qmm_attend_args)]),
+        "qmm_attend_workspace_bytes": (sz, [ctypes.POINTER(qmm_attend_args)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -379,3 +419,179 @@ def matmul_glu(act, fmt, w_gate, w_up, x, k: int, n: int, *, y=None, j_start=0, 
     qmm_matmul_glu(a, w_up, act)
     _keep_until_done(ws, stream)
     return y
+
+
+# -------------------------------------------------- paged key-value cache ----
+
+ROPE_HALF, ROPE_PAIRS = 0, 1
+ROPE_STYLES = {"half": ROPE_HALF, "pairs": ROPE_PAIRS}
+
+
+def qmm_kv_page_bytes(fmt_k, fmt_v, page_size: int, n_kv_heads: int, head_dim: int) -> int:
+    return load().qmm_kv_page_bytes(_fmt(fmt_k), _fmt(fmt_v), page_size, n_kv_heads, head_dim)
+
+
+def qmm_kv_append(args: qmm_kv_append_args) -> int:
+    return _check(load().qmm_kv_append(ctypes.byref(args)))
+
+
+def qmm_kv_read(args: qmm_kv_read_args) -> int:
+    return _check(load().qmm_kv_read(ctypes.byref(args)))
+
+
+def qmm_attend(args: qmm_attend_args) -> int:
+    return _check(load().qmm_attend(ctypes.byref(args)))
+
+
+def qmm_attend_workspace_bytes(args: qmm_attend_args) -> int:
+    return load().qmm_attend_workspace_bytes(ctypes.byref(args))
+
+
+class KvCache:
+    """A pool of cache pages: `pages` is a uint8 CUDA tensor [n_pages, page bytes]
+    (one page holds page_size positions of every kv head), the formats are
+    "f16", "bf16", "q8_0" or "q4_0" (the same for K and V, or K "q8_0" and V
+    "q4_0"). Page tables and lengths belong to the calls."""
+
+    def __init__(self, fmt_k, fmt_v, pages, page_size: int, n_kv_heads: int, head_dim: int):
+        self.fmt_k, self.fmt_v, self.pages = _fmt(fmt_k), _fmt(fmt_v), pages
+        self.page_size, self.n_kv_heads, self.head_dim = page_size, n_kv_heads, head_dim
+        self.page_bytes = qmm_kv_page_bytes(fmt_k, fmt_v, page_size, n_kv_heads, head_dim)
+        if self.page_bytes == 0:
+            raise QmmError(2, qmm_last_error())
+        if pages.dim() != 2 or pages.shape[1] != self.page_bytes or not pages.is_contiguous() \
+                or pages.element_size() != 1:
+            raise ValueError(f"pages must be contiguous bytes [n_pages, {self.page_bytes}], "
+                             f"got {tuple(pages.shape)}")
+
+    @classmethod
+    def empty(cls, fmt_k, fmt_v, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
+              device="cuda"):
+        """A cache over `n_pages` pages of new memory (not cleared)."""
+        import torch
+        size = qmm_kv_page_bytes(fmt_k, fmt_v, page_size, n_kv_heads, head_dim)
+        if size == 0:
+            raise QmmError(2, qmm_last_error())
+        pages = torch.empty((n_pages, size), dtype=torch.uint8, device=device)
+        return cls(fmt_k, fmt_v, pages, page_size, n_kv_heads, head_dim)
+
+    def view(self, page_table, lens) -> qmm_kv_cache:
+        """The C description of this pool with a call's int32 page_table
+        [n_seqs, max_pages] (rows may be strided) and lens [n_seqs]."""
+        if page_table.dim() != 2 or page_table.shape[0] != lens.shape[0] \
+                or page_table.element_size() != 4 or lens.element_size() != 4 or lens.dim() != 1 \
+                or page_table.is_floating_point() or lens.is_floating_point():
+            raise ValueError("page_table and lens must be int32 [n_seqs, max_pages] and [n_seqs]")
+        n_seqs, max_pages = page_table.shape
+        if (max_pages > 1 and page_table.stride(1) != 1) or (n_seqs > 1 and lens.stride(0) != 1):
+            raise ValueError("entries of page_table's rows and of lens must be adjacent")
+        return qmm_kv_cache(self.fmt_k, self.fmt_v, self.pages.data_ptr(), self.pages.numel(),
+                            self.pages.shape[0], self.page_size, self.n_kv_heads, self.head_dim,
+                            page_table.data_ptr(),
+                            page_table.stride(0) if n_seqs > 1 else max_pages, max_pages,
+                            lens.data_ptr(), n_seqs)
+
+    def rows(self, name, t, n_seqs: int):
+        """Row stride of fp32 rows [n_seqs, n_new, heads, head_dim] and their n_new and heads."""
+        if t.dim() != 4 or t.shape[0] != n_seqs or t.shape[3] != self.head_dim \
+                or t.element_size() != 4 or not t.is_floating_point():
+            raise ValueError(f"{name} must be float32 [{n_seqs}, n_new, heads, {self.head_dim}], "
+                             f"got {tuple(t.shape)}")
+        s0, s1, s2, s3 = t.stride()
+        n_new, heads = t.shape[1], t.shape[2]
+        row = s1 if n_new > 1 else s0 if n_seqs > 1 else heads * self.head_dim
+        if s3 != 1 or (heads > 1 and s2 != self.head_dim) or \
+                (n_new > 1 and n_seqs > 1 and s0 != n_new * s1):
+            raise ValueError(f"{name}: the heads of a row must be adjacent and rows equally spaced")
+        return row, n_new, heads
+
+
+def rope_table(n_pos: int, n_rot: int, base: float = 10000.0, scale: float = 1.0, device="cuda"):
+    """Rotary table [n_pos, n_rot / 2, 2] float32 for kv_append: cos and sin of
+    position * scale * base^(-2 a / n_rot), from float64."""
+    import torch
+    turns = base ** (-2.0 * torch.arange(n_rot // 2, dtype=torch.float64) / n_rot)
+    angle = torch.arange(n_pos, dtype=torch.float64).unsqueeze(1) * (scale * turns)
+    return torch.stack((angle.cos(), angle.sin()), -1).float().to(device)
+
+
+def kv_append(cache: KvCache, k, v, page_table, lens, *, q=None, q_out=None, rope=None,
+              rope_style="half", stream=None):
+    """Append the rows k, v [n_seqs, n_new, n_kv_heads, head_dim] at the last
+    n_new of each sequence's lens positions; with `rope` (see rope_table) k is
+    rotated, and q [n_seqs, n_new, n_heads, head_dim] into q_out (returned; a
+    new tensor when not given)."""
+    import torch
+    c = cache.view(page_table, lens)
+    ks, n_new, heads = cache.rows("k", k, c.n_seqs)
+    vs = cache.rows("v", v, c.n_seqs)
+    if heads != cache.n_kv_heads or vs[1:] != (n_new, heads):
+        raise ValueError(f"k and v must have {cache.n_kv_heads} heads and the same rows")
+    qs = qos = n_heads = 0
+    if q is not None:
+        qs, q_new, n_heads = cache.rows("q", q, c.n_seqs)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        qos, o_new, o_heads = cache.rows("q_out", q_out, c.n_seqs)
+        if q_new != n_new or o_new != n_new or o_heads != n_heads:
+            raise ValueError("q and q_out must have k's rows and the same heads")
+    rope_len = n_rot = 0
+    if rope is not None:
+        if rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous() \
+                or rope.dtype != torch.float32:
+            raise ValueError("rope must be contiguous float32 [positions, n_rot / 2, 2]")
+        rope_len, n_rot = rope.shape[0], 2 * rope.shape[1]
+    style = ROPE_STYLES[rope_style] if isinstance(rope_style, str) else int(rope_style)
+    qmm_kv_append(qmm_kv_append_args(
+        c, n_new, k.data_ptr(), v.data_ptr(), ks, vs[0], _ptr(q), _ptr(q_out) if n_heads else None,
+        qs, qos, n_heads, _ptr(rope), rope_len, n_rot, style, _stream(stream), 0))
+    return q_out
+
+
+def kv_read(cache: KvCache, page_table, lens, count: int, *, first=None, k=None, v=None,
+            stream=None):
+    """fp32 k and v [n_seqs, count, n_kv_heads, head_dim] of the positions
+    first .. first + count - 1 of every sequence (first None: its last `count`
+    positions); zeros where a sequence has no such position."""
+    import torch
+    c = cache.view(page_table, lens)
+    shape = (c.n_seqs, count, cache.n_kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=torch.float32, device=cache.pages.device) if k is None else k
+    v = torch.empty(shape, dtype=torch.float32, device=cache.pages.device) if v is None else v
+    for name, t in (("k", k), ("v", v)):
+        if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != torch.float32:
+            raise ValueError(f"{name} must be contiguous float32 {shape}")
+    qmm_kv_read(qmm_kv_read_args(c, -1 if first is None else first, count, k.data_ptr(),
+                                 v.data_ptr(), _stream(stream), 0))
+    return k, v
+
+
+def attend(cache: KvCache, q, page_table, lens, *, scale=None, window=0, out=None, workspace=None,
+           stream=None):
+    """Attention of the last n_new positions of every sequence over the cache:
+    q [n_seqs, n_new, n_heads, head_dim] (n_heads a multiple of the cache's kv
+    heads), scale 1 / sqrt(head_dim) unless given, window 0 (all positions) or
+    the number of last positions that a row sees. Returns out, shaped like q
+    (the given one when passed). Scratch is `workspace` (uint8) when given,
+    else a torch allocation."""
+    import torch
+    c = cache.view(page_table, lens)
+    qs, n_new, n_heads = cache.rows("q", q, c.n_seqs)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    os_, o_new, o_heads = cache.rows("out", out, c.n_seqs)
+    if (o_new, o_heads) != (n_new, n_heads):
+        raise ValueError("out must have q's shape")
+    a = qmm_attend_args(c, n_new, n_heads, q.data_ptr(), out.data_ptr(), qs, os_,
+                        cache.head_dim ** -0.5 if scale is None else scale, window, None, 0,
+                        _stream(stream), 0)
+    ws = None
+    if workspace is None:
+        need = qmm_attend_workspace_bytes(a)
+        if need:
+            ws = workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    qmm_attend(a)
+    _keep_until_done(ws, stream)
+    return out

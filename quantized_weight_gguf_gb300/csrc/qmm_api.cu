@@ -426,6 +426,8 @@ int experts_impl(const qmm_args *a, const int32_t *ids, int64_t n_experts, int64
 }  // namespace
 
 namespace qmm {
+int current_device(DeviceInfo **out) { return device_info(out); }
+int scratch_of_library(size_t need, void **out) { return library_workspace(need, out); }
 int set_error(int status, const char *fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -757,6 +759,10 @@ int qmm_device_status(void *stream) {
         cudaMemcpy(dev->err, &zero, sizeof zero, cudaMemcpyHostToDevice);
         if (v == qmm::DERR_BAD_ID)
             return fail(QMM_ERR_BAD_ID, "an expert id was outside [0, n_experts)");
+        if (v == qmm::DERR_BAD_PAGE)
+            return fail(QMM_ERR_BAD_PAGE,
+                        "a cache call met a page id outside the pool, a length beyond its page table "
+                        "or a position beyond its rotary table");
         return fail(QMM_ERR_DEVICE_TIMEOUT, "a kernel gave up waiting on a pipeline barrier (code %u)", v);
     }
     return QMM_OK;

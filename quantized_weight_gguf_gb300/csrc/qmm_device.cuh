@@ -29,7 +29,9 @@ enum DevErr : unsigned int {
     DERR_MMA_ACC = 6,      // epilogue gave up waiting for the accumulator
     DERR_TEARDOWN = 7,     // copies still in flight at exit after a fault
     DERR_BAD_ID = 8,       // an expert id outside [0, n_experts)
-    DERR_WAIT_PROBE = 9    // the bounded-wait check gave up, as it must
+    DERR_WAIT_PROBE = 9,   // the bounded-wait check gave up, as it must
+    DERR_BAD_PAGE = 10,    // a page id, length or position outside a cache call's tables
+    DERR_ATTEND = 11       // attention gave up waiting for a strip's bytes
 };
 
 // Block geometry (elements per block, bytes per block) of each format.

@@ -117,6 +117,11 @@ cudaError_t launch_zero_cols(float *y, int64_t n_tokens, int64_t n, int64_t j0, 
 // One block waiting on a barrier nothing satisfies; it gives up after
 // limit_ns and records an error in *err (see qmm_check_bounded_wait).
 cudaError_t launch_bounded_wait_probe(unsigned int *err, uint64_t limit_ns, cudaStream_t s);
+// The current device's properties (first use looks them up); QMM_OK, or the
+// status and message of what it cannot be.
+int current_device(DeviceInfo **out);
+// The library-owned grow-only scratch of the current device, at least `need` bytes.
+int scratch_of_library(size_t need, void **out);
 // Record a status and message for qmm_last_error() on this host thread; returns status.
 int set_error(int status, const char *fmt, ...);
 
