@@ -18,7 +18,8 @@ LIB = os.path.join(PKG, "libqmm.so")
 SOURCES = ["qmm_mma_inst_q4k.cu", "qmm_mma_inst_16.cu", "qmm_mma_inst_q.cu", "qmm_mma_inst_aff.cu",
            "qmm_mma_inst_grp.cu",
            "qmm_api.cu", "qmm_gemv.cu", "qmm_mma.cu", "qmm_dequant.cu", "qmm_noalloc.cu",
-           "qmm_back_input.cu", "qmm_attend.cu", "qmm_kv.cu", "qmm_kv_api.cu"]
+           "qmm_back_input.cu", "qmm_attend_inst_bf16.cu", "qmm_attend_inst_f16.cu",
+           "qmm_attend_inst_q8.cu", "qmm_attend_inst_q4.cu", "qmm_attend_inst_q8q4.cu", "qmm_attend.cu", "qmm_kv.cu", "qmm_kv_api.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 

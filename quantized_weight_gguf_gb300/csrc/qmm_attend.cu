@@ -1,108 +1,130 @@
-// qmm_attend.cu -- attention of new rows over the paged key-value cache.
-//
-// o = sum_t softmax_t(scale q . k_t) v_t. One CTA per (row, head): each warp
-// takes every fourth position, its lanes four dims each, and keeps a running
-// maximum m, total l = sum e^(s - m) and sum of e^(s - m) v in fp32; the four
-// warps' results are joined in a fixed order at the end.
-#include "qmm_kv.cuh"
-#include "qmm_kv_launch.h"
+// qmm_attend.cu -- host side of the attention over the paged key-value cache
+// (the kernel is in qmm_attend_kernel.cuh), and the join of items whose
+// positions were split over several CTAs.
+#include "qmm_attend.h"
 
 namespace qmm {
 
-namespace {
+namespace attend {
 
-constexpr int kWarps = 4;
-
-__global__ void __launch_bounds__(kWarps * 32) attend_kernel(const Attend a) {
+// Joins split items: out = sum_k 2^(m_k - M) s_k / sum_k 2^(m_k - M) l_k over
+// an item's parts k. Block c serves the boundary between the shares of CTAs
+// c and c + 1, if an item straddles it; the blocks of one item's boundaries
+// divide its 8 x dim values evenly, so an item of many parts has as many
+// blocks. Threads take the parts in a fixed order: the sum is the same on
+// every call.
+__global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendParams a) {
     pdl_wait_prev();
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][256];
-    const KvView &c = a.c;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = blockIdx.x / a.n_heads;
-    const int head = (int)(blockIdx.x - row * a.n_heads);
-    const int h = head / (a.n_heads / c.n_kv);
-    const int s = (int)(row / a.n_new);
-    const int len = kv_length(c, s);
-    const int64_t pos = (int64_t)max(__ldg(c.lens + s), 0) - a.n_new + (row - s * a.n_new);
-    const int64_t lo = a.window && pos + 1 > a.window ? pos + 1 - a.window : 0;
-    const int64_t hi = pos + 1 < len ? pos + 1 : len;
-    float q[8], o[8];
-    const float *qr = a.q + row * a.q_stride + (int64_t)head * c.dim;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int d = (i >> 2) * 128 + lane * 4 + (i & 3);
-        q[i] = d < c.dim ? qr[d] * a.scale : 0.0f;
-        o[i] = 0.0f;
-    }
-    float m = -INFINITY, l = 0.0f;
-    for (int64_t t = lo + warp; t < hi; t += kWarps) {
-        const uint8_t *strip = kv_strip(c, s, h, (int)(t / kStrip));
-        if (!strip) continue;
-        const int tt = (int)(t % kStrip);
-        float v[8], x = 0.0f;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const int d = g * 128 + lane * 4;
-            float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
-            if (d < c.dim) {
-                kk = kv_load4(strip, c.fmt_k, c.dim, tt, d);
-                vv = kv_load4(strip + c.v_off, c.fmt_v, c.dim, tt, d);
+    pdl_launch_dependents();
+    const Join x = a.joins[blockIdx.x];
+    if (x.parts < 2) return;
+    const int dim = a.c.dim, quads = kRows * dim / 4, blocks = x.parts - 1;
+    const int me = (int)blockIdx.x - x.first;
+    const int f0 = (int)((int64_t)me * quads / blocks), f1 = (int)((int64_t)(me + 1) * quads / blocks);
+    if (f0 >= f1) return;
+    // `wide` neighbouring lanes share a value and take its parts in turn
+    int wide = 1;
+    while (wide < 32 && 2 * wide * (f1 - f0) <= kThreads) wide *= 2;
+    const int l = threadIdx.x % wide;
+    for (int f = f0 + threadIdx.x / wide; f - (int)threadIdx.x / wide < f1; f += kThreads / wide) {
+        const int row = f / (dim / 4), d = (f - row * (dim / 4)) * 4;
+        float m = -INFINITY, total = 0.0f;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (f < f1) {
+#pragma unroll 4
+            for (int k = l; k < x.parts; k += wide) {
+                // the first part is its CTA's last item, the others their CTAs' first
+                const float *p = a.parts + (int64_t)(2 * (x.first + k) + (k == 0)) * part_floats(dim);
+                const float mk = p[row], lk = p[kRows + row];
+                const float4 v = *reinterpret_cast<const float4 *>(p + 2 * kRows + row * dim + d);
+                if (mk == -INFINITY) continue;
+                const float top = fmaxf(m, mk);
+                const float fo = exp2f(m - top), fn = exp2f(mk - top);
+                total = total * fo + lk * fn;
+                s.x = s.x * fo + v.x * fn;
+                s.y = s.y * fo + v.y * fn;
+                s.z = s.z * fo + v.z * fn;
+                s.w = s.w * fo + v.w * fn;
+                m = top;
             }
-            x += q[4 * g] * kk.x + q[4 * g + 1] * kk.y + q[4 * g + 2] * kk.z + q[4 * g + 3] * kk.w;
-            v[4 * g] = vv.x; v[4 * g + 1] = vv.y; v[4 * g + 2] = vv.z; v[4 * g + 3] = vv.w;
         }
-#pragma unroll
-        for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(~0u, x, i);
-        const float mn = fmaxf(m, x);
-        const float f = expf(m - mn), p = expf(x - mn);
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = o[i] * f + p * v[i];
-        m = mn;
-    }
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) so[warp][(i >> 2) * 128 + lane * 4 + (i & 3)] = o[i];
-    __syncthreads();
-    float mm = -INFINITY, ll = 0.0f;
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm[w]);
-    float f[kWarps];
-    for (int w = 0; w < kWarps; ++w) {
-        f[w] = sm[w] == -INFINITY ? 0.0f : expf(sm[w] - mm);
-        ll += f[w] * sl[w];
-    }
-    float *out = a.out + row * a.out_stride + (int64_t)head * c.dim;
-    for (int d = threadIdx.x; d < c.dim; d += kWarps * 32) {
-        float r = 0.0f;
-        for (int w = 0; w < kWarps; ++w) r += f[w] * so[w][d];
-        out[d] = ll > 0.0f ? r / ll : mm != mm || ll != ll ? NAN : 0.0f;
+        for (int o = 1; o < wide; o <<= 1) {
+            const float mo = __shfl_xor_sync(~0u, m, o), to = __shfl_xor_sync(~0u, total, o);
+            const float4 so = make_float4(__shfl_xor_sync(~0u, s.x, o), __shfl_xor_sync(~0u, s.y, o),
+                                          __shfl_xor_sync(~0u, s.z, o), __shfl_xor_sync(~0u, s.w, o));
+            const float top = fmaxf(m, mo);
+            const float fa = m == -INFINITY ? 0.0f : exp2f(m - top);
+            const float fb = mo == -INFINITY ? 0.0f : exp2f(mo - top);
+            total = total * fa + to * fb;
+            s.x = s.x * fa + so.x * fb;
+            s.y = s.y * fa + so.y * fb;
+            s.z = s.z * fa + so.z * fb;
+            s.w = s.w * fa + so.w * fb;
+            m = top;
+        }
+        if (f < f1 && l == 0 && row < x.heads) put_out(a, x.row, x.head0 + row, d, dim, s, total);
     }
 }
 
+namespace {
+
+// CTAs of a launch: one resident wave, or fewer when even the longest rows
+// that the tables can hold make less work than that.
+int grid_of(const Attend &a, const DeviceInfo &dev) {
+    const int wave = dev.sm_count * shape_of(a.c.fmt_k, a.c.fmt_v, a.c.dim).ctas;
+    int64_t most = a.c.capacity;
+    if (a.window && a.window < most) most = a.window + kStrip - 1;
+    const int64_t strips = (most + kStrip - 1) / kStrip + 1;
+    const int64_t subs = (a.n_heads / a.c.n_kv + kRows - 1) / kRows;
+    const int64_t items = (int64_t)a.c.n_seqs * a.n_new * a.c.n_kv * subs;
+    if (items >= wave) return wave;  // also keeps the product in range
+    const int64_t shares = (items * (strips + kItemCost) + kMinShare - 1) / kMinShare;
+    return shares < wave ? (int)shares : wave;
+}
+
+size_t parts_bytes(int dim, int grid) {
+    return ((size_t)2 * grid * part_floats(dim) * 4 + 255) & ~(size_t)255;
+}
+
 }  // namespace
+
+}  // namespace attend
 
 bool attend_supports(int dim) {
     return dim == 64 || dim == 96 || dim == 128 || dim == 192 || dim == 256;
 }
 
-size_t attend_workspace_bytes(const Attend &, const DeviceInfo &) { return 0; }
+size_t attend_workspace_bytes(const Attend &a, const DeviceInfo &dev) {
+    const int grid = attend::grid_of(a, dev);
+    return attend::parts_bytes(a.c.dim, grid) + sizeof(attend::Join) * grid;
+}
 
-cudaError_t launch_attend(const Attend &a, const DeviceInfo &, cudaStream_t s) {
-    const int64_t grid = (int64_t)a.c.n_seqs * a.n_new * a.n_heads;
-    if (grid == 0) return cudaSuccess;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_kernel, a);
+cudaError_t launch_attend(const Attend &a, const DeviceInfo &dev, cudaStream_t s) {
+    const int grid = attend::grid_of(a, dev);
+    attend::AttendParams p;
+    p.c = a.c;
+    p.q = a.q;
+    p.out = a.out;
+    p.parts = static_cast<float *>(a.workspace);
+    p.joins = reinterpret_cast<attend::Join *>(static_cast<uint8_t *>(a.workspace) +
+                                               attend::parts_bytes(a.c.dim, grid));
+    p.q_stride = a.q_stride;
+    p.out_stride = a.out_stride;
+    p.window = a.window;
+    p.rows = a.c.n_seqs * a.n_new;
+    p.n_new = (int)a.n_new;
+    p.group = a.n_heads / a.c.n_kv;
+    p.subs = (p.group + attend::kRows - 1) / attend::kRows;
+    p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+    p.vec = a.vec;
+    cudaError_t e;
+    if (a.c.fmt_k == F_F16) e = attend::launch_f16(p, grid, s);
+    else if (a.c.fmt_k == F_BF16) e = attend::launch_bf16(p, grid, s);
+    else if (a.c.fmt_k == F_Q4_0) e = attend::launch_q4(p, grid, s);
+    else if (a.c.fmt_v == F_Q4_0) e = attend::launch_q8q4(p, grid, s);
+    else e = attend::launch_q8(p, grid, s);
+    if (e != cudaSuccess || grid < 2) return e;
+    return attend::launch_programmatic(attend::attend_join_kernel, p, grid - 1, attend::kThreads, 0, s);
 }
 
 }  // namespace qmm

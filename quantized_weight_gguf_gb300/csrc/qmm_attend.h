@@ -1,0 +1,270 @@
+// qmm_attend.h -- parameters, work division and partial results of the
+// attention kernels (qmm_attend_kernel.cuh: a strip at a time; qmm_attend.cu:
+// the join of split items and the host side).
+#pragma once
+
+#include "qmm_kv.cuh"
+#include "qmm_kv_launch.h"
+
+namespace qmm {
+
+namespace attend {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 8;            // query heads of an item
+constexpr int kFixedBytes = 1024;   // barriers, flags, states (see attend_kernel)
+
+// How the shared memory of an SM (228 KB, of which the system takes 1 KB per
+// CTA) is divided for a pair of formats and a head_dim: resident CTAs, and
+// each warp's ring. A strip is one copy, or two (K, then V) where whole strips
+// would leave a ring of this size fewer than three slots.
+struct Shape {
+    int q_bytes;     // query fragments: 16 bytes per lane and 16 dims, 24 for bf16's third term
+    int units;       // copies per strip
+    int slot_bytes, slots;
+    int ring_bytes;  // of one warp; also holds its [kRows][dim + 4] results at an item's end
+    int smem, ctas;
+};
+constexpr int kMaxSlots = 8;
+__host__ __device__ constexpr Shape shape_for(int fk, int fv, int dim, int ctas) {
+    Shape s = {};
+    s.ctas = ctas;
+    s.q_bytes = dim / 16 * 32 * (fk == F_BF16 ? 24 : 16);
+    const int budget = (228 * 1024 / ctas - 1024 - s.q_bytes - kFixedBytes) / kWarps / 16 * 16;
+    const int k = kv_half_bytes(fk, dim), v = kv_half_bytes(fv, dim);
+    s.units = budget / (k + v) >= 3 ? 1 : 2;
+    s.slot_bytes = s.units == 1 ? k + v : k > v ? k : v;
+    s.slots = budget / s.slot_bytes < kMaxSlots ? budget / s.slot_bytes : kMaxSlots;
+    const int merge = (kRows * (dim + 4) * 4 + 127) / 128 * 128;
+    s.ring_bytes = s.slots * s.slot_bytes > merge ? s.slots * s.slot_bytes : merge;
+    s.smem = kFixedBytes + s.q_bytes + kWarps * s.ring_bytes;
+    return s;
+}
+// Four CTAs of 128 threads per SM up to 128 dims (128 registers a thread),
+// three above (168); fewer where their rings would have less than two slots.
+__host__ __device__ constexpr Shape shape_of(int fk, int fv, int dim) {
+    int ctas = dim <= 128 ? 4 : 3;
+    while (ctas > 1 && shape_for(fk, fv, dim, ctas).slots < 2) --ctas;
+    return shape_for(fk, fv, dim, ctas);
+}
+
+// What an item costs beside its strips, in strips: its query rows are
+// loaded and converted, and the warps' results joined.
+constexpr int kItemCost = 4;
+// Strips (and item costs) below which a CTA's share is not cut further: two
+// strips per warp.
+constexpr int kMinShare = 8;
+
+// A split item, written by each CTA whose share ends inside one: the CTAs
+// first .. first + parts - 1 hold its partial results.
+struct Join {
+    int parts;   // 0: none
+    int first;
+    int head0, heads;
+    int64_t row;
+};
+
+struct AttendParams {
+    KvView c;
+    const float *q;
+    float *out;
+    float *parts;      // [2 grid][part_floats]: results of a share's first (0) and last (1) item
+    Join *joins;       // [grid]
+    int64_t q_stride, out_stride, window, rows;  // rows = n_seqs * n_new
+    int n_new, group, subs;  // query heads per kv head, and items that they make
+    float scale_log2;  // scale * log2(e)
+    bool vec;
+};
+
+// a partial result: [kRows] maxima, [kRows] totals, [kRows][dim] sums
+__host__ __device__ constexpr int part_floats(int dim) { return kRows * (dim + 2); }
+
+// The positions [lo, hi) that row r = s * n_new + i sees, its sequence and strips.
+struct RowRange {
+    int seq, lo, hi, first, strips;
+};
+__device__ __forceinline__ RowRange row_range(const AttendParams &a, int64_t r) {
+    RowRange x;
+    x.seq = (int)(r / a.n_new);
+    const int held = __ldg(a.c.lens + x.seq);
+    const int64_t pos = (int64_t)(held < 0 ? 0 : held) - a.n_new + (r - (int64_t)x.seq * a.n_new);
+    int64_t hi = pos + 1;
+    if (hi > a.c.capacity) {
+        record_error(a.c.err, DERR_BAD_PAGE);
+        hi = a.c.capacity;
+    }
+    int64_t lo = a.window ? pos + 1 - a.window : 0;
+    if (lo < 0) lo = 0;
+    if (hi <= lo) lo = hi = 0;  // sees nothing
+    x.lo = (int)lo;
+    x.hi = (int)hi;
+    x.first = x.lo / kStrip;
+    x.strips = hi > lo ? (x.hi + kStrip - 1) / kStrip - x.first : 0;
+    return x;
+}
+// An item of no strips counts as one that holds nothing, so that its output
+// is written like any other.
+__device__ __forceinline__ int item_strips(const RowRange &x) { return x.strips > 0 ? x.strips : 1; }
+
+// Where a CTA's share begins.
+struct WorkSearch {
+    long long sum[kWarps];
+    long long row, base;
+};
+struct Work {
+    int64_t at, end;     // the share, in strips and item costs of all items end to end
+    int64_t total;
+    int shares;          // CTAs that have one
+    int64_t row, base;   // the row that `at` is in, and where it begins
+};
+
+// The share of CTA `cta`; false when it has none. Every thread of the block
+// calls it. The rows' weights are summed by the block's threads, a run of
+// rows each: a few loads for a decoding batch.
+__device__ __forceinline__ bool find_work(const AttendParams &a, int cta, WorkSearch *sh, Work &w) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t per = (a.rows + kThreads - 1) / kThreads;
+    const int64_t r0 = tid * per < a.rows ? tid * per : a.rows;
+    const int64_t r1 = r0 + per < a.rows ? r0 + per : a.rows;
+    const int64_t items = (int64_t)a.c.n_kv * a.subs;
+    int64_t mine = 0;
+    for (int64_t r = r0; r < r1; ++r) mine += item_strips(row_range(a, r)) + kItemCost;
+    mine *= items;
+    int64_t upto = mine;  // inclusive sums over the warp, then over the warps
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sh->sum[warp] = upto;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int k = 0; k < kWarps; ++k) {
+        if (k < warp) before += sh->sum[k];
+        total += sh->sum[k];
+    }
+    w.total = total;
+    const int64_t most = (total + kMinShare - 1) / kMinShare;
+    w.shares = most < (int64_t)gridDim.x ? (int)most : (int)gridDim.x;
+    if (cta >= w.shares) return false;
+    w.at = (int64_t)cta * total / w.shares;
+    w.end = (int64_t)(cta + 1) * total / w.shares;
+    int64_t base = before + upto - mine;
+    if (w.at >= base && w.at < base + mine) {
+        for (int64_t r = r0; r < r1; ++r) {
+            const int64_t n = (item_strips(row_range(a, r)) + kItemCost) * items;
+            if (w.at < base + n) {
+                sh->row = r;
+                sh->base = base;
+                break;
+            }
+            base += n;
+        }
+    }
+    __syncthreads();
+    w.row = sh->row;
+    w.base = sh->base;
+    return true;
+}
+
+// The CTA whose share holds position v of the strips laid end to end.
+__device__ __forceinline__ int share_of(const Work &w, int64_t v) {
+    return (int)(((v + 1) * w.shares + w.total - 1) / w.total) - 1;
+}
+
+// The next item of a share: which rows and heads, which positions, and the
+// part [begin, end) of its strips that the share holds.
+struct Item {
+    int64_t row;
+    int64_t base;        // where its strips begin
+    int seq, head;       // sequence, kv head
+    int head0, heads;    // query heads
+    int lo, hi, first;   // positions seen, first strip
+    int strips, begin, end;
+    bool live;           // has strips at all
+};
+__device__ __forceinline__ bool next_item(const AttendParams &a, Work &w, Item &it) {
+    while (w.at < w.end) {
+        const RowRange x = row_range(a, w.row);
+        const int n = item_strips(x), cost = n + kItemCost;
+        const int64_t all = (int64_t)cost * a.c.n_kv * a.subs;
+        if (w.at >= w.base + all) {
+            w.base += all;
+            ++w.row;
+            continue;
+        }
+        const int k = (int)((w.at - w.base) / cost);
+        it.base = w.base + (int64_t)k * cost;
+        const int64_t stop = it.base + cost < w.end ? it.base + cost : w.end;
+        it.begin = (int)(w.at - it.base);
+        it.end = stop - it.base < n ? (int)(stop - it.base) : n;
+        w.at = stop;
+        if (it.begin >= it.end) continue;  // only of the item's cost
+        it.row = w.row;
+        it.seq = x.seq;
+        it.head = k / a.subs;
+        const int sub = k - it.head * a.subs;
+        it.head0 = it.head * a.group + sub * kRows;
+        it.heads = a.group - sub * kRows < kRows ? a.group - sub * kRows : kRows;
+        it.lo = x.lo;
+        it.hi = x.hi;
+        it.first = x.first;
+        it.strips = n;
+        it.live = x.strips > 0;
+        return true;
+    }
+    return false;
+}
+
+__device__ __forceinline__ Join make_join(const AttendParams &, const Work &w, const Item &it) {
+    Join x;
+    x.first = share_of(w, it.base);
+    x.parts = share_of(w, it.base + it.strips - 1) - x.first + 1;
+    x.head0 = it.head0;
+    x.heads = it.heads;
+    x.row = it.row;
+    return x;
+}
+
+// out = sum / total: 0 where nothing was seen.
+__device__ __forceinline__ void put_out(const AttendParams &a, int64_t row, int head, int d, int dim,
+                                        float4 sum, float total) {
+    float *o = a.out + row * a.out_stride + (int64_t)head * dim + d;
+    const float f = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+    const float4 v = make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f);
+    if (a.vec) {
+        *reinterpret_cast<float4 *>(o) = v;
+    } else {
+        o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+    }
+}
+
+// Launches `kernel` as a programmatic dependent of the kernel before it in
+// the stream (which it waits for before it reads or writes anything).
+template <class P>
+cudaError_t launch_programmatic(void (*kernel)(P), const P &p, int grid, int threads, size_t smem,
+                                cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// one translation unit per pair of formats
+cudaError_t launch_f16(const AttendParams &a, int grid, cudaStream_t s);
+cudaError_t launch_bf16(const AttendParams &a, int grid, cudaStream_t s);
+cudaError_t launch_q8(const AttendParams &a, int grid, cudaStream_t s);
+cudaError_t launch_q4(const AttendParams &a, int grid, cudaStream_t s);
+cudaError_t launch_q8q4(const AttendParams &a, int grid, cudaStream_t s);
+
+}  // namespace attend
+
+}  // namespace qmm
