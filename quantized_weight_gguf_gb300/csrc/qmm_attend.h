@@ -18,11 +18,12 @@ constexpr int kFixedBytes = 1024;   // barriers, flags, states (see attend_kerne
 // How the shared memory of an SM (228 KB, of which the system takes 1 KB per
 // CTA) is divided for a pair of formats and a head_dim: resident CTAs, and
 // each warp's ring. A strip is one copy, or two (K, then V) where whole strips
-// would leave a ring of this size fewer than three slots.
+// would leave a ring of this size fewer than four slots (two pairs).
 struct Shape {
     int q_bytes;     // query fragments: 16 bytes per lane and 16 dims, 24 for bf16's third term
     int units;       // copies per strip
     int slot_bytes, slots;
+    int step;        // strips taken at a time: two where the ring holds four slots, so that copies stay ahead
     int ring_bytes;  // of one warp; also holds its [kRows][dim + 4] results at an item's end
     int smem, ctas;
 };
@@ -33,9 +34,10 @@ __host__ __device__ constexpr Shape shape_for(int fk, int fv, int dim, int ctas)
     s.q_bytes = dim / 16 * 32 * (fk == F_BF16 ? 24 : 16);
     const int budget = (228 * 1024 / ctas - 1024 - s.q_bytes - kFixedBytes) / kWarps / 16 * 16;
     const int k = kv_half_bytes(fk, dim), v = kv_half_bytes(fv, dim);
-    s.units = budget / (k + v) >= 3 ? 1 : 2;
+    s.units = budget / (k + v) >= 4 ? 1 : 2;
     s.slot_bytes = s.units == 1 ? k + v : k > v ? k : v;
     s.slots = budget / s.slot_bytes < kMaxSlots ? budget / s.slot_bytes : kMaxSlots;
+    s.step = s.slots >= 4 ? 2 : 1;
     const int merge = (kRows * (dim + 4) * 4 + 127) / 128 * 128;
     s.ring_bytes = s.slots * s.slot_bytes > merge ? s.slots * s.slot_bytes : merge;
     s.smem = kFixedBytes + s.q_bytes + kWarps * s.ring_bytes;

@@ -10,29 +10,42 @@
 // item whose strips fall to several CTAs is joined by attend_join_kernel from
 // partial results (maximum, total, weighted sum).
 //
-// A CTA is kWarps warps that take an item's strips in turn. Each warp streams
-// its strips through a ring of its own in shared memory with bulk copies (one
-// or two per strip, issued by one lane, no barrier between warps) and keeps a running
-// maximum m, total l and weighted sums in registers, fp32.
+// A CTA is kWarps warps that take an item's strips in turn, two at a time
+// where the ring has room.
+// Each warp streams its strips through a ring of its own in shared memory with
+// bulk copies (one or two per strip, issued by one lane, no barrier between
+// warps) and keeps totals and weighted sums in registers, fp32.
 //
 // Scores and sums are tensor-core products (mma.m16n8k16) on fragments that
 // are unpacked from the strip in registers:
 //  - S = Q K^T: eight query rows are the 16 rows of A as two fp16 terms each
 //    (rows g and g + 8 of a fragment are the high part and the remainder, 22
-//    significant bits, after a power-of-two scale per row), the strip's 16
-//    positions are two n-tiles. Integer codes enter as exact fp16 integers; a
-//    block's scale multiplies its fp32 partial sum.
+//    significant bits, after a power-of-two scale per row), a strip's 16
+//    positions are two n-tiles. A block's scale multiplies its fp32 sum.
 //  - O^T = V^T P^T: 16 dims are the rows of A, the eight query rows the columns
 //    of B. The weights p enter as two fp16 terms as well (two products into
 //    one accumulator). For quantised V a block's scale d is folded into the
-//    weight first: w = p d. A common power of two keeps the largest w near
-//    2^14, where both terms are normal numbers: p's exponent carries it, as
-//    part of the maximum that is subtracted, and it follows the largest |d|
-//    seen, like the maximum itself.
+//    weight first: w = p d. A strip's product starts from zero and is added
+//    to the running sums in fp32, so their rounding is to nearest.
+//  - Integer codes enter as exact fp16 integers: the code with its offset
+//    under the exponent of 1024 (a byte permute or a mask), less 1024 and the
+//    offset. (Leaving the offset in, to be subtracted from the sums, or taking
+//    the code as a subnormal, saves that subtraction, but the tensor cores cut
+//    each product at the largest one's last bits: sums of 8 Q4_0 positions
+//    then missed the tests' bound.)
 //  - BF16 K and V are bf16 operands; q and p then have three bf16 terms.
 // The scores of a strip come out of the first product in the lanes that need
 // them for the second, so p stays in registers.
+//
+// The softmax subtracts a reference R per row that is not the exact running
+// maximum: a weight 2^(s - R) may grow to 2^lim, where the largest w = p d is
+// just below 2^15. Only when a score (or a scale d) passes that limit is R moved, to
+// 4 below the limit for the largest score seen, and the sums rescaled; so a
+// strip normally takes no shuffles, and the weights that matter stay far from
+// the fp16 terms' subnormal range.
 #pragma once
+
+#include <cfloat>
 
 #include "qmm_attend.h"
 
@@ -42,24 +55,45 @@ namespace attend {
 
 // ---------------------------------------------------------- small pieces ----
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+// d = a b + c on one m16n8k16 fragment, operands in fp16 or bf16
+template <bool BF>
+__device__ __forceinline__ float4 mma(const uint4 &a, uint32_t b0, uint32_t b1, const float4 &c) {
+    float4 d;
+    if constexpr (BF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%10, %11, %12, %13};"
+            : "=f"(d.x), "=f"(d.y), "=f"(d.z), "=f"(d.w)
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y), "f"(c.z),
+              "f"(c.w));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%10, %11, %12, %13};"
+            : "=f"(d.x), "=f"(d.y), "=f"(d.z), "=f"(d.w)
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y), "f"(c.z),
+              "f"(c.w));
+    return d;
 }
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+
+// pairs of fp32 in one 64-bit register
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
-template <int F>
-__device__ __forceinline__ void mma16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
-    if constexpr (F == F_BF16) mma_bf16(c, a, b0, b1);
-    else mma_f16(c, a, b0, b1);
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -75,8 +109,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_f16(uint32_t v) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
-__device__ __forceinline__ float2 unpack_bf16(uint32_t v) {
-    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+// (x, y) less the fp16 pair t
+__device__ __forceinline__ float2 less_f16(float x, float y, uint32_t t) {
+    float2 r;
+    asm("{\n .reg .b16 l, h, m;\n mov.b32 {l, h}, %2;\n mov.b16 m, 0xbc00;\n"
+        " fma.rn.f32.f16 %0, l, m, %3;\n fma.rn.f32.f16 %1, h, m, %4;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(t), "f"(x), "f"(y));
+    return r;
 }
 // A pair of fp32 values as 16-bit terms whose sum they are: two of fp16 (22
 // bits), three of bf16 (24 bits).
@@ -84,15 +124,13 @@ template <bool BF>
 __device__ __forceinline__ void split(float x, float y, uint32_t (&t)[3]) {
     if constexpr (BF) {
         t[0] = pack_bf16(x, y);
-        const float2 a = unpack_bf16(t[0]);
-        const float rx = x - a.x, ry = y - a.y;
+        const float rx = x - __uint_as_float(t[0] << 16), ry = y - __uint_as_float(t[0] & 0xffff0000u);
         t[1] = pack_bf16(rx, ry);
-        const float2 b = unpack_bf16(t[1]);
-        t[2] = pack_bf16(rx - b.x, ry - b.y);
+        t[2] = pack_bf16(rx - __uint_as_float(t[1] << 16), ry - __uint_as_float(t[1] & 0xffff0000u));
     } else {
         t[0] = pack_f16(x, y);
-        const float2 a = unpack_f16(t[0]);
-        t[1] = pack_f16(x - a.x, y - a.y);
+        const float2 r = less_f16(x, y, t[0]);
+        t[1] = pack_f16(r.x, r.y);
         t[2] = 0;
     }
 }
@@ -103,11 +141,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -118,14 +151,8 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
-__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// Bytes (two's complement, bit 7 already flipped) I0 and I1 of w as an exact
-// fp16 pair: the byte under the exponent of 1024, less 1024 + 128.
+// Two bytes of w (two's complement, bit 7 already flipped) as an exact fp16
+// pair: 1024 + 128 + code, less 1152.
 template <int SEL>
 __device__ __forceinline__ uint32_t bytes_f16(uint32_t w) {
     return hsub2(prmt(w, 0x64646464u, SEL), 0x64806480u);
@@ -138,18 +165,27 @@ __device__ __forceinline__ uint32_t nibbles_f16(uint32_t w) {
     else return hfma2((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);
 }
 
-// ------------------------------------------------------------- fragments ----
-// Lane 4 g + j of a warp. Position n of n-tile x is position
-// 8 x + (n ^ (n >> 2)) of the strip: with this order both the eight positions
-// g of a K fragment and the positions 2 j + e of a V fragment (e fixed) fall
-// on distinct banks of a plane.
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+// four 8 x 8 tiles of 16-bit values, transposed; each lane gives a row's address
+__device__ __forceinline__ uint4 ldsm_trans(uint32_t a) {
+    uint4 v;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a));
+    return v;
+}
 
-// B fragments of K: per 16 dims ("step") two registers for one n-tile.
-// dims of lane j, step k: 16-bit: 16 k + 4 j + {0, 1 | 2, 3}; Q8_0: plane k/2,
-// 8 j + 4 (k % 2) + {0, 1 | 2, 3}; Q4_0: plane k/2, 8 j + 2 (k % 2) +
-// {0, 4 | 1, 5}.
-// For a plane p of K at `base`, `row` = the lane's position times the row
-// bytes plus its byte offset: fills the steps of that plane.
+// ------------------------------------------------------------- fragments ----
+// Lane 4 g + j of a warp.
+
+// B fragments of K from plane p of a strip: one or two steps of 16 dims, two
+// registers each. `row`: the lane's position (g, or 8 + g) times the row bytes
+// plus its bytes in the row. The dims of lane j: 16-bit: 4 j + {0, 1 | 2, 3};
+// Q8_0, step k: 8 j + 4 k + {0, 1 | 2, 3}; Q4_0, step k: 8 j + 2 k + {0, 4 | 1, 5}.
 template <int F>
 __device__ __forceinline__ void k_frag(uint32_t base, int p, uint32_t row, uint32_t (&b)[4]) {
     if constexpr (!kv_quantised(F)) {
@@ -174,23 +210,20 @@ __device__ __forceinline__ void k_frag(uint32_t base, int p, uint32_t row, uint3
 }
 
 // A fragments of V^T from plane p: rows are dims, columns positions. 16-bit:
-// one tile, rows g and g + 8 are dims 16 p + 2 g and + 1. Quantised: two
-// tiles, rows g and g + 8 of tile u are dims 32 p + 4 g + 2 u and + 1.
-// row[x][e]: byte offset of the lane's position e of n-tile x and its dims.
+// one tile, rows g and g + 8 are dims 16 p + g and 16 p + 8 + g (`row` is the
+// lane's ldmatrix row). Quantised: two tiles, rows g and g + 8 of tile u are
+// dims 32 p + 4 g + 2 u and + 1; `row` is the byte offset of position 2 j and
+// dims 4 g.
 template <int F>
-__device__ __forceinline__ void v_frag(uint32_t base, int p, const uint32_t (&row)[2][2],
-                                       uint4 (&a)[2]) {
+__device__ __forceinline__ void v_frag(uint32_t base, int p, uint32_t row, uint4 (&a)[2]) {
     if constexpr (!kv_quantised(F)) {
-        const uint32_t w00 = lds32(base + p * 512 + row[0][0]), w01 = lds32(base + p * 512 + row[0][1]);
-        const uint32_t w10 = lds32(base + p * 512 + row[1][0]), w11 = lds32(base + p * 512 + row[1][1]);
-        a[0] = make_uint4(prmt(w00, w01, 0x5410), prmt(w00, w01, 0x7632), prmt(w10, w11, 0x5410),
-                          prmt(w10, w11, 0x7632));
+        a[0] = ldsm_trans(base + p * 512 + row);
     } else if constexpr (F == F_Q8_0) {
         uint32_t lo[2], hi[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const uint32_t w0 = lds32(base + p * 512 + row[x][0]) ^ 0x80808080u;
-            const uint32_t w1 = lds32(base + p * 512 + row[x][1]) ^ 0x80808080u;
+            const uint32_t w0 = lds32(base + p * 512 + row + x * 256) ^ 0x80808080u;
+            const uint32_t w1 = lds32(base + p * 512 + row + x * 256 + 32) ^ 0x80808080u;
             lo[x] = prmt(w0, w1, 0x5140);
             hi[x] = prmt(w0, w1, 0x7362);
         }
@@ -202,16 +235,14 @@ __device__ __forceinline__ void v_frag(uint32_t base, int p, const uint32_t (&ro
         uint32_t w[2], v[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            w[x] = prmt(lds16(base + p * 256 + row[x][0]), lds16(base + p * 256 + row[x][1]), 0x5410);
+            w[x] = prmt(lds16(base + p * 256 + row + x * 128), lds16(base + p * 256 + row + x * 128 + 16),
+                        0x5410);
             v[x] = w[x] >> 8;
         }
-        a[0] = make_uint4(nibbles_f16<0>(w[0]), nibbles_f16<4>(w[0]), nibbles_f16<0>(w[1]),
-                          nibbles_f16<4>(w[1]));
-        a[1] = make_uint4(nibbles_f16<0>(v[0]), nibbles_f16<4>(v[0]), nibbles_f16<0>(v[1]),
-                          nibbles_f16<4>(v[1]));
+        a[0] = make_uint4(nibbles_f16<0>(w[0]), nibbles_f16<4>(w[0]), nibbles_f16<0>(w[1]), nibbles_f16<4>(w[1]));
+        a[1] = make_uint4(nibbles_f16<0>(v[0]), nibbles_f16<4>(v[0]), nibbles_f16<0>(v[1]), nibbles_f16<4>(v[1]));
     }
 }
-
 // ----------------------------------------------------------------- config ----
 
 template <int FK, int FV, int D>
@@ -220,6 +251,7 @@ struct Cfg {
     static constexpr int kUnits = kShape.units, kSlots = kShape.slots, kSlotBytes = kShape.slot_bytes;
     static constexpr int kBytesK = kv_half_bytes(FK, D), kBytesV = kv_half_bytes(FV, D);
     static constexpr int kSteps = D / 16;
+    static constexpr int kStep = kShape.step;
     static constexpr int kQBytes = kShape.q_bytes;
     static constexpr int kRingBytes = kShape.ring_bytes;
     static constexpr int kMergeRow = D + 4;  // floats; + 4 spreads the rows j over the banks
@@ -240,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
     constexpr int kPlanesK = D / kv_plane_dims(FK), kPlanesV = D / kv_plane_dims(FV);
     constexpr int kStepsPerPlane = kv_plane_dims(FK) / 16;  // 2 for quantised K
     constexpr int kTilesPerPlane = kv_plane_dims(FV) / 16;  // 2 for quantised V
+    constexpr int S = C::kStep;                             // strips taken at a time
     extern __shared__ __align__(128) uint8_t smem[];
     // fixed part: barriers, flags, row scales, softmax states, work search
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem);                      // [kWarps][kMaxSlots]
@@ -259,7 +292,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
         fence_barrier_init();
     }
     pdl_wait_prev();
-    pdl_launch_dependents();
 
     Work w;
     if (!find_work(a, (int)blockIdx.x, search, w)) {
@@ -269,65 +301,68 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
     Join next_join;
     next_join.parts = 0;
 
-    // positions of this lane's fragments in a strip
-    const uint32_t k_pos = g ^ (g >> 2);
-    const uint32_t k_row = k_pos * kv_row_bytes(FK) + j * (FK == F_Q4_0 ? 4 : 8);
-    uint32_t v_row[2][2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            v_row[x][e] = (8 * x + ((2 * j + e) ^ (j >> 1))) * kv_row_bytes(FV) + g * (FV == F_Q4_0 ? 2 : 4);
-    const uint32_t swap = (j >> 1) ? 0x1032u : 0x3210u;  // order of a pair of scales
+    const uint32_t k_row = g * kv_row_bytes(FK) + j * (FK == F_Q4_0 ? 4 : 8);
+    const uint32_t v_row = kv_quantised(FV) ? 2 * j * kv_row_bytes(FV) + g * (FV == F_Q4_0 ? 2 : 4)
+                                            : ((lane & 7) + (lane >> 4) * 8) * 32 + ((lane >> 3) & 1) * 16;
 
-    int issued = 0, taken = 0;  // strips of this warp over the whole launch: ring phases
+    // ring state of this warp, over the whole launch: copies ("units") issued
+    // and taken, the next slot of each, and the phase that the taken slot is in
+    int issued = 0, taken = 0, slot_i = 0, slot_t = 0;
+    uint32_t phase = 0;
     bool dead = false;
     Item it;
     while (next_item(a, w, it)) {
         // ---- copies of the first strips ----
-        const int mine =
-            !dead && it.end > it.begin + warp ? (it.end - it.begin - warp + kWarps - 1) / kWarps : 0;
-        // copies ("units") are numbered over the whole launch; strip n of this
-        // warp and item is it.begin + warp + kWarps n
-        const int base = issued, goal = issued + mine * C::kUnits;
+        // The warps take runs of S strips in turn; unit order within a run: the
+        // strips, or their K halves, then their V halves.
+        const int runs = (it.end - it.begin + S - 1) / S;
+        const int mine = !dead && runs > warp ? (runs - warp + kWarps - 1) / kWarps : 0;
+        const int base = issued, goal = issued + mine * S * C::kUnits;
         const uint8_t *src = nullptr;
         auto issue = [&]() {
-            const int n = (issued - base) / C::kUnits;
-            const bool is_v = C::kUnits == 2 && ((issued - base) & 1);
-            if ((n & 31) == 0 && !is_v) {  // the addresses of the next 32 strips, one per lane
-                const int strip = it.begin + warp + kWarps * (n + lane);
+            const int u = issued - base;
+            const int n = C::kUnits == 1 ? u : u / (2 * S) * S + u % S;  // strip of this warp
+            const bool is_v = C::kUnits == 2 && u % (2 * S) >= S;
+            if (u % (32 * C::kUnits) == 0) {  // the addresses of the next 32 strips, one per lane
+                const int strip = it.begin + S * warp + (n + lane) / S * S * kWarps + lane % S;
                 src = strip < it.end && it.live ? kv_strip(c, it.seq, it.head, it.first + strip) : nullptr;
             }
-            const int slot = issued % C::kSlots;
             if (lane == (n & 31)) {
-                skip[warp * kMaxSlots + slot] = src == nullptr;
+                const uint32_t bar = bar0 + 8 * slot_i;
+                skip[warp * kMaxSlots + slot_i] = src == nullptr;
                 if (src) {
                     const uint32_t bytes = C::kUnits == 1 ? C::kBytesK + C::kBytesV
                                            : is_v         ? C::kBytesV
                                                           : C::kBytesK;
-                    mbar_arrive_expect_tx(bar0 + 8 * slot, bytes);
-                    bulk_g2s(ring + slot * C::kSlotBytes, is_v ? src + C::kBytesK : src, bytes, bar0 + 8 * slot);
+                    mbar_arrive_expect_tx(bar, bytes);
+                    bulk_g2s(ring + slot_i * C::kSlotBytes, is_v ? src + C::kBytesK : src, bytes, bar);
                 } else {
-                    mbar_arrive(bar0 + 8 * slot);
+                    mbar_arrive(bar);
                 }
             }
             ++issued;
+            if (++slot_i == C::kSlots) slot_i = 0;
         };
-        // unit `taken` has landed; its slot
+        // waits for the next unit; its slot
         auto await = [&]() {
-            const int slot = taken % C::kSlots;
-            if (!mbar_wait(bar0 + 8 * slot, (uint32_t)(taken / C::kSlots) & 1u)) {
+            const int slot = slot_t;
+            if (!mbar_wait(bar0 + 8 * slot, phase)) {
                 if (lane == 0) record_error(c.err, DERR_ATTEND);
                 dead = true;
             }
+            ++taken;
+            if (++slot_t == C::kSlots) {
+                slot_t = 0;
+                phase ^= 1;
+            }
             return slot;
         };
-        // unit `taken` has been read by the whole warp: its slot is refilled
-        auto release = [&]() {
-            ++taken;
+        // n units have been read by the whole warp: their slots are refilled
+        auto refill = [&](int n) {
             fence_proxy_async_smem();
             __syncwarp();
-            if (issued < goal) issue();
+            for (int i = 0; i < n; ++i)
+                if (issued < goal) issue();
         };
         while (issued < goal && issued < taken + C::kSlots) issue();
 
@@ -374,23 +409,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                 if (d < D) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        // four dims: step and lane they belong to (see k_frag)
+                        // four dims: the step and lane that they belong to (see k_frag)
                         int step, jj;
                         float v0, v1, v2, v3;
                         if constexpr (FK == F_Q4_0) {
                             step = d / 32 * 2 + h;
                             jj = d % 32 / 8;
-                            v0 = x[i][2 * h]; v1 = x[i][2 * h + 4];
-                            v2 = x[i][2 * h + 1]; v3 = x[i][2 * h + 5];
+                            v0 = x[i][2 * h] * up; v1 = x[i][2 * h + 4] * up;
+                            v2 = x[i][2 * h + 1] * up; v3 = x[i][2 * h + 5] * up;
                         } else {
                             step = FK == F_Q8_0 ? d / 32 * 2 + h : d / 16;
                             jj = FK == F_Q8_0 ? d % 32 / 8 : d % 16 / 4 + h;
-                            v0 = x[i][4 * h]; v1 = x[i][4 * h + 1];
-                            v2 = x[i][4 * h + 2]; v3 = x[i][4 * h + 3];
+                            v0 = x[i][4 * h] * up; v1 = x[i][4 * h + 1] * up;
+                            v2 = x[i][4 * h + 2] * up; v3 = x[i][4 * h + 3] * up;
                         }
                         uint32_t s[3], t[3];
-                        split<kBfK>(v0 * up, v1 * up, s);
-                        split<kBfK>(v2 * up, v3 * up, t);
+                        split<kBfK>(v0, v1, s);
+                        split<kBfK>(v2, v3, t);
                         const int at = step * 32 + row * 4 + jj;
                         sts128(qf + at * 16, s[0], s[1], t[0], t[1]);
                         if constexpr (kBfK) {
@@ -406,208 +441,246 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
 
         // ---- the strips ----
         const float rs = row_scale[g];
-        float o[D / 16][4];
+        uint64_t o[D / 16][2];  // [tile]: rows g and g + 8 (dims), columns 2 j and 2 j + 1 (query rows)
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
+        for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = 0;
+        // the reference of the row's weights; the limit lim of s - ref, and
+        // the f16 pattern of the largest scale that lim allows for
+        float ref = -FLT_MAX, l = 0.0f;
+        float lim = kv_quantised(FV) ? 38.0f : kBfV ? 40.0f : 15.0f;
+        uint32_t d_bound = 0;
+        for (int n = 0; n < mine && !dead; ++n) {
+            const int first0 = (it.first + it.begin + S * (warp + kWarps * n)) * kStrip;
+            uint32_t sk[S], sv[S];
+            bool absent[S], edge[S], any_edge = false;
+            float s[S][2][2];  // [strip][n-tile][position 8 x + 2 j + e]
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
-        // m: running maximum of the scores (log2 domain); ref: what is
-        // subtracted, m less the exponent `up` that the weights carry
-        float m = -INFINITY, ref = -INFINITY, l = 0.0f;
-        float up = kBfV ? 0.0f : kv_quantised(FV) ? 38.0f : 14.0f;
-        while (taken < goal && !dead) {
-            int slot = await();
+            for (int t = 0; t < S; ++t) {
+                const int slot = await();
+                sk[t] = ring + slot * C::kSlotBytes;
+                sv[t] = sk[t] + C::kBytesK;
+                absent[t] = skip[warp * kMaxSlots + slot];
+                const int first = first0 + t * kStrip;
+                edge[t] = absent[t] || first < it.lo || first + kStrip > it.hi;
+                any_edge = any_edge || edge[t];
+            }
             if (dead) break;
-            const uint32_t sk = ring + slot * C::kSlotBytes;
-            const int first = (it.first + it.begin + warp + kWarps * ((taken - base) / C::kUnits)) * kStrip;
-            const bool edge = first < it.lo || first + kStrip > it.hi;
-            const bool absent = skip[warp * kMaxSlots + slot];
-            float s[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-            if (!absent) {
-                // scores
-                float acc[2][4];
+            // scores
+            {
+                float4 acc[S][2];
+                uint64_t sum[S][2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[x][k] = 0.0f;
+                for (int t = 0; t < S; ++t) sum[t][0] = sum[t][1] = 0;
 #pragma unroll
                 for (int p = 0; p < kPlanesK; ++p) {
-                    uint32_t b[2][4];
-                    k_frag<FK>(sk, p, k_row, b[0]);
-                    k_frag<FK>(sk, p, k_row + 8 * kv_row_bytes(FK), b[1]);
+                    uint32_t b[S][2][4];
+#pragma unroll
+                    for (int t = 0; t < S; ++t) {
+                        k_frag<FK>(sk[t], p, k_row, b[t][0]);
+                        k_frag<FK>(sk[t], p, k_row + 8 * kv_row_bytes(FK), b[t][1]);
+                    }
+                    if (kv_quantised(FK) || p == 0) {
+#pragma unroll
+                        for (int t = 0; t < S; ++t)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) acc[t][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
 #pragma unroll
                     for (int k = 0; k < kStepsPerPlane; ++k) {
                         const int step = p * kStepsPerPlane + k;
                         const uint4 q = lds128(qf + (step * 32 + lane) * 16);
-                        mma16<FK>(acc[0], q, b[0][2 * k], b[0][2 * k + 1]);
-                        mma16<FK>(acc[1], q, b[1][2 * k], b[1][2 * k + 1]);
+#pragma unroll
+                        for (int t = 0; t < S; ++t)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                acc[t][x] = mma<kBfK>(q, b[t][x][2 * k], b[t][x][2 * k + 1], acc[t][x]);
                         if constexpr (kBfK) {
                             const uint2 r = lds64(qf + C::kSteps * 512 + (step * 32 + lane) * 8);
                             const uint4 q3 = make_uint4(r.x, 0, r.y, 0);
-                            mma16<FK>(acc[0], q3, b[0][0], b[0][1]);
-                            mma16<FK>(acc[1], q3, b[1][0], b[1][1]);
+#pragma unroll
+                            for (int t = 0; t < S; ++t)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+                                    acc[t][x] = mma<kBfK>(q3, b[t][x][0], b[t][x][1], acc[t][x]);
                         }
                     }
-                    if constexpr (kv_quantised(FK)) {
+                    if (kv_quantised(FK) || p == kPlanesK - 1) {
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint32_t dd =
-                                lds32(sk + kv_code_bytes(FK, D) + (p * kStrip + 8 * x + 2 * j) * 2);
-                            const float2 d = unpack_f16(prmt(dd, dd, swap));
-                            s[x][0] = fmaf(d.x, acc[x][0] + acc[x][2], s[x][0]);
-                            s[x][1] = fmaf(d.y, acc[x][1] + acc[x][3], s[x][1]);
+                        for (int t = 0; t < S; ++t)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) acc[x][k] = 0.0f;
-                        }
+                            for (int x = 0; x < 2; ++x) {
+                                const uint64_t both = add2(pack_f2(acc[t][x].x, acc[t][x].y),
+                                                           pack_f2(acc[t][x].z, acc[t][x].w));
+                                if constexpr (kv_quantised(FK)) {
+                                    const float2 d = unpack_f16(lds32(
+                                        sk[t] + kv_code_bytes(FK, D) + (p * kStrip + 8 * x + 2 * j) * 2));
+                                    sum[t][x] = fma2(pack_f2(d.x, d.y), both, sum[t][x]);
+                                } else {
+                                    sum[t][x] = both;
+                                }
+                            }
                     }
                 }
-                if constexpr (!kv_quantised(FK)) {
+#pragma unroll
+                for (int t = 0; t < S; ++t)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        s[x][0] = acc[x][0] + acc[x][2];
-                        s[x][1] = acc[x][1] + acc[x][3];
+                        const float2 v = unpack2(mul2(sum[t][x], pack_f2(rs, rs)));
+                        s[t][x][0] = v.x;
+                        s[t][x][1] = v.y;
                     }
-                }
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        s[x][e] *= rs;
-                        if (edge) {
-                            const int t = first + 8 * x + ((2 * j + e) ^ (j >> 1));
-                            if (t < it.lo || t >= it.hi) s[x][e] = -INFINITY;
-                        }
-                    }
-
             }
             if constexpr (C::kUnits == 2) {
-                release();
-                slot = await();
+                refill(S);
+#pragma unroll
+                for (int t = 0; t < S; ++t) sv[t] = ring + await() * C::kSlotBytes;
                 if (dead) break;
             }
-            const uint32_t sv = ring + slot * C::kSlotBytes + (C::kUnits == 1 ? C::kBytesK : 0);
-            if (!absent) {
-                if (edge) {
+            if (any_edge) {
+#pragma unroll
+                for (int t = 0; t < S; ++t) {
+                    const int first = first0 + t * kStrip;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int at = first + 8 * x + 2 * j + e;
+                            if (absent[t] || at < it.lo || at >= it.hi) s[t][x][e] = -INFINITY;
+                        }
                     // positions that the row does not see: weights of 0 must
                     // not meet an Inf or NaN, so their V (or its scales) is cleared
-                    uint8_t *v = ring_ptr + (sv - ring);
+                    if (!edge[t]) continue;
+                    uint8_t *v = ring_ptr + (sv[t] - ring);
                     if constexpr (kv_quantised(FV)) {
                         uint16_t *d = reinterpret_cast<uint16_t *>(v + kv_code_bytes(FV, D));
                         for (int i = lane; i < D / 2; i += 32) {
-                            const int t = first + (i & 15);
-                            if (t < it.lo || t >= it.hi) d[i] = 0;
+                            const int at = first + (i & 15);
+                            if (absent[t] || at < it.lo || at >= it.hi) d[i] = 0;
                         }
                     } else {
                         for (int i = lane; i < 2 * D; i += 32) {
-                            const int t = first + ((i >> 1) & 15);
-                            if (t < it.lo || t >= it.hi)
+                            const int at = first + ((i >> 1) & 15);
+                            if (absent[t] || at < it.lo || at >= it.hi)
                                 *reinterpret_cast<uint4 *>(v + i * 16) = make_uint4(0, 0, 0, 0);
                         }
                     }
-                    __syncwarp();
                 }
+                __syncwarp();
+            }
 
-                // V's scales, and the exponent that they leave to the weights
-                uint32_t dv[kv_quantised(FV) ? kPlanesV : 1][2];
-                if constexpr (kv_quantised(FV)) {
-                    uint32_t big = 0;
+            // limits of the weights
+            float mx = s[0][0][0];
+#pragma unroll
+            for (int i = 1; i < 4 * S; ++i) mx = fmaxf(mx, s[i >> 2][(i >> 1) & 1][i & 1]);
+            bool over = mx - ref > lim;
+            uint32_t dv[S][kv_quantised(FV) ? kPlanesV : 1][2], big = 0;
+            if constexpr (kv_quantised(FV)) {
+#pragma unroll
+                for (int t = 0; t < S; ++t)
 #pragma unroll
                     for (int p = 0; p < kPlanesV; ++p)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            dv[p][x] = lds32(sv + kv_code_bytes(FV, D) + (p * kStrip + 8 * x + 2 * j) * 2);
-                            big = hmax2(big, dv[p][x] & 0x7fff7fffu);
+                            dv[t][p][x] = lds32(sv[t] + kv_code_bytes(FV, D) + (p * kStrip + 8 * x + 2 * j) * 2);
+                            big = __vmaxu2(big, dv[t][p][x] & 0x7fff7fffu);
                         }
-                    big = hmax2(big, big >> 16 | big << 16);
-                    big = hmax2(big, __shfl_xor_sync(~0u, big, 1));
-                    big = hmax2(big, __shfl_xor_sync(~0u, big, 2));
-                    // exponent of the largest scale (0 for none): weights below 2^15
-                    const float top = unpack_f16(big).x;
-                    const int e = (int)(__float_as_uint(top) >> 23) - 127;
-                    up = fminf(up, (float)(14 - max(-24, min(15, e))));
-                }
-
-                // running maximum
-                float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+                big = max(big & 0xffffu, big >> 16);
+                over = over || big > d_bound;
+            }
+            if (__any_sync(~0u, over)) {
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-                m = fmaxf(m, mx);
-                const float ref_new = m - up;  // -inf while nothing has been seen
-                const float sub = ref_new == -INFINITY ? 0.0f : ref_new;
-                if (__any_sync(~0u, ref_new != ref)) {
-                    const float f = exp2_fast(ref - sub);
-                    l *= f;
-                    const float f0 = __shfl_sync(~0u, f, 8 * j), f1 = __shfl_sync(~0u, f, 8 * j + 4);
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        o[i][0] *= f0;
-                        o[i][1] *= f1;
-                        o[i][2] *= f0;
-                        o[i][3] *= f1;
+                if constexpr (kv_quantised(FV)) {
+                    big = max(big, __shfl_xor_sync(~0u, big, 1));
+                    big = max(big, __shfl_xor_sync(~0u, big, 2));
+                    if (big > d_bound) {
+                        d_bound = big | 0x3ffu;  // all scales of this exponent
+                        const float top = f16_bits_to_f32(d_bound < 0x7c00u ? d_bound : 0x7bffu);
+                        lim = (float)(14 - ((int)(__float_as_uint(top) >> 23) - 127));
                     }
-                    ref = ref_new;
                 }
+                const float r = mx - ref > lim ? mx - (lim - 4.0f) : ref;
+                const float f = exp2_fast(ref - r);
+                ref = r;
+                l *= f;
+                const uint64_t ff = pack_f2(__shfl_sync(~0u, f, 8 * j), __shfl_sync(~0u, f, 8 * j + 4));
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    o[i][0] = mul2(o[i][0], ff);
+                    o[i][1] = mul2(o[i][1], ff);
+                }
+            }
+
+            // weights, and the weighted sum of V
+#pragma unroll
+            for (int t = 0; t < S; ++t) {
                 float pr[2][2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) pr[x][e] = exp2_fast(s[x][e] - sub);
+                    for (int e = 0; e < 2; ++e) pr[x][e] = exp2_fast(s[t][x][e] - ref);
                 l += (pr[0][0] + pr[0][1]) + (pr[1][0] + pr[1][1]);
-
-                // weighted sum of V
-                uint32_t b0[3], b1[3];
-                if constexpr (!kv_quantised(FV)) {
-                    split<kBfV>(pr[0][0], pr[0][1], b0);
-                    split<kBfV>(pr[1][0], pr[1][1], b1);
-                }
-#pragma unroll
-                for (int p = 0; p < kPlanesV; ++p) {
-                    if constexpr (kv_quantised(FV)) {
-                        const float2 d0 = unpack_f16(prmt(dv[p][0], dv[p][0], swap));
-                        const float2 d1 = unpack_f16(prmt(dv[p][1], dv[p][1], swap));
-                        split<false>(pr[0][0] * d0.x, pr[0][1] * d0.y, b0);
-                        split<false>(pr[1][0] * d1.x, pr[1][1] * d1.y, b1);
+                if (!absent[t]) {
+                    uint32_t b0[3], b1[3];
+                    if constexpr (!kv_quantised(FV)) {
+                        split<kBfV>(pr[0][0], pr[0][1], b0);
+                        split<kBfV>(pr[1][0], pr[1][1], b1);
                     }
-                    uint4 v[2];
-                    v_frag<FV>(sv, p, v_row, v);
 #pragma unroll
-                    for (int u = 0; u < kTilesPerPlane; ++u) {
-                        mma16<FV>(o[p * kTilesPerPlane + u], v[u], b0[0], b1[0]);
-                        mma16<FV>(o[p * kTilesPerPlane + u], v[u], b0[1], b1[1]);
-                        if constexpr (kBfV) mma16<FV>(o[p * kTilesPerPlane + u], v[u], b0[2], b1[2]);
+                    for (int p = 0; p < kPlanesV; ++p) {
+                        if constexpr (kv_quantised(FV)) {
+                            const float2 d0 = unpack_f16(dv[t][p][0]), d1 = unpack_f16(dv[t][p][1]);
+                            const float2 w0 = unpack2(mul2(pack_f2(pr[0][0], pr[0][1]), pack_f2(d0.x, d0.y)));
+                            const float2 w1 = unpack2(mul2(pack_f2(pr[1][0], pr[1][1]), pack_f2(d1.x, d1.y)));
+                            split<false>(w0.x, w0.y, b0);
+                            split<false>(w1.x, w1.y, b1);
+                        }
+                        uint4 v[2];
+                        v_frag<FV>(sv[t], p, v_row, v);
+#pragma unroll
+                        for (int u = 0; u < kTilesPerPlane; ++u) {
+                            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if constexpr (kBfV) acc = mma<kBfV>(v[u], b0[2], b1[2], acc);
+                            acc = mma<kBfV>(v[u], b0[1], b1[1], acc);
+                            acc = mma<kBfV>(v[u], b0[0], b1[0], acc);
+                            uint64_t(&to)[2] = o[p * kTilesPerPlane + u];
+                            to[0] = add2(to[0], pack_f2(acc.x, acc.y));
+                            to[1] = add2(to[1], pack_f2(acc.z, acc.w));
+                        }
                     }
                 }
             }
-            release();
+            refill(S);
         }
         if (dead) {
             // nothing more is issued; copies in flight land before the block ends
-            for (; taken < issued; ++taken)
-                if (!mbar_wait(bar0 + 8 * (taken % C::kSlots), (uint32_t)(taken / C::kSlots) & 1u))
-                    if (lane == 0) record_error(c.err, DERR_TEARDOWN);
-            issued = taken;
+            while (taken < issued) await();
         }
 
         // ---- the warps' results joined ----
         l += __shfl_xor_sync(~0u, l, 1);
         l += __shfl_xor_sync(~0u, l, 2);
         if (j == 0) {
-            state_m[warp * kRows + g] = ref;
+            state_m[warp * kRows + g] = ref == -FLT_MAX ? -INFINITY : ref;
             state_l[warp * kRows + g] = l;
         }
         float *merge = reinterpret_cast<float *>(ring_ptr);  // this warp's ring, all of it taken
         if (mine > 0) {
 #pragma unroll
-            for (int p = 0; p < kPlanesV; ++p)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float *to = merge + (2 * j + r) * C::kMergeRow;
-                    if constexpr (kv_quantised(FV))
-                        *reinterpret_cast<float4 *>(to + 32 * p + 4 * g) =
-                            make_float4(o[2 * p][r], o[2 * p][2 + r], o[2 * p + 1][r], o[2 * p + 1][2 + r]);
-                    else
-                        *reinterpret_cast<float2 *>(to + 16 * p + 2 * g) = make_float2(o[p][r], o[p][2 + r]);
+            for (int i = 0; i < D / 16; ++i) {
+                const float2 even = unpack2(o[i][0]), odd = unpack2(o[i][1]);
+                float *r0 = merge + 2 * j * C::kMergeRow, *r1 = r0 + C::kMergeRow;
+                if constexpr (kv_quantised(FV)) {
+                    const int d = 32 * (i / 2) + 4 * g + 2 * (i & 1);
+                    *reinterpret_cast<float2 *>(r0 + d) = make_float2(even.x, odd.x);
+                    *reinterpret_cast<float2 *>(r1 + d) = make_float2(even.y, odd.y);
+                } else {
+                    r0[16 * i + g] = even.x;
+                    r1[16 * i + g] = even.y;
+                    r0[16 * i + 8 + g] = odd.x;
+                    r1[16 * i + 8 + g] = odd.y;
                 }
+            }
         }
         __syncthreads();
         const bool whole = it.begin == 0 && it.end == it.strips;
@@ -648,6 +721,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
         __syncthreads();
     }
     if (threadIdx.x == 0) a.joins[blockIdx.x] = next_join;
+    pdl_launch_dependents();
 }
 
 template <int FK, int FV, int D>
