@@ -111,7 +111,7 @@ cudaError_t launch_attend(const Attend &a, const DeviceInfo &dev, cudaStream_t s
     p.q_stride = a.q_stride;
     p.out_stride = a.out_stride;
     p.window = a.window;
-    p.rows = a.c.n_seqs * a.n_new;
+    p.rows = (int)(a.c.n_seqs * a.n_new);
     p.n_new = (int)a.n_new;
     p.group = a.n_heads / a.c.n_kv;
     p.subs = (p.group + attend::kRows - 1) / attend::kRows;

@@ -38,6 +38,7 @@ __host__ __device__ constexpr Shape shape_for(int fk, int fv, int dim, int ctas)
     s.slot_bytes = s.units == 1 ? k + v : k > v ? k : v;
     s.slots = budget / s.slot_bytes < kMaxSlots ? budget / s.slot_bytes : kMaxSlots;
     s.step = s.slots >= 4 ? 2 : 1;
+    s.slots -= s.slots % s.step;
     const int merge = (kRows * (dim + 4) * 4 + 127) / 128 * 128;
     s.ring_bytes = s.slots * s.slot_bytes > merge ? s.slots * s.slot_bytes : merge;
     s.smem = kFixedBytes + s.q_bytes + kWarps * s.ring_bytes;
@@ -73,7 +74,8 @@ struct AttendParams {
     float *out;
     float *parts;      // [2 grid][part_floats]: results of a share's first (0) and last (1) item
     Join *joins;       // [grid]
-    int64_t q_stride, out_stride, window, rows;  // rows = n_seqs * n_new
+    int64_t q_stride, out_stride, window;
+    int rows;                // n_seqs * n_new
     int n_new, group, subs;  // query heads per kv head, and items that they make
     float scale_log2;  // scale * log2(e)
     bool vec;
@@ -86,11 +88,11 @@ __host__ __device__ constexpr int part_floats(int dim) { return kRows * (dim + 2
 struct RowRange {
     int seq, lo, hi, first, strips;
 };
-__device__ __forceinline__ RowRange row_range(const AttendParams &a, int64_t r) {
+__device__ __forceinline__ RowRange row_range(const AttendParams &a, int r) {
     RowRange x;
-    x.seq = (int)(r / a.n_new);
+    x.seq = a.n_new == 1 ? r : r / a.n_new;
     const int held = __ldg(a.c.lens + x.seq);
-    const int64_t pos = (int64_t)(held < 0 ? 0 : held) - a.n_new + (r - (int64_t)x.seq * a.n_new);
+    const int64_t pos = (int64_t)(held < 0 ? 0 : held) - a.n_new + (r - x.seq * a.n_new);
     int64_t hi = pos + 1;
     if (hi > a.c.capacity) {
         record_error(a.c.err, DERR_BAD_PAGE);
@@ -112,13 +114,15 @@ __device__ __forceinline__ int item_strips(const RowRange &x) { return x.strips 
 // Where a CTA's share begins.
 struct WorkSearch {
     long long sum[kWarps];
-    long long row, base;
+    long long base;
+    int row;
 };
 struct Work {
     int64_t at, end;     // the share, in strips and item costs of all items end to end
     int64_t total;
     int shares;          // CTAs that have one
-    int64_t row, base;   // the row that `at` is in, and where it begins
+    int row;             // the row that `at` is in
+    int64_t base;        // and where that begins
 };
 
 // The share of CTA `cta`; false when it has none. Every thread of the block
@@ -126,12 +130,11 @@ struct Work {
 // rows each: a few loads for a decoding batch.
 __device__ __forceinline__ bool find_work(const AttendParams &a, int cta, WorkSearch *sh, Work &w) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t per = (a.rows + kThreads - 1) / kThreads;
-    const int64_t r0 = tid * per < a.rows ? tid * per : a.rows;
-    const int64_t r1 = r0 + per < a.rows ? r0 + per : a.rows;
+    const int per = (a.rows + kThreads - 1) / kThreads;
+    const int r0 = min(tid * per, a.rows), r1 = min(r0 + per, a.rows);
     const int64_t items = (int64_t)a.c.n_kv * a.subs;
     int64_t mine = 0;
-    for (int64_t r = r0; r < r1; ++r) mine += item_strips(row_range(a, r)) + kItemCost;
+    for (int r = r0; r < r1; ++r) mine += item_strips(row_range(a, r)) + kItemCost;
     mine *= items;
     int64_t upto = mine;  // inclusive sums over the warp, then over the warps
 #pragma unroll
@@ -154,7 +157,7 @@ __device__ __forceinline__ bool find_work(const AttendParams &a, int cta, WorkSe
     w.end = (int64_t)(cta + 1) * total / w.shares;
     int64_t base = before + upto - mine;
     if (w.at >= base && w.at < base + mine) {
-        for (int64_t r = r0; r < r1; ++r) {
+        for (int r = r0; r < r1; ++r) {
             const int64_t n = (item_strips(row_range(a, r)) + kItemCost) * items;
             if (w.at < base + n) {
                 sh->row = r;

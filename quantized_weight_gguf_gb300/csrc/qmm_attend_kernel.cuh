@@ -135,6 +135,18 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&t)[3]) {
     }
 }
 
+// Whether the phase with this parity has completed (no waiting).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -251,12 +263,14 @@ struct Cfg {
     static constexpr int kUnits = kShape.units, kSlots = kShape.slots, kSlotBytes = kShape.slot_bytes;
     static constexpr int kBytesK = kv_half_bytes(FK, D), kBytesV = kv_half_bytes(FV, D);
     static constexpr int kSteps = D / 16;
-    static constexpr int kStep = kShape.step;
+    static constexpr int kStep = kShape.step, kGroups = kSlots / kStep;
     static constexpr int kQBytes = kShape.q_bytes;
     static constexpr int kRingBytes = kShape.ring_bytes;
     static constexpr int kMergeRow = D + 4;  // floats; + 4 spreads the rows j over the banks
     static constexpr int kSmem = kShape.smem;
-    static_assert(kSlots >= 2, "a ring needs two slots");
+    static_assert(kSlots % kStep == 0 && kGroups >= 2 && kSlots <= kMaxSlots, "a ring holds two runs");
+    static_assert(kWarps * kMaxSlots * 12 + kRows * 4 + kWarps * kRows * 8 + sizeof(WorkSearch) <= kFixedBytes,
+                  "fixed part of shared memory");
     static_assert(kShape.ctas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
     static_assert(kSlotBytes % 16 == 0 && kBytesK % 16 == 0 && kRingBytes % 16 == 0 && kQBytes % 16 == 0,
                   "alignment");
@@ -276,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
     extern __shared__ __align__(128) uint8_t smem[];
     // fixed part: barriers, flags, row scales, softmax states, work search
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem);                      // [kWarps][kMaxSlots]
-    uint32_t *skip = reinterpret_cast<uint32_t *>(smem + kWarps * 64);        // [kWarps][kMaxSlots]
+    uint32_t *landed = reinterpret_cast<uint32_t *>(smem + kWarps * 64);      // [kWarps][kMaxSlots]
     float *row_scale = reinterpret_cast<float *>(smem + kWarps * 96);         // [kRows]
     float *state_m = row_scale + kRows;                                       // [kWarps][kRows]
     float *state_l = state_m + kWarps * kRows;                                // [kWarps][kRows]
@@ -288,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
     uint8_t *ring_ptr = q_frag + C::kQBytes + warp * C::kRingBytes;
     const uint32_t ring = smem_addr(ring_ptr), qf = smem_addr(q_frag);
     if (lane == 0) {
-        for (int i = 0; i < C::kSlots; ++i) mbar_init(bar0 + 8 * i, 1);
+        for (int i = 0; i < C::kGroups; ++i) mbar_init(bar0 + 8 * i, 1);
         fence_barrier_init();
     }
     pdl_wait_prev();
@@ -305,66 +319,79 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
     const uint32_t v_row = kv_quantised(FV) ? 2 * j * kv_row_bytes(FV) + g * (FV == F_Q4_0 ? 2 : 4)
                                             : ((lane & 7) + (lane >> 4) * 8) * 32 + ((lane >> 3) & 1) * 16;
 
-    // ring state of this warp, over the whole launch: copies ("units") issued
-    // and taken, the next slot of each, and the phase that the taken slot is in
-    int issued = 0, taken = 0, slot_i = 0, slot_t = 0;
+    // what the accumulators of a product start from; opaque, so that the four
+    // registers are kept instead of being cleared for every product
+    float4 zero;
+    asm volatile("mov.b32 %0, 0; mov.b32 %1, 0; mov.b32 %2, 0; mov.b32 %3, 0;"
+                 : "=f"(zero.x), "=f"(zero.y), "=f"(zero.z), "=f"(zero.w));
+
+    // Ring of this warp, over the whole launch: groups of S slots (the strips
+    // of a run, or their K or V halves) with one barrier each; the next group
+    // to be filled and to be taken, and the phase of the latter.
+    int fill = 0, take = 0, flying = 0;
     uint32_t phase = 0;
     bool dead = false;
     Item it;
     while (next_item(a, w, it)) {
+        if (!it.live) {
+            for (int i = threadIdx.x; i < it.heads * D / 4; i += kThreads) {
+                const int row = i / (D / 4);
+                put_out(a, it.row, it.head0 + row, (i - row * (D / 4)) * 4, D, make_float4(0.f, 0.f, 0.f, 0.f), 0.0f);
+            }
+            continue;
+        }
         // ---- copies of the first strips ----
-        // The warps take runs of S strips in turn; unit order within a run: the
-        // strips, or their K halves, then their V halves.
+        // The warps take runs of S strips in turn.
         const int runs = (it.end - it.begin + S - 1) / S;
         const int mine = !dead && runs > warp ? (runs - warp + kWarps - 1) / kWarps : 0;
-        const int base = issued, goal = issued + mine * S * C::kUnits;
-        const uint8_t *src = nullptr;
+        int left = mine * C::kUnits, strip = 0;  // groups to be issued; the next one's first strip
+        bool half_v = false;
+        const uint8_t *src = nullptr;            // of lane l: strip l of the current 32 of this warp
+        uint32_t have = 0;                       // which of them exist
         auto issue = [&]() {
-            const int u = issued - base;
-            const int n = C::kUnits == 1 ? u : u / (2 * S) * S + u % S;  // strip of this warp
-            const bool is_v = C::kUnits == 2 && u % (2 * S) >= S;
-            if (u % (32 * C::kUnits) == 0) {  // the addresses of the next 32 strips, one per lane
-                const int strip = it.begin + S * warp + (n + lane) / S * S * kWarps + lane % S;
-                src = strip < it.end && it.live ? kv_strip(c, it.seq, it.head, it.first + strip) : nullptr;
+            if ((strip & 31) == 0 && !half_v) {
+                const int at = it.begin + S * warp + (strip + lane) / S * S * kWarps + lane % S;
+                src = at < it.end ? kv_strip(c, it.seq, it.head, it.first + at) : nullptr;
+                have = __ballot_sync(~0u, src != nullptr);
             }
-            if (lane == (n & 31)) {
-                const uint32_t bar = bar0 + 8 * slot_i;
-                skip[warp * kMaxSlots + slot_i] = src == nullptr;
-                if (src) {
-                    const uint32_t bytes = C::kUnits == 1 ? C::kBytesK + C::kBytesV
-                                           : is_v         ? C::kBytesV
-                                                          : C::kBytesK;
-                    mbar_arrive_expect_tx(bar, bytes);
-                    bulk_g2s(ring + slot_i * C::kSlotBytes, is_v ? src + C::kBytesK : src, bytes, bar);
-                } else {
-                    mbar_arrive(bar);
-                }
+            const uint32_t bytes = C::kUnits == 1 ? C::kBytesK + C::kBytesV : half_v ? C::kBytesV : C::kBytesK;
+            const uint32_t bar = bar0 + 8 * fill, t = lane - (strip & 31);
+            const uint32_t these = (have >> (strip & 31)) & ((1u << S) - 1);
+            if (t == 0) {
+                landed[warp * kMaxSlots + fill] = these;
+                mbar_arrive_expect_tx(bar, __popc(these) * bytes);
             }
-            ++issued;
-            if (++slot_i == C::kSlots) slot_i = 0;
+            __syncwarp();
+            if (t < S && src)
+                bulk_g2s(ring + (fill * S + t) * C::kSlotBytes, half_v ? src + C::kBytesK : src, bytes, bar);
+            if (C::kUnits == 1 || half_v) strip += S;
+            if (C::kUnits == 2) half_v = !half_v;
+            if (++fill == C::kGroups) fill = 0;
+            ++flying;
+            --left;
         };
-        // waits for the next unit; its slot
+        // waits for the next group; its index
         auto await = [&]() {
-            const int slot = slot_t;
-            if (!mbar_wait(bar0 + 8 * slot, phase)) {
-                if (lane == 0) record_error(c.err, DERR_ATTEND);
-                dead = true;
-            }
-            ++taken;
-            if (++slot_t == C::kSlots) {
-                slot_t = 0;
+            const int group = take;
+            if (!__all_sync(~0u, mbar_test(bar0 + 8 * group, phase)))
+                if (__any_sync(~0u, !mbar_wait(bar0 + 8 * group, phase))) {
+                    if (lane == 0) record_error(c.err, DERR_ATTEND);
+                    dead = true;
+                }
+            if (++take == C::kGroups) {
+                take = 0;
                 phase ^= 1;
             }
-            return slot;
+            --flying;
+            return group;
         };
-        // n units have been read by the whole warp: their slots are refilled
-        auto refill = [&](int n) {
+        // the group last taken has been read by the whole warp: it is refilled
+        auto refill = [&]() {
             fence_proxy_async_smem();
             __syncwarp();
-            for (int i = 0; i < n; ++i)
-                if (issued < goal) issue();
+            if (left > 0) issue();
         };
-        while (issued < goal && issued < taken + C::kSlots) issue();
+        while (left > 0 && flying < C::kGroups) issue();
 
         // ---- query rows as A fragments ----
         {
@@ -449,22 +476,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
         float ref = -FLT_MAX, l = 0.0f;
         float lim = kv_quantised(FV) ? 38.0f : kBfV ? 40.0f : 15.0f;
         uint32_t d_bound = 0;
-        for (int n = 0; n < mine && !dead; ++n) {
-            const int first0 = (it.first + it.begin + S * (warp + kWarps * n)) * kStrip;
-            uint32_t sk[S], sv[S];
-            bool absent[S], edge[S], any_edge = false;
-            float s[S][2][2];  // [strip][n-tile][position 8 x + 2 j + e]
-#pragma unroll
-            for (int t = 0; t < S; ++t) {
-                const int slot = await();
-                sk[t] = ring + slot * C::kSlotBytes;
-                sv[t] = sk[t] + C::kBytesK;
-                absent[t] = skip[warp * kMaxSlots + slot];
-                const int first = first0 + t * kStrip;
-                edge[t] = absent[t] || first < it.lo || first + kStrip > it.hi;
-                any_edge = any_edge || edge[t];
-            }
+        for (int n = 0; n < mine; ++n) {
+            const int first = (it.first + it.begin + S * (warp + kWarps * n)) * kStrip;
+            int group = await();
             if (dead) break;
+            const uint32_t sk = ring + group * S * C::kSlotBytes;
+            const uint32_t here = landed[warp * kMaxSlots + group];
+            const bool edge = first < it.lo || first + S * kStrip > it.hi || here != (1u << S) - 1;
+            float s[S][2][2];  // [strip][n-tile][position 8 x + 2 j + e]
             // scores
             {
                 float4 acc[S][2];
@@ -476,14 +495,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                     uint32_t b[S][2][4];
 #pragma unroll
                     for (int t = 0; t < S; ++t) {
-                        k_frag<FK>(sk[t], p, k_row, b[t][0]);
-                        k_frag<FK>(sk[t], p, k_row + 8 * kv_row_bytes(FK), b[t][1]);
+                        k_frag<FK>(sk + t * C::kSlotBytes, p, k_row, b[t][0]);
+                        k_frag<FK>(sk + t * C::kSlotBytes, p, k_row + 8 * kv_row_bytes(FK), b[t][1]);
                     }
                     if (kv_quantised(FK) || p == 0) {
 #pragma unroll
                         for (int t = 0; t < S; ++t)
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) acc[t][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            for (int x = 0; x < 2; ++x) acc[t][x] = zero;
                     }
 #pragma unroll
                     for (int k = 0; k < kStepsPerPlane; ++k) {
@@ -513,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                                                            pack_f2(acc[t][x].z, acc[t][x].w));
                                 if constexpr (kv_quantised(FK)) {
                                     const float2 d = unpack_f16(lds32(
-                                        sk[t] + kv_code_bytes(FK, D) + (p * kStrip + 8 * x + 2 * j) * 2));
+                                        sk + t * C::kSlotBytes + kv_code_bytes(FK, D) + (p * kStrip + 8 * x + 2 * j) * 2));
                                     sum[t][x] = fma2(pack_f2(d.x, d.y), both, sum[t][x]);
                                 } else {
                                     sum[t][x] = both;
@@ -531,36 +550,37 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                     }
             }
             if constexpr (C::kUnits == 2) {
-                refill(S);
-#pragma unroll
-                for (int t = 0; t < S; ++t) sv[t] = ring + await() * C::kSlotBytes;
+                refill();
+                group = await();
                 if (dead) break;
             }
-            if (any_edge) {
+            const uint32_t sv = ring + group * S * C::kSlotBytes + (C::kUnits == 1 ? C::kBytesK : 0);
+            if (edge) {
+                // positions that the row does not see: their scores are
+                // dropped, and since weights of 0 must not meet an Inf or NaN,
+                // their V (or its scales) is cleared
 #pragma unroll
                 for (int t = 0; t < S; ++t) {
-                    const int first = first0 + t * kStrip;
+                    const int from = it.lo - (first + t * kStrip);
+                    const int to = here >> t & 1 ? it.hi - (first + t * kStrip) : 0;
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int at = first + 8 * x + 2 * j + e;
-                            if (absent[t] || at < it.lo || at >= it.hi) s[t][x][e] = -INFINITY;
+                            const int at = 8 * x + 2 * j + e;
+                            if (at < from || at >= to) s[t][x][e] = -INFINITY;
                         }
-                    // positions that the row does not see: weights of 0 must
-                    // not meet an Inf or NaN, so their V (or its scales) is cleared
-                    if (!edge[t]) continue;
-                    uint8_t *v = ring_ptr + (sv[t] - ring);
+                    uint8_t *v = ring_ptr + (sv - ring) + t * C::kSlotBytes;
                     if constexpr (kv_quantised(FV)) {
                         uint16_t *d = reinterpret_cast<uint16_t *>(v + kv_code_bytes(FV, D));
                         for (int i = lane; i < D / 2; i += 32) {
-                            const int at = first + (i & 15);
-                            if (absent[t] || at < it.lo || at >= it.hi) d[i] = 0;
+                            const int at = i & 15;
+                            if (at < from || at >= to) d[i] = 0;
                         }
                     } else {
                         for (int i = lane; i < 2 * D; i += 32) {
-                            const int at = first + ((i >> 1) & 15);
-                            if (absent[t] || at < it.lo || at >= it.hi)
+                            const int at = (i >> 1) & 15;
+                            if (at < from || at >= to)
                                 *reinterpret_cast<uint4 *>(v + i * 16) = make_uint4(0, 0, 0, 0);
                         }
                     }
@@ -581,8 +601,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                     for (int p = 0; p < kPlanesV; ++p)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            dv[t][p][x] = lds32(sv[t] + kv_code_bytes(FV, D) + (p * kStrip + 8 * x + 2 * j) * 2);
-                            big = __vmaxu2(big, dv[t][p][x] & 0x7fff7fffu);
+                            dv[t][p][x] = lds32(sv + t * C::kSlotBytes + kv_code_bytes(FV, D) +
+                                                (p * kStrip + 8 * x + 2 * j) * 2);
+                            // Q8_0's scales have no sign
+                            big = __vmaxu2(big, FV == F_Q8_0 ? dv[t][p][x] : dv[t][p][x] & 0x7fff7fffu);
                         }
                 big = max(big & 0xffffu, big >> 16);
                 over = over || big > d_bound;
@@ -620,8 +642,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) pr[x][e] = exp2_fast(s[t][x][e] - ref);
                 l += (pr[0][0] + pr[0][1]) + (pr[1][0] + pr[1][1]);
-                if (!absent[t]) {
-                    uint32_t b0[3], b1[3];
+                uint32_t b0[3], b1[3];
+                {
                     if constexpr (!kv_quantised(FV)) {
                         split<kBfV>(pr[0][0], pr[0][1], b0);
                         split<kBfV>(pr[1][0], pr[1][1], b1);
@@ -636,10 +658,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                             split<false>(w1.x, w1.y, b1);
                         }
                         uint4 v[2];
-                        v_frag<FV>(sv[t], p, v_row, v);
+                        v_frag<FV>(sv + t * C::kSlotBytes, p, v_row, v);
 #pragma unroll
                         for (int u = 0; u < kTilesPerPlane; ++u) {
-                            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                            float4 acc = zero;
                             if constexpr (kBfV) acc = mma<kBfV>(v[u], b0[2], b1[2], acc);
                             acc = mma<kBfV>(v[u], b0[1], b1[1], acc);
                             acc = mma<kBfV>(v[u], b0[0], b1[0], acc);
@@ -650,12 +672,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                     }
                 }
             }
-            refill(S);
+            refill();
         }
-        if (dead) {
-            // nothing more is issued; copies in flight land before the block ends
-            while (taken < issued) await();
-        }
+        // after an expired wait nothing more is issued; copies in flight land
+        // (or their waits expire too) before the block ends
+        while (dead && flying > 0) await();
 
         // ---- the warps' results joined ----
         l += __shfl_xor_sync(~0u, l, 1);
