@@ -25,7 +25,8 @@
 //  - O^T = V^T P^T: 16 dims are the rows of A, the eight query rows the columns
 //    of B. The weights p enter as two fp16 terms as well (two products into
 //    one accumulator). For quantised V a block's scale d is folded into the
-//    weight first: w = p d. A strip's product starts from zero and is added
+//    weight's terms first, w = p d = h + r: h = fl(p_h d), and with one fma
+//    each r = fl(p_r d + (p_h d - h)), where the bracket is exact. A strip's product starts from zero and is added
 //    to the running sums in fp32, so their rounding is to nearest.
 //  - Integer codes enter as exact fp16 integers: the code with its offset
 //    under the exponent of 1024 (a byte permute or a mask), less 1024 and the
@@ -38,11 +39,11 @@
 // them for the second, so p stays in registers.
 //
 // The softmax subtracts a reference R per row that is not the exact running
-// maximum: a weight 2^(s - R) may grow to 2^lim, where the largest w = p d is
-// just below 2^15. Only when a score (or a scale d) passes that limit is R moved, to
-// 4 below the limit for the largest score seen, and the sums rescaled; so a
-// strip normally takes no shuffles, and the weights that matter stay far from
-// the fp16 terms' subnormal range.
+// maximum: a weight 2^(s - R) may grow to 2^lim, lim = 15, less where scales d
+// of 1 and more would take w = p d past 2^15. Only when a score (or a scale)
+// passes that limit is R moved, to 4 below the limit for the largest score
+// seen, and the sums rescaled; so a strip normally takes no shuffles, and the
+// weights that matter stay far from the fp16 terms' subnormal range.
 #pragma once
 
 #include <cfloat>
@@ -163,18 +164,40 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// a b - c
+__device__ __forceinline__ uint32_t hfms2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("{\n .reg .b32 n;\n neg.f16x2 n, %3;\n fma.rn.f16x2 %0, %1, %2, n;\n}"
+        : "=r"(r)
+        : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+// A value that the compiler takes for a variable: constants that every
+// fragment needs stay in registers instead of being moved there each time
+// (with one immediate per instruction, permutes and masks need them there).
+__device__ __forceinline__ uint32_t held(uint32_t v) {
+    uint32_t r;
+    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
 // Two bytes of w (two's complement, bit 7 already flipped) as an exact fp16
-// pair: 1024 + 128 + code, less 1152.
+// pair: 1024 + 128 + code, less 1152. k0: 0x64646464.
 template <int SEL>
-__device__ __forceinline__ uint32_t bytes_f16(uint32_t w) {
-    return hsub2(prmt(w, 0x64646464u, SEL), 0x64806480u);
+__device__ __forceinline__ uint32_t bytes_f16(uint32_t w, uint32_t k0) {
+    return hsub2(prmt(w, k0, SEL), 0x64806480u);
 }
 // The two nibbles that sit at bits SH and SH + 16 of w (SH 0 or 4), less 8, as
-// an exact fp16 pair: 1024 + n - 1032, or (1024 + 16 n) / 16 - 72.
+// an exact fp16 pair: 1024 + n - 1032, or (1024 + 16 n) / 16 - 72. k0:
+// 0x64006400, k1: 1/16 twice.
 template <int SH>
-__device__ __forceinline__ uint32_t nibbles_f16(uint32_t w) {
-    if constexpr (SH == 0) return hsub2((w & 0x000f000fu) | 0x64006400u, 0x64086408u);
-    else return hfma2((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);
+__device__ __forceinline__ uint32_t nibbles_f16(uint32_t w, uint32_t k0, uint32_t k1) {
+    if constexpr (SH == 0) return hsub2((w & 0x000f000fu) | k0, 0x64086408u);
+    else return hfma2((w & 0x00f000f0u) | k0, k1, 0xd480d480u);
 }
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -199,7 +222,8 @@ __device__ __forceinline__ uint4 ldsm_trans(uint32_t a) {
 // plus its bytes in the row. The dims of lane j: 16-bit: 4 j + {0, 1 | 2, 3};
 // Q8_0, step k: 8 j + 4 k + {0, 1 | 2, 3}; Q4_0, step k: 8 j + 2 k + {0, 4 | 1, 5}.
 template <int F>
-__device__ __forceinline__ void k_frag(uint32_t base, int p, uint32_t row, uint32_t (&b)[4]) {
+__device__ __forceinline__ void k_frag(uint32_t base, int p, uint32_t row, uint32_t k0, uint32_t k1,
+                                       uint32_t (&b)[4]) {
     if constexpr (!kv_quantised(F)) {
         const uint2 w = lds64(base + p * 512 + row);
         b[0] = w.x;
@@ -208,16 +232,16 @@ __device__ __forceinline__ void k_frag(uint32_t base, int p, uint32_t row, uint3
         uint2 w = lds64(base + p * 512 + row);
         w.x ^= 0x80808080u;
         w.y ^= 0x80808080u;
-        b[0] = bytes_f16<0x4140>(w.x);
-        b[1] = bytes_f16<0x4342>(w.x);
-        b[2] = bytes_f16<0x4140>(w.y);
-        b[3] = bytes_f16<0x4342>(w.y);
+        b[0] = bytes_f16<0x4140>(w.x, k0);
+        b[1] = bytes_f16<0x4342>(w.x, k0);
+        b[2] = bytes_f16<0x4140>(w.y, k0);
+        b[3] = bytes_f16<0x4342>(w.y, k0);
     } else {
         const uint32_t w = lds32(base + p * 256 + row), v = w >> 8;
-        b[0] = nibbles_f16<0>(w);
-        b[1] = nibbles_f16<4>(w);
-        b[2] = nibbles_f16<0>(v);
-        b[3] = nibbles_f16<4>(v);
+        b[0] = nibbles_f16<0>(w, k0, k1);
+        b[1] = nibbles_f16<4>(w, k0, k1);
+        b[2] = nibbles_f16<0>(v, k0, k1);
+        b[3] = nibbles_f16<4>(v, k0, k1);
     }
 }
 
@@ -227,7 +251,8 @@ __device__ __forceinline__ void k_frag(uint32_t base, int p, uint32_t row, uint3
 // dims 32 p + 4 g + 2 u and + 1; `row` is the byte offset of position 2 j and
 // dims 4 g.
 template <int F>
-__device__ __forceinline__ void v_frag(uint32_t base, int p, uint32_t row, uint4 (&a)[2]) {
+__device__ __forceinline__ void v_frag(uint32_t base, int p, uint32_t row, uint32_t k0, uint32_t k1,
+                                       uint4 (&a)[2]) {
     if constexpr (!kv_quantised(F)) {
         a[0] = ldsm_trans(base + p * 512 + row);
     } else if constexpr (F == F_Q8_0) {
@@ -239,10 +264,10 @@ __device__ __forceinline__ void v_frag(uint32_t base, int p, uint32_t row, uint4
             lo[x] = prmt(w0, w1, 0x5140);
             hi[x] = prmt(w0, w1, 0x7362);
         }
-        a[0] = make_uint4(bytes_f16<0x4140>(lo[0]), bytes_f16<0x4342>(lo[0]), bytes_f16<0x4140>(lo[1]),
-                          bytes_f16<0x4342>(lo[1]));
-        a[1] = make_uint4(bytes_f16<0x4140>(hi[0]), bytes_f16<0x4342>(hi[0]), bytes_f16<0x4140>(hi[1]),
-                          bytes_f16<0x4342>(hi[1]));
+        a[0] = make_uint4(bytes_f16<0x4140>(lo[0], k0), bytes_f16<0x4342>(lo[0], k0), bytes_f16<0x4140>(lo[1], k0),
+                          bytes_f16<0x4342>(lo[1], k0));
+        a[1] = make_uint4(bytes_f16<0x4140>(hi[0], k0), bytes_f16<0x4342>(hi[0], k0), bytes_f16<0x4140>(hi[1], k0),
+                          bytes_f16<0x4342>(hi[1], k0));
     } else {
         uint32_t w[2], v[2];
 #pragma unroll
@@ -251,8 +276,8 @@ __device__ __forceinline__ void v_frag(uint32_t base, int p, uint32_t row, uint4
                         0x5410);
             v[x] = w[x] >> 8;
         }
-        a[0] = make_uint4(nibbles_f16<0>(w[0]), nibbles_f16<4>(w[0]), nibbles_f16<0>(w[1]), nibbles_f16<4>(w[1]));
-        a[1] = make_uint4(nibbles_f16<0>(v[0]), nibbles_f16<4>(v[0]), nibbles_f16<0>(v[1]), nibbles_f16<4>(v[1]));
+        a[0] = make_uint4(nibbles_f16<0>(w[0], k0, k1), nibbles_f16<4>(w[0], k0, k1), nibbles_f16<0>(w[1], k0, k1), nibbles_f16<4>(w[1], k0, k1));
+        a[1] = make_uint4(nibbles_f16<0>(v[0], k0, k1), nibbles_f16<4>(v[0], k0, k1), nibbles_f16<0>(v[1], k0, k1), nibbles_f16<4>(v[1], k0, k1));
     }
 }
 // ----------------------------------------------------------------- config ----
@@ -319,11 +344,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
     const uint32_t v_row = kv_quantised(FV) ? 2 * j * kv_row_bytes(FV) + g * (FV == F_Q4_0 ? 2 : 4)
                                             : ((lane & 7) + (lane >> 4) * 8) * 32 + ((lane >> 3) & 1) * 16;
 
-    // what the accumulators of a product start from; opaque, so that the four
-    // registers are kept instead of being cleared for every product
-    float4 zero;
-    asm volatile("mov.b32 %0, 0; mov.b32 %1, 0; mov.b32 %2, 0; mov.b32 %3, 0;"
-                 : "=f"(zero.x), "=f"(zero.y), "=f"(zero.z), "=f"(zero.w));
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint32_t kk0 = FK == F_Q8_0 ? held(0x64646464u) : FK == F_Q4_0 ? held(0x64006400u) : 0;
+    const uint32_t vk0 = FV == FK ? kk0 : FV == F_Q4_0 ? held(0x64006400u) : 0;
+    const uint32_t vk1 = FV == F_Q4_0 ? held(0x2c002c00u) : 0, kk1 = FK == F_Q4_0 ? vk1 : 0;
 
     // Ring of this warp, over the whole launch: groups of S slots (the strips
     // of a run, or their K or V halves) with one barrier each; the next group
@@ -471,11 +495,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
         uint64_t o[D / 16][2];  // [tile]: rows g and g + 8 (dims), columns 2 j and 2 j + 1 (query rows)
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = 0;
-        // the reference of the row's weights; the limit lim of s - ref, and
-        // the f16 pattern of the largest scale that lim allows for
-        float ref = -FLT_MAX, l = 0.0f;
-        float lim = kv_quantised(FV) ? 38.0f : kBfV ? 40.0f : 15.0f;
-        uint32_t d_bound = 0;
+        // the reference of the row's weights and their total (of positions
+        // 2 j and 2 j + 1 of the n-tiles); the limit lim of s - ref, and the f16
+        // pattern of the largest scale that lim allows for
+        float ref = -FLT_MAX;
+        uint64_t l = 0;
+        float lim = kBfV ? 40.0f : 15.0f;
+        uint32_t d_bound = 0x3bffu;  // below 1
         for (int n = 0; n < mine; ++n) {
             const int first = (it.first + it.begin + S * (warp + kWarps * n)) * kStrip;
             int group = await();
@@ -495,8 +521,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                     uint32_t b[S][2][4];
 #pragma unroll
                     for (int t = 0; t < S; ++t) {
-                        k_frag<FK>(sk + t * C::kSlotBytes, p, k_row, b[t][0]);
-                        k_frag<FK>(sk + t * C::kSlotBytes, p, k_row + 8 * kv_row_bytes(FK), b[t][1]);
+                        k_frag<FK>(sk + t * C::kSlotBytes, p, k_row, kk0, kk1, b[t][0]);
+                        k_frag<FK>(sk + t * C::kSlotBytes, p, k_row + 8 * kv_row_bytes(FK), kk0,
+                                   kk1, b[t][1]);
                     }
                     if (kv_quantised(FK) || p == 0) {
 #pragma unroll
@@ -624,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                 const float r = mx - ref > lim ? mx - (lim - 4.0f) : ref;
                 const float f = exp2_fast(ref - r);
                 ref = r;
-                l *= f;
+                l = mul2(l, pack_f2(f, f));
                 const uint64_t ff = pack_f2(__shfl_sync(~0u, f, 8 * j), __shfl_sync(~0u, f, 8 * j + 4));
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -633,43 +660,53 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                 }
             }
 
-            // weights, and the weighted sum of V
+            // weights, as the terms of n-tiles 0 and 1
+            uint32_t w0[S][3], w1[S][3];
+            const uint64_t less = pack_f2(-ref, -ref);
 #pragma unroll
             for (int t = 0; t < S; ++t) {
-                float pr[2][2];
+                float2 x0 = unpack2(add2(pack_f2(s[t][0][0], s[t][0][1]), less));
+                float2 x1 = unpack2(add2(pack_f2(s[t][1][0], s[t][1][1]), less));
+                x0 = make_float2(exp2_fast(x0.x), exp2_fast(x0.y));
+                x1 = make_float2(exp2_fast(x1.x), exp2_fast(x1.y));
+                l = add2(l, add2(pack_f2(x0.x, x0.y), pack_f2(x1.x, x1.y)));
+                split<kBfV>(x0.x, x0.y, w0[t]);
+                split<kBfV>(x1.x, x1.y, w1[t]);
+            }
+            // weighted sum of V
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+            for (int p = 0; p < kPlanesV; ++p) {
+                float4 acc[2] = {zero, zero};
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) pr[x][e] = exp2_fast(s[t][x][e] - ref);
-                l += (pr[0][0] + pr[0][1]) + (pr[1][0] + pr[1][1]);
-                uint32_t b0[3], b1[3];
-                {
-                    if constexpr (!kv_quantised(FV)) {
-                        split<kBfV>(pr[0][0], pr[0][1], b0);
-                        split<kBfV>(pr[1][0], pr[1][1], b1);
-                    }
+                for (int t = 0; t < S; ++t) {
+                    uint32_t b0[3], b1[3];
+                    if constexpr (kv_quantised(FV)) {
+                        const uint32_t d0 = dv[t][p][0], d1 = dv[t][p][1];
+                        b0[0] = hmul2(w0[t][0], d0);
+                        b1[0] = hmul2(w1[t][0], d1);
+                        b0[1] = hfma2(w0[t][1], d0, hfms2(w0[t][0], d0, b0[0]));
+                        b1[1] = hfma2(w1[t][1], d1, hfms2(w1[t][0], d1, b1[0]));
+                    } else {
 #pragma unroll
-                    for (int p = 0; p < kPlanesV; ++p) {
-                        if constexpr (kv_quantised(FV)) {
-                            const float2 d0 = unpack_f16(dv[t][p][0]), d1 = unpack_f16(dv[t][p][1]);
-                            const float2 w0 = unpack2(mul2(pack_f2(pr[0][0], pr[0][1]), pack_f2(d0.x, d0.y)));
-                            const float2 w1 = unpack2(mul2(pack_f2(pr[1][0], pr[1][1]), pack_f2(d1.x, d1.y)));
-                            split<false>(w0.x, w0.y, b0);
-                            split<false>(w1.x, w1.y, b1);
-                        }
-                        uint4 v[2];
-                        v_frag<FV>(sv + t * C::kSlotBytes, p, v_row, v);
-#pragma unroll
-                        for (int u = 0; u < kTilesPerPlane; ++u) {
-                            float4 acc = zero;
-                            if constexpr (kBfV) acc = mma<kBfV>(v[u], b0[2], b1[2], acc);
-                            acc = mma<kBfV>(v[u], b0[1], b1[1], acc);
-                            acc = mma<kBfV>(v[u], b0[0], b1[0], acc);
-                            uint64_t(&to)[2] = o[p * kTilesPerPlane + u];
-                            to[0] = add2(to[0], pack_f2(acc.x, acc.y));
-                            to[1] = add2(to[1], pack_f2(acc.z, acc.w));
+                        for (int k = 0; k < 3; ++k) {
+                            b0[k] = w0[t][k];
+                            b1[k] = w1[t][k];
                         }
                     }
+                    uint4 v[2];
+                    v_frag<FV>(sv + t * C::kSlotBytes, p, v_row, vk0, vk1, v);
+#pragma unroll
+                    for (int u = 0; u < kTilesPerPlane; ++u) {
+                        if constexpr (kBfV) acc[u] = mma<kBfV>(v[u], b0[2], b1[2], acc[u]);
+                        acc[u] = mma<kBfV>(v[u], b0[1], b1[1], acc[u]);
+                        acc[u] = mma<kBfV>(v[u], b0[0], b1[0], acc[u]);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kTilesPerPlane; ++u) {
+                    uint64_t(&to)[2] = o[p * kTilesPerPlane + u];
+                    to[0] = add2(to[0], pack_f2(acc[u].x, acc[u].y));
+                    to[1] = add2(to[1], pack_f2(acc[u].z, acc[u].w));
                 }
             }
             refill();
@@ -679,11 +716,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
         while (dead && flying > 0) await();
 
         // ---- the warps' results joined ----
-        l += __shfl_xor_sync(~0u, l, 1);
-        l += __shfl_xor_sync(~0u, l, 2);
+        const float2 l2 = unpack2(l);
+        float total_l = l2.x + l2.y;
+        total_l += __shfl_xor_sync(~0u, total_l, 1);
+        total_l += __shfl_xor_sync(~0u, total_l, 2);
         if (j == 0) {
             state_m[warp * kRows + g] = ref == -FLT_MAX ? -INFINITY : ref;
-            state_l[warp * kRows + g] = l;
+            state_l[warp * kRows + g] = total_l;
         }
         float *merge = reinterpret_cast<float *>(ring_ptr);  // this warp's ring, all of it taken
         if (mine > 0) {
