@@ -447,6 +447,30 @@ def qmm_attend_workspace_bytes(args: qmm_attend_args) -> int:
     return load().qmm_attend_workspace_bytes(ctypes.byref(args))
 
 
+_torch_mod = None
+
+
+def _torch():
+    """torch, imported on first use (the C-named calls above work without it)."""
+    global _torch_mod
+    if _torch_mod is None:
+        import torch
+        _torch_mod = torch
+    return _torch_mod
+
+
+def _stream_of(stream, tensor):
+    """The raw handle of `stream`, or of torch's current stream on the tensor's device."""
+    if stream is not None:
+        return _stream(stream)
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a tenth of current_stream's time
+    index = tensor.device.index
+    if raw is not None and index is not None:
+        return raw(index)
+    return torch.cuda.current_stream(tensor.device).cuda_stream
+
+
 class KvCache:
     """A pool of cache pages: `pages` is a uint8 CUDA tensor [n_pages, page bytes]
     (one page holds page_size positions of every kv head), the formats are
@@ -463,6 +487,12 @@ class KvCache:
                 or pages.element_size() != 1:
             raise ValueError(f"pages must be contiguous bytes [n_pages, {self.page_bytes}], "
                              f"got {tuple(pages.shape)}")
+        # each call starts from a copy of its arguments with the pool filled in
+        pool = qmm_kv_cache(self.fmt_k, self.fmt_v, pages.data_ptr(), pages.numel(), pages.shape[0],
+                            page_size, n_kv_heads, head_dim)
+        self._append = qmm_kv_append_args(cache=pool)
+        self._read = qmm_kv_read_args(cache=pool)
+        self._attend = qmm_attend_args(cache=pool)
 
     @classmethod
     def empty(cls, fmt_k, fmt_v, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
@@ -475,33 +505,41 @@ class KvCache:
         pages = torch.empty((n_pages, size), dtype=torch.uint8, device=device)
         return cls(fmt_k, fmt_v, pages, page_size, n_kv_heads, head_dim)
 
-    def view(self, page_table, lens) -> qmm_kv_cache:
-        """The C description of this pool with a call's int32 page_table
-        [n_seqs, max_pages] (rows may be strided) and lens [n_seqs]."""
-        if page_table.dim() != 2 or page_table.shape[0] != lens.shape[0] \
-                or page_table.element_size() != 4 or lens.element_size() != 4 or lens.dim() != 1 \
-                or page_table.is_floating_point() or lens.is_floating_point():
+    def _args(self, template, page_table, lens):
+        """A call's arguments with its int32 page_table [n_seqs, max_pages] (rows may be strided)
+        and lens [n_seqs], and n_seqs."""
+        int32 = _torch().int32
+        shape, count = page_table.shape, lens.shape
+        if len(shape) != 2 or len(count) != 1 or shape[0] != count[0] \
+                or page_table.dtype is not int32 or lens.dtype is not int32:
             raise ValueError("page_table and lens must be int32 [n_seqs, max_pages] and [n_seqs]")
-        n_seqs, max_pages = page_table.shape
-        if (max_pages > 1 and page_table.stride(1) != 1) or (n_seqs > 1 and lens.stride(0) != 1):
+        n_seqs, max_pages = shape
+        stride = page_table.stride()
+        if (max_pages > 1 and stride[1] != 1) or (n_seqs > 1 and lens.stride()[0] != 1):
             raise ValueError("entries of page_table's rows and of lens must be adjacent")
-        return qmm_kv_cache(self.fmt_k, self.fmt_v, self.pages.data_ptr(), self.pages.numel(),
-                            self.pages.shape[0], self.page_size, self.n_kv_heads, self.head_dim,
-                            page_table.data_ptr(),
-                            page_table.stride(0) if n_seqs > 1 else max_pages, max_pages,
-                            lens.data_ptr(), n_seqs)
+        a = type(template).from_buffer_copy(template)
+        c = a.cache
+        c.page_table = page_table.data_ptr()
+        c.table_stride = stride[0] if n_seqs > 1 else max_pages
+        c.max_pages = max_pages
+        c.lens = lens.data_ptr()
+        c.n_seqs = n_seqs
+        return a, n_seqs
+
+    def view(self, page_table, lens) -> qmm_kv_cache:
+        """The C description of this pool with a call's page_table and lens."""
+        return self._args(self._read, page_table, lens)[0].cache
 
     def rows(self, name, t, n_seqs: int):
         """Row stride of fp32 rows [n_seqs, n_new, heads, head_dim] and their n_new and heads."""
-        if t.dim() != 4 or t.shape[0] != n_seqs or t.shape[3] != self.head_dim \
-                or t.element_size() != 4 or not t.is_floating_point():
-            raise ValueError(f"{name} must be float32 [{n_seqs}, n_new, heads, {self.head_dim}], "
-                             f"got {tuple(t.shape)}")
+        shape, dim = t.shape, self.head_dim
+        if len(shape) != 4 or shape[0] != n_seqs or shape[3] != dim or t.dtype is not _torch().float32:
+            raise ValueError(f"{name} must be float32 [{n_seqs}, n_new, heads, {dim}], "
+                             f"got {tuple(shape)}")
         s0, s1, s2, s3 = t.stride()
-        n_new, heads = t.shape[1], t.shape[2]
-        row = s1 if n_new > 1 else s0 if n_seqs > 1 else heads * self.head_dim
-        if s3 != 1 or (heads > 1 and s2 != self.head_dim) or \
-                (n_new > 1 and n_seqs > 1 and s0 != n_new * s1):
+        n_new, heads = shape[1], shape[2]
+        row = s1 if n_new > 1 else s0 if n_seqs > 1 else heads * dim
+        if s3 != 1 or (heads > 1 and s2 != dim) or (n_new > 1 and n_seqs > 1 and s0 != n_new * s1):
             raise ValueError(f"{name}: the heads of a row must be adjacent and rows equally spaced")
         return row, n_new, heads
 
@@ -521,30 +559,29 @@ def kv_append(cache: KvCache, k, v, page_table, lens, *, q=None, q_out=None, rop
     n_new of each sequence's lens positions; with `rope` (see rope_table) k is
     rotated, and q [n_seqs, n_new, n_heads, head_dim] into q_out (returned; a
     new tensor when not given)."""
-    import torch
-    c = cache.view(page_table, lens)
-    ks, n_new, heads = cache.rows("k", k, c.n_seqs)
-    vs = cache.rows("v", v, c.n_seqs)
-    if heads != cache.n_kv_heads or vs[1:] != (n_new, heads):
+    a, n_seqs = cache._args(cache._append, page_table, lens)
+    a.k_stride, n_new, heads = cache.rows("k", k, n_seqs)
+    a.v_stride, v_new, v_heads = cache.rows("v", v, n_seqs)
+    if heads != cache.n_kv_heads or v_new != n_new or v_heads != heads:
         raise ValueError(f"k and v must have {cache.n_kv_heads} heads and the same rows")
-    qs = qos = n_heads = 0
+    a.n_new, a.k, a.v = n_new, k.data_ptr(), v.data_ptr()
     if q is not None:
-        qs, q_new, n_heads = cache.rows("q", q, c.n_seqs)
+        a.q_stride, q_new, a.n_heads = cache.rows("q", q, n_seqs)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-        qos, o_new, o_heads = cache.rows("q_out", q_out, c.n_seqs)
-        if q_new != n_new or o_new != n_new or o_heads != n_heads:
+            q_out = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
+        a.q_out_stride, o_new, o_heads = cache.rows("q_out", q_out, n_seqs)
+        if q_new != n_new or o_new != n_new or o_heads != a.n_heads:
             raise ValueError("q and q_out must have k's rows and the same heads")
-    rope_len = n_rot = 0
+        a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
     if rope is not None:
-        if rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous() \
-                or rope.dtype != torch.float32:
+        shape = rope.shape
+        if len(shape) != 3 or shape[2] != 2 or not rope.is_contiguous() \
+                or rope.dtype is not _torch().float32:
             raise ValueError("rope must be contiguous float32 [positions, n_rot / 2, 2]")
-        rope_len, n_rot = rope.shape[0], 2 * rope.shape[1]
-    style = ROPE_STYLES[rope_style] if isinstance(rope_style, str) else int(rope_style)
-    qmm_kv_append(qmm_kv_append_args(
-        c, n_new, k.data_ptr(), v.data_ptr(), ks, vs[0], _ptr(q), _ptr(q_out) if n_heads else None,
-        qs, qos, n_heads, _ptr(rope), rope_len, n_rot, style, _stream(stream), 0))
+        a.rope, a.rope_len, a.n_rot = rope.data_ptr(), shape[0], 2 * shape[1]
+    a.rope_style = ROPE_STYLES[rope_style] if isinstance(rope_style, str) else int(rope_style)
+    a.stream = _stream_of(stream, cache.pages)
+    qmm_kv_append(a)
     return q_out
 
 
@@ -553,16 +590,20 @@ def kv_read(cache: KvCache, page_table, lens, count: int, *, first=None, k=None,
     """fp32 k and v [n_seqs, count, n_kv_heads, head_dim] of the positions
     first .. first + count - 1 of every sequence (first None: its last `count`
     positions); zeros where a sequence has no such position."""
-    import torch
-    c = cache.view(page_table, lens)
-    shape = (c.n_seqs, count, cache.n_kv_heads, cache.head_dim)
-    k = torch.empty(shape, dtype=torch.float32, device=cache.pages.device) if k is None else k
-    v = torch.empty(shape, dtype=torch.float32, device=cache.pages.device) if v is None else v
-    for name, t in (("k", k), ("v", v)):
-        if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != torch.float32:
+    a, n_seqs = cache._args(cache._read, page_table, lens)
+    shape = (n_seqs, count, cache.n_kv_heads, cache.head_dim)
+    a.first, a.count = -1 if first is None else first, count
+    given, torch = (("k", k), ("v", v)), _torch()
+    for name, t in given:
+        if t is not None and (t.shape != shape or not t.is_contiguous() or t.dtype is not torch.float32):
             raise ValueError(f"{name} must be contiguous float32 {shape}")
-    qmm_kv_read(qmm_kv_read_args(c, -1 if first is None else first, count, k.data_ptr(),
-                                 v.data_ptr(), _stream(stream), 0))
+    if k is None:
+        k = torch.empty(shape, dtype=torch.float32, device=cache.pages.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.float32, device=cache.pages.device)
+    a.k, a.v = k.data_ptr(), v.data_ptr()
+    a.stream = _stream_of(stream, cache.pages)
+    qmm_kv_read(a)
     return k, v
 
 
@@ -574,24 +615,26 @@ def attend(cache: KvCache, q, page_table, lens, *, scale=None, window=0, out=Non
     the number of last positions that a row sees. Returns out, shaped like q
     (the given one when passed). Scratch is `workspace` (uint8) when given,
     else a torch allocation."""
-    import torch
-    c = cache.view(page_table, lens)
-    qs, n_new, n_heads = cache.rows("q", q, c.n_seqs)
+    a, n_seqs = cache._args(cache._attend, page_table, lens)
+    a.q_stride, n_new, n_heads = cache.rows("q", q, n_seqs)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    os_, o_new, o_heads = cache.rows("out", out, c.n_seqs)
-    if (o_new, o_heads) != (n_new, n_heads):
+        out = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
+    a.out_stride, o_new, o_heads = cache.rows("out", out, n_seqs)
+    if o_new != n_new or o_heads != n_heads:
         raise ValueError("out must have q's shape")
-    a = qmm_attend_args(c, n_new, n_heads, q.data_ptr(), out.data_ptr(), qs, os_,
-                        cache.head_dim ** -0.5 if scale is None else scale, window, None, 0,
-                        _stream(stream), 0)
+    a.n_new, a.n_heads, a.q, a.out = n_new, n_heads, q.data_ptr(), out.data_ptr()
+    a.scale = cache.head_dim ** -0.5 if scale is None else scale
+    a.window = window
+    a.stream = _stream_of(stream, cache.pages)
     ws = None
     if workspace is None:
         need = qmm_attend_workspace_bytes(a)
         if need:
+            torch = _torch()
             ws = workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     if workspace is not None:
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
     qmm_attend(a)
-    _keep_until_done(ws, stream)
+    if stream is not None:
+        _keep_until_done(ws, stream)
     return out
