@@ -196,8 +196,10 @@ __device__ __forceinline__ uint32_t bytes_f16(uint32_t w, uint32_t k0) {
 // 0x64006400, k1: 1/16 twice.
 template <int SH>
 __device__ __forceinline__ uint32_t nibbles_f16(uint32_t w, uint32_t k0, uint32_t k1) {
-    if constexpr (SH == 0) return hsub2((w & 0x000f000fu) | k0, 0x64086408u);
-    else return hfma2((w & 0x00f000f0u) | k0, k1, 0xd480d480u);
+    uint32_t r;  // (w & mask) | k0
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "n"(SH == 0 ? 0x000f000f : 0x00f000f0), "r"(k0));
+    if constexpr (SH == 0) return hsub2(r, 0x64086408u);
+    else return hfma2(r, k1, 0xd480d480u);
 }
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -372,11 +374,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
         bool half_v = false;
         const uint8_t *src = nullptr;            // of lane l: strip l of the current 32 of this warp
         uint32_t have = 0;                       // which of them exist
+        int length = 1;                          // strips that this lane copies at once
         auto issue = [&]() {
             if ((strip & 31) == 0 && !half_v) {
                 const int at = it.begin + S * warp + (strip + lane) / S * S * kWarps + lane % S;
                 src = at < it.end ? kv_strip(c, it.seq, it.head, it.first + at) : nullptr;
                 have = __ballot_sync(~0u, src != nullptr);
+                if constexpr (C::kUnits == 1) {
+                    // strips of a run that lie one after the other are one copy,
+                    // made by the first one's lane
+                    const uint64_t before = __shfl_up_sync(~0u, (uint64_t)src, 1);
+                    const uint32_t joined = __ballot_sync(
+                        ~0u, lane % S != 0 && src && (uint64_t)src == before + C::kSlotBytes);
+                    const uint32_t after = joined >> lane >> 1;  // the strips that follow this one
+                    length = joined >> lane & 1 ? 0 : __ffs(~after);
+                }
             }
             const uint32_t bytes = C::kUnits == 1 ? C::kBytesK + C::kBytesV : half_v ? C::kBytesV : C::kBytesK;
             const uint32_t bar = bar0 + 8 * fill, t = lane - (strip & 31);
@@ -386,8 +398,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                 mbar_arrive_expect_tx(bar, __popc(these) * bytes);
             }
             __syncwarp();
-            if (t < S && src)
-                bulk_g2s(ring + (fill * S + t) * C::kSlotBytes, half_v ? src + C::kBytesK : src, bytes, bar);
+            if (t < S && src && length > 0)
+                bulk_g2s(ring + (fill * S + t) * C::kSlotBytes, half_v ? src + C::kBytesK : src, length * bytes,
+                         bar);
             if (C::kUnits == 1 || half_v) strip += S;
             if (C::kUnits == 2) half_v = !half_v;
             if (++fill == C::kGroups) fill = 0;

@@ -15,6 +15,7 @@ struct KvAppend {
     int64_t k_stride, v_stride, q_stride, q_out_stride;
     int64_t n_new, rope_len;
     int n_heads, n_rot, style;  // n_heads 0: no q
+    int teams;                  // of lanes per row; set by launch_kv_append
     bool vec;                   // every row starts on a 16-byte boundary
 };
 cudaError_t launch_kv_append(const KvAppend &a, const DeviceInfo &dev, cudaStream_t s);
