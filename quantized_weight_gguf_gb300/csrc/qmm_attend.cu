@@ -68,6 +68,10 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendParam
 
 namespace {
 
+int cost_of(const Attend &a) {
+    return item_cost_of(a.c.fmt_k, a.c.fmt_v, a.c.dim, shape_of(a.c.fmt_k, a.c.fmt_v, a.c.dim).ctas);
+}
+
 // CTAs of a launch: one resident wave, or fewer when even the longest rows
 // that the tables can hold make less work than that.
 int grid_of(const Attend &a, const DeviceInfo &dev) {
@@ -78,7 +82,7 @@ int grid_of(const Attend &a, const DeviceInfo &dev) {
     const int64_t subs = (a.n_heads / a.c.n_kv + kRows - 1) / kRows;
     const int64_t items = (int64_t)a.c.n_seqs * a.n_new * a.c.n_kv * subs;
     if (items >= wave) return wave;  // also keeps the product in range
-    const int64_t shares = (items * (strips + kItemCost) + kMinShare - 1) / kMinShare;
+    const int64_t shares = (items * (strips + cost_of(a)) + kMinShare - 1) / kMinShare;
     return shares < wave ? (int)shares : wave;
 }
 
@@ -117,6 +121,7 @@ cudaError_t launch_attend(const Attend &a, const DeviceInfo &dev, cudaStream_t s
     p.subs = (p.group + attend::kRows - 1) / attend::kRows;
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
     p.vec = a.vec;
+    p.item_cost = attend::cost_of(a);
     cudaError_t e;
     if (a.c.fmt_k == F_F16) e = attend::launch_f16(p, grid, s);
     else if (a.c.fmt_k == F_BF16) e = attend::launch_bf16(p, grid, s);

@@ -44,17 +44,26 @@ __host__ __device__ constexpr Shape shape_for(int fk, int fv, int dim, int ctas)
     s.smem = kFixedBytes + s.q_bytes + kWarps * s.ring_bytes;
     return s;
 }
-// Four CTAs of 128 threads per SM up to 128 dims (128 registers a thread),
-// three above (168); fewer where their rings would have less than two slots.
+// CTAs of 128 threads per SM: four up to 64 dims (128 registers a thread),
+// three above (168; with four at 96 and 128 dims 64 F16 sequences took 186 us
+// instead of 183, 48 Q8_0 ones 67 instead of 65); fewer where their rings would
+// have less than two slots.
 __host__ __device__ constexpr Shape shape_of(int fk, int fv, int dim) {
-    int ctas = dim <= 128 ? 4 : 3;
+    int ctas = dim <= 64 ? 4 : 3;
     while (ctas > 1 && shape_for(fk, fv, dim, ctas).slots < 2) --ctas;
     return shape_for(fk, fv, dim, ctas);
 }
 
-// What an item costs beside its strips, in strips: its query rows are
-// loaded and converted, and the warps' results joined.
-constexpr int kItemCost = 4;
+// What an item costs a CTA beside its strips, in strips: first copies on their
+// way, query rows converted, the warps' results joined; about 5 us, where a
+// strip takes the CTA its share of an SM's 45 GB/s (at least 0.25 us: the
+// arithmetic on a strip of Q4_0). With 4 strips for every format, CTAs with
+// several items finished 6 us (of 63) after the others on 48 ragged sequences.
+__host__ __device__ constexpr int item_cost_of(int fk, int fv, int dim, int ctas) {
+    const int ns = kv_strip_bytes(fk, fv, dim) * ctas / 45;
+    return 5000 / (ns > 250 ? ns : 250);
+}
+
 // Strips (and item costs) below which a CTA's share is not cut further: two
 // strips per warp.
 constexpr int kMinShare = 8;
@@ -77,6 +86,7 @@ struct AttendParams {
     int64_t q_stride, out_stride, window;
     int rows;                // n_seqs * n_new
     int n_new, group, subs;  // query heads per kv head, and items that they make
+    int item_cost;           // see item_cost_of
     float scale_log2;  // scale * log2(e)
     bool vec;
 };
@@ -110,6 +120,9 @@ __device__ __forceinline__ RowRange row_range(const AttendParams &a, int r) {
 // An item of no strips counts as one that holds nothing, so that its output
 // is written like any other.
 __device__ __forceinline__ int item_strips(const RowRange &x) { return x.strips > 0 ? x.strips : 1; }
+__device__ __forceinline__ int item_weight(const AttendParams &a, const RowRange &x) {
+    return x.strips > 0 ? x.strips + a.item_cost : 1 + a.item_cost / 4;
+}
 
 // Where a CTA's share begins.
 struct WorkSearch {
@@ -125,6 +138,12 @@ struct Work {
     int64_t base;        // and where that begins
 };
 
+// a / b of non-negative numbers; a 64-bit division takes an order of magnitude
+// longer than a 32-bit one, and nearly all numbers here fit
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+    return a >> 32 ? a / b : (int64_t)((unsigned)a / (unsigned)b);
+}
+
 // The share of CTA `cta`; false when it has none. Every thread of the block
 // calls it. The rows' weights are summed by the block's threads, a run of
 // rows each: a few loads for a decoding batch.
@@ -134,7 +153,7 @@ __device__ __forceinline__ bool find_work(const AttendParams &a, int cta, WorkSe
     const int r0 = min(tid * per, a.rows), r1 = min(r0 + per, a.rows);
     const int64_t items = (int64_t)a.c.n_kv * a.subs;
     int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) mine += item_strips(row_range(a, r)) + kItemCost;
+    for (int r = r0; r < r1; ++r) mine += item_weight(a, row_range(a, r));
     mine *= items;
     int64_t upto = mine;  // inclusive sums over the warp, then over the warps
 #pragma unroll
@@ -153,12 +172,12 @@ __device__ __forceinline__ bool find_work(const AttendParams &a, int cta, WorkSe
     const int64_t most = (total + kMinShare - 1) / kMinShare;
     w.shares = most < (int64_t)gridDim.x ? (int)most : (int)gridDim.x;
     if (cta >= w.shares) return false;
-    w.at = (int64_t)cta * total / w.shares;
-    w.end = (int64_t)(cta + 1) * total / w.shares;
+    w.at = quotient((int64_t)cta * total, w.shares);
+    w.end = quotient((int64_t)(cta + 1) * total, w.shares);
     int64_t base = before + upto - mine;
     if (w.at >= base && w.at < base + mine) {
         for (int r = r0; r < r1; ++r) {
-            const int64_t n = (item_strips(row_range(a, r)) + kItemCost) * items;
+            const int64_t n = item_weight(a, row_range(a, r)) * items;
             if (w.at < base + n) {
                 sh->row = r;
                 sh->base = base;
@@ -175,7 +194,13 @@ __device__ __forceinline__ bool find_work(const AttendParams &a, int cta, WorkSe
 
 // The CTA whose share holds position v of the strips laid end to end.
 __device__ __forceinline__ int share_of(const Work &w, int64_t v) {
-    return (int)(((v + 1) * w.shares + w.total - 1) / w.total) - 1;
+    // the last c with c total < (v + 1) shares, from an estimate that is off by
+    // one at most (shares < 2^11)
+    const int64_t limit = (v + 1) * w.shares;
+    int c = (int)((float)limit / (float)w.total);
+    while (c * w.total >= limit) --c;
+    while ((c + 1) * w.total < limit) ++c;
+    return c;
 }
 
 // The next item of a share: which rows and heads, which positions, and the
@@ -192,14 +217,14 @@ struct Item {
 __device__ __forceinline__ bool next_item(const AttendParams &a, Work &w, Item &it) {
     while (w.at < w.end) {
         const RowRange x = row_range(a, w.row);
-        const int n = item_strips(x), cost = n + kItemCost;
+        const int n = item_strips(x), cost = item_weight(a, x);
         const int64_t all = (int64_t)cost * a.c.n_kv * a.subs;
         if (w.at >= w.base + all) {
             w.base += all;
             ++w.row;
             continue;
         }
-        const int k = (int)((w.at - w.base) / cost);
+        const int k = (int)quotient(w.at - w.base, cost);
         it.base = w.base + (int64_t)k * cost;
         const int64_t stop = it.base + cost < w.end ? it.base + cost : w.end;
         it.begin = (int)(w.at - it.base);
