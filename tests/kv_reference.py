@@ -51,7 +51,12 @@ def pack(x, fmt):
 
 
 def unpack(codes, d, fmt):
-    """Values [.., dim] in 64 bits."""
+    """Values [.., dim] in 64 bits (any bytes, NaN and Inf among them)."""
+    with np.errstate(invalid="ignore"):
+        return _unpack(codes, d, fmt)
+
+
+def _unpack(codes, d, fmt):
     if fmt == "f16":
         return codes.view(np.float16).astype(np.float64)
     if fmt == "bf16":
