@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendParam
             s.w = s.w * fa + so.w * fb;
             m = top;
         }
-        if (f < f1 && l == 0 && row < x.heads) put_out(a, x.row, x.head0 + row, d, dim, s, total);
+        if (f < f1 && l == 0) put_out<true>(a, x, row, d, dim, s, total);
     }
 }
 
@@ -72,15 +72,17 @@ int cost_of(const Attend &a) {
     return item_cost_of(a.c.fmt_k, a.c.fmt_v, a.c.dim, shape_of(a.c.fmt_k, a.c.fmt_v, a.c.dim).ctas);
 }
 
+// Tiles of a sequence and kv head; n_new * group is below 2^31.
+int tiles_of(const Attend &a) { return (int)((a.n_new * (a.n_heads / a.c.n_kv) + kRows - 1) / kRows); }
+
 // CTAs of a launch: one resident wave, or fewer when even the longest rows
 // that the tables can hold make less work than that.
 int grid_of(const Attend &a, const DeviceInfo &dev) {
     const int wave = dev.sm_count * shape_of(a.c.fmt_k, a.c.fmt_v, a.c.dim).ctas;
     int64_t most = a.c.capacity;
-    if (a.window && a.window < most) most = a.window + kStrip - 1;
+    if (a.window && a.window < most) most = a.window + kRows + kStrip - 1;  // of a tile's rows
     const int64_t strips = (most + kStrip - 1) / kStrip + 1;
-    const int64_t subs = (a.n_heads / a.c.n_kv + kRows - 1) / kRows;
-    const int64_t items = (int64_t)a.c.n_seqs * a.n_new * a.c.n_kv * subs;
+    const int64_t items = (int64_t)a.c.n_seqs * tiles_of(a) * a.c.n_kv;
     if (items >= wave) return wave;  // also keeps the product in range
     const int64_t shares = (items * (strips + cost_of(a)) + kMinShare - 1) / kMinShare;
     return shares < wave ? (int)shares : wave;
@@ -115,10 +117,10 @@ cudaError_t launch_attend(const Attend &a, const DeviceInfo &dev, cudaStream_t s
     p.q_stride = a.q_stride;
     p.out_stride = a.out_stride;
     p.window = a.window;
-    p.rows = (int)(a.c.n_seqs * a.n_new);
     p.n_new = (int)a.n_new;
     p.group = a.n_heads / a.c.n_kv;
-    p.subs = (p.group + attend::kRows - 1) / attend::kRows;
+    p.tiles = attend::tiles_of(a);
+    p.all_tiles = a.c.n_seqs * p.tiles;
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
     p.vec = a.vec;
     p.item_cost = attend::cost_of(a);

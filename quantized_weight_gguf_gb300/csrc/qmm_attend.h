@@ -12,7 +12,7 @@ namespace attend {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 8;            // query heads of an item
+constexpr int kRows = 8;            // query rows of an item
 constexpr int kFixedBytes = 1024;   // barriers, flags, states (see attend_kernel)
 
 // How the shared memory of an SM (228 KB, of which the system takes 1 KB per
@@ -73,8 +73,7 @@ constexpr int kMinShare = 8;
 struct Join {
     int parts;   // 0: none
     int first;
-    int head0, heads;
-    int64_t row;
+    int seq, head, tile;
 };
 
 struct AttendParams {
@@ -84,8 +83,8 @@ struct AttendParams {
     float *parts;      // [2 grid][part_floats]: results of a share's first (0) and last (1) item
     Join *joins;       // [grid]
     int64_t q_stride, out_stride, window;
-    int rows;                // n_seqs * n_new
-    int n_new, group, subs;  // query heads per kv head, and items that they make
+    int n_new, group;        // new positions per sequence, query heads per kv head
+    int tiles, all_tiles;    // kRows of the n_new x group query rows of a sequence and kv head; of all sequences
     int item_cost;           // see item_cost_of
     float scale_log2;  // scale * log2(e)
     bool vec;
@@ -94,33 +93,53 @@ struct AttendParams {
 // a partial result: [kRows] maxima, [kRows] totals, [kRows][dim] sums
 __host__ __device__ constexpr int part_floats(int dim) { return kRows * (dim + 2); }
 
-// The positions [lo, hi) that row r = s * n_new + i sees, its sequence and strips.
-struct RowRange {
-    int seq, lo, hi, first, strips;
+// The positions [lo, hi) that the row of position pos sees.
+struct Range {
+    int lo, hi;
 };
-__device__ __forceinline__ RowRange row_range(const AttendParams &a, int r) {
-    RowRange x;
-    x.seq = a.n_new == 1 ? r : r / a.n_new;
+__device__ __forceinline__ Range seen_from(const AttendParams &a, int64_t pos) {
+    const int64_t hi = pos + 1 < a.c.capacity ? pos + 1 : a.c.capacity;
+    const int64_t lo = a.window && pos + 1 > a.window ? pos + 1 - a.window : 0;
+    Range x;
+    x.lo = hi > lo ? (int)lo : 0;
+    x.hi = hi > lo ? (int)hi : 0;
+    return x;
+}
+
+// Query row x of a sequence and kv head is new position x / group and head
+// x % group of the kv head's; x past the last counts as the last. MANY: there
+// are several new positions (see launch_one).
+template <bool MANY>
+__device__ __forceinline__ int new_of(const AttendParams &a, int x) {
+    return MANY ? min(x / a.group, a.n_new - 1) : 0;
+}
+
+// Tile r of all sequences' tiles: its sequence, the positions that one of its
+// rows sees, and their strips. pos0: the sequence's first new position.
+struct TileRange {
+    int seq, tile, lo, hi, first, strips;
+    int64_t pos0;
+};
+template <bool MANY>
+__device__ __forceinline__ TileRange tile_range(const AttendParams &a, int r) {
+    TileRange x;
+    x.seq = a.tiles == 1 ? r : r / a.tiles;
+    x.tile = r - x.seq * a.tiles;
     const int held = __ldg(a.c.lens + x.seq);
-    const int64_t pos = (int64_t)(held < 0 ? 0 : held) - a.n_new + (r - x.seq * a.n_new);
-    int64_t hi = pos + 1;
-    if (hi > a.c.capacity) {
-        record_error(a.c.err, DERR_BAD_PAGE);
-        hi = a.c.capacity;
-    }
-    int64_t lo = a.window ? pos + 1 - a.window : 0;
-    if (lo < 0) lo = 0;
-    if (hi <= lo) lo = hi = 0;  // sees nothing
-    x.lo = (int)lo;
-    x.hi = (int)hi;
+    x.pos0 = (int64_t)(held < 0 ? 0 : held) - a.n_new;
+    const int64_t last = x.pos0 + new_of<MANY>(a, x.tile * kRows + kRows - 1);
+    if (last + 1 > a.c.capacity) record_error(a.c.err, DERR_BAD_PAGE);
+    const Range l = seen_from(a, last);
+    x.lo = MANY ? seen_from(a, x.pos0 + new_of<MANY>(a, x.tile * kRows)).lo : l.lo;  // 0 for padding
+    x.hi = l.hi;
     x.first = x.lo / kStrip;
-    x.strips = hi > lo ? (x.hi + kStrip - 1) / kStrip - x.first : 0;
+    x.strips = x.hi > x.lo ? (x.hi + kStrip - 1) / kStrip - x.first : 0;
     return x;
 }
 // An item of no strips counts as one that holds nothing, so that its output
 // is written like any other.
-__device__ __forceinline__ int item_strips(const RowRange &x) { return x.strips > 0 ? x.strips : 1; }
-__device__ __forceinline__ int item_weight(const AttendParams &a, const RowRange &x) {
+__device__ __forceinline__ int item_strips(const TileRange &x) { return x.strips > 0 ? x.strips : 1; }
+__device__ __forceinline__ int item_weight(const AttendParams &a, const TileRange &x) {
     return x.strips > 0 ? x.strips + a.item_cost : 1 + a.item_cost / 4;
 }
 
@@ -128,13 +147,13 @@ __device__ __forceinline__ int item_weight(const AttendParams &a, const RowRange
 struct WorkSearch {
     long long sum[kWarps];
     long long base;
-    int row;
+    int tile;
 };
 struct Work {
     int64_t at, end;     // the share, in strips and item costs of all items end to end
     int64_t total;
     int shares;          // CTAs that have one
-    int row;             // the row that `at` is in
+    int tile;            // the tile of all sequences' that `at` is in
     int64_t base;        // and where that begins
 };
 
@@ -145,16 +164,16 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int b) {
 }
 
 // The share of CTA `cta`; false when it has none. Every thread of the block
-// calls it. The rows' weights are summed by the block's threads, a run of
-// rows each: a few loads for a decoding batch.
+// calls it. The tiles' weights are summed by the block's threads, a run of
+// tiles each: a few loads for a decoding batch.
+template <bool MANY>
 __device__ __forceinline__ bool find_work(const AttendParams &a, int cta, WorkSearch *sh, Work &w) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.rows + kThreads - 1) / kThreads;
-    const int r0 = min(tid * per, a.rows), r1 = min(r0 + per, a.rows);
-    const int64_t items = (int64_t)a.c.n_kv * a.subs;
+    const int per = (a.all_tiles + kThreads - 1) / kThreads;
+    const int r0 = min(tid * per, a.all_tiles), r1 = min(r0 + per, a.all_tiles);
     int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) mine += item_weight(a, row_range(a, r));
-    mine *= items;
+    for (int r = r0; r < r1; ++r) mine += item_weight(a, tile_range<MANY>(a, r));
+    mine *= a.c.n_kv;
     int64_t upto = mine;  // inclusive sums over the warp, then over the warps
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -177,9 +196,9 @@ __device__ __forceinline__ bool find_work(const AttendParams &a, int cta, WorkSe
     int64_t base = before + upto - mine;
     if (w.at >= base && w.at < base + mine) {
         for (int r = r0; r < r1; ++r) {
-            const int64_t n = item_weight(a, row_range(a, r)) * items;
+            const int64_t n = (int64_t)item_weight(a, tile_range<MANY>(a, r)) * a.c.n_kv;
             if (w.at < base + n) {
-                sh->row = r;
+                sh->tile = r;
                 sh->base = base;
                 break;
             }
@@ -187,7 +206,7 @@ __device__ __forceinline__ bool find_work(const AttendParams &a, int cta, WorkSe
         }
     }
     __syncthreads();
-    w.row = sh->row;
+    w.tile = sh->tile;
     w.base = sh->base;
     return true;
 }
@@ -203,25 +222,25 @@ __device__ __forceinline__ int share_of(const Work &w, int64_t v) {
     return c;
 }
 
-// The next item of a share: which rows and heads, which positions, and the
-// part [begin, end) of its strips that the share holds.
+// The next item of a share: which query rows, which positions, and the part
+// [begin, end) of its strips that the share holds.
 struct Item {
-    int64_t row;
     int64_t base;        // where its strips begin
-    int seq, head;       // sequence, kv head
-    int head0, heads;    // query heads
-    int lo, hi, first;   // positions seen, first strip
+    int64_t pos0;        // the sequence's first new position
+    int seq, head, tile; // sequence, kv head, tile of its query rows
+    int lo, hi, first;   // positions that one of the rows sees, first strip
     int strips, begin, end;
     bool live;           // has strips at all
 };
+template <bool MANY>
 __device__ __forceinline__ bool next_item(const AttendParams &a, Work &w, Item &it) {
     while (w.at < w.end) {
-        const RowRange x = row_range(a, w.row);
+        const TileRange x = tile_range<MANY>(a, w.tile);
         const int n = item_strips(x), cost = item_weight(a, x);
-        const int64_t all = (int64_t)cost * a.c.n_kv * a.subs;
+        const int64_t all = (int64_t)cost * a.c.n_kv;
         if (w.at >= w.base + all) {
             w.base += all;
-            ++w.row;
+            ++w.tile;
             continue;
         }
         const int k = (int)quotient(w.at - w.base, cost);
@@ -231,12 +250,10 @@ __device__ __forceinline__ bool next_item(const AttendParams &a, Work &w, Item &
         it.end = stop - it.base < n ? (int)(stop - it.base) : n;
         w.at = stop;
         if (it.begin >= it.end) continue;  // only of the item's cost
-        it.row = w.row;
+        it.pos0 = x.pos0;
         it.seq = x.seq;
-        it.head = k / a.subs;
-        const int sub = k - it.head * a.subs;
-        it.head0 = it.head * a.group + sub * kRows;
-        it.heads = a.group - sub * kRows < kRows ? a.group - sub * kRows : kRows;
+        it.head = k;
+        it.tile = x.tile;
         it.lo = x.lo;
         it.hi = x.hi;
         it.first = x.first;
@@ -251,16 +268,29 @@ __device__ __forceinline__ Join make_join(const AttendParams &, const Work &w, c
     Join x;
     x.first = share_of(w, it.base);
     x.parts = share_of(w, it.base + it.strips - 1) - x.first + 1;
-    x.head0 = it.head0;
-    x.heads = it.heads;
-    x.row = it.row;
+    x.seq = it.seq;
+    x.head = it.head;
+    x.tile = it.tile;
     return x;
 }
 
+// Row `row` of a tile (it: an item or a join): whether there is one, and its
+// offset among q's (or out's) rows of `stride` floats.
+template <bool MANY, class T>
+__device__ __forceinline__ bool row_offset(const AttendParams &a, const T &it, int row, int dim,
+                                           int64_t stride, int64_t &at) {
+    const int x = it.tile * kRows + row, i = new_of<MANY>(a, x);
+    at = ((int64_t)it.seq * a.n_new + i) * stride + ((int64_t)it.head * a.group + x - i * a.group) * dim;
+    return x < a.n_new * a.group;
+}
+
 // out = sum / total: 0 where nothing was seen.
-__device__ __forceinline__ void put_out(const AttendParams &a, int64_t row, int head, int d, int dim,
+template <bool MANY, class T>
+__device__ __forceinline__ void put_out(const AttendParams &a, const T &it, int row, int d, int dim,
                                         float4 sum, float total) {
-    float *o = a.out + row * a.out_stride + (int64_t)head * dim + d;
+    int64_t at;
+    if (!row_offset<MANY>(a, it, row, dim, a.out_stride, at)) return;
+    float *o = a.out + at + d;
     const float f = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
     const float4 v = make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f);
     if (a.vec) {

@@ -145,6 +145,54 @@ def test_nan_outside_a_rows_range_does_not_reach_it(fmt):
 
 
 @pytest.mark.parametrize("fmt", range(len(ref.FORMATS)))
+@pytest.mark.parametrize("n_heads,n_kv,n_new,window", [(1, 1, 8, 0), (2, 2, 11, 19), (12, 1, 2, 0), (5, 1, 7, 3),
+                                                       (6, 3, 33, 16)])
+def test_new_rows_that_share_an_item(fmt, n_heads, n_kv, n_new, window):
+    """Rows of several new positions are worked on together: each keeps its own range, and a NaN in
+    a position that only the later ones see stays with those."""
+    fk, fv = ref.FORMATS[fmt]
+    rng = np.random.default_rng(n_new + n_heads)
+    lens = [n_new + 40, n_new - 1, n_new + 3, 0]
+    table, host, cache = _setup(rng, fk, fv, lens, 16, n_kv, 96)
+    xq = rng.standard_normal((4, n_new, n_heads, 96)).astype(np.float32)
+    _check(host, cache, table, lens, xq, window=window)
+    bad = lens[0] - n_new // 2
+    x = torch.full((1, 1, n_kv, 96), np.nan, device=DEV)
+    q.kv_append(cache, x, x, _dev(table[:1]), _dev(np.array([bad + 1], np.int32)))
+    out = q.attend(cache, _dev(xq), _dev(table), _dev(np.array(lens, np.int32)), window=window).cpu().numpy()
+    k, v = host.values(0, table[0], lens[0]), host.values(1, table[0], lens[0])
+    for i in range(n_new):
+        last = lens[0] - n_new + i
+        first = max(0, last + 1 - window) if window else 0
+        if first <= bad <= last:
+            assert np.isnan(out[0, i]).all()
+        else:
+            want, tol = ref.attention(xq[0, i], k, v, first, last, np.float64(np.float32(96 ** -0.5)))
+            assert (np.abs(out[0, i] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", range(len(ref.FORMATS)))
+@pytest.mark.parametrize("n", [1, 17, 33, 65, 129, 600])
+def test_a_nan_that_is_seen_shows(fmt, n):
+    """A NaN at the last position alone, wherever that falls among the strips; a query row with a
+    NaN beside one without."""
+    fk, fv = ref.FORMATS[fmt]
+    rng = np.random.default_rng(n)
+    table, host, cache = _setup(rng, fk, fv, [n], 16, 1, 64)
+    xq = rng.standard_normal((1, 1, 3, 64)).astype(np.float32)
+    xq[0, 0, 1, 5] = np.nan
+    dt, dl = _dev(table), _dev(np.array([n], np.int32))
+    out = q.attend(cache, _dev(xq), dt, dl).cpu().numpy()[0, 0]
+    assert np.isnan(out[1]).all()
+    want, tol = ref.attention(xq[0, 0, ::2], host.values(0, table[0], n), host.values(1, table[0], n), 0,
+                              n - 1, np.float64(np.float32(0.125)))
+    assert (np.abs(out[::2] - want) <= tol).all()
+    x = torch.full((1, 1, 1, 64), np.nan, device=DEV)
+    q.kv_append(cache, x, torch.zeros_like(x), dt, dl)
+    assert np.isnan(q.attend(cache, _dev(xq), dt, dl).cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("fmt", range(len(ref.FORMATS)))
 @pytest.mark.parametrize("kind", ["peaked", "shifted", "large_q", "tiny_v", "large_v", "negative_scale"])
 def test_ranges_of_scores_and_values(fmt, kind):
     """Softmaxes with one heavy weight, a common offset of all scores (the maximum far from 0),
