@@ -509,8 +509,9 @@ typedef struct qmm_attend_args {
  * t over max(0, pos + 1 - window) .. pos of the row's position pos (the row's
  * own position included, so its k and v are appended first). A row that sees
  * no position gives zeros. Cache bytes outside the range, whatever they hold,
- * do not reach the result. Sums, the softmax's maximum and its total are fp32;
- * q and the weights enter the tensor cores as sums of 16-bit terms that keep
+ * do not reach the result; one that is Inf or NaN within the range makes the
+ * row's outputs Inf or NaN. Sums, the softmax's maximum and its total are
+ * fp32; q and the weights enter the tensor cores as sums of 16-bit terms that keep
  * at least 22 bits. The same call gives the same result each time. Scratch as
  * for qmm_matmul_ex (calls that can run concurrently pass their own). */
 int qmm_attend(const qmm_attend_args *a);

@@ -312,3 +312,32 @@ def test_an_appended_token_is_attended_to_in_stream_order_and_in_a_graph():
                                       host.values(1, table[s], n), 0, n - 1, np.float64(np.float32(dim ** -0.5)))
             assert (np.abs(out[s, 0].cpu().numpy() - want) <= tol).all()
     assert q.qmm_device_status() == 0
+
+
+def test_scratch_of_streams_and_of_a_capture():
+    """Without a given workspace: calls of different needs on several streams at once, and captured."""
+    rng = np.random.default_rng(9)
+    cases = []
+    for lens, n_heads, dim in (([3], 4, 64), ([5000, 70, 900], 16, 256), ([333] * 5, 8, 128)):
+        table, host, cache = _setup(rng, "q4_0", "q4_0", lens, 32, 2, dim)
+        xq = _dev(rng.standard_normal((len(lens), 1, n_heads, dim)).astype(np.float32))
+        dt, dl = _dev(table), _dev(np.array(lens, np.int32))
+        ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+        cases.append((cache, xq, dt, dl, q.attend(cache, xq, dt, dl, workspace=ws)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got += [(q.attend(*c[:4]), c[4]) for c in cases]
+            got += [(q.attend(*c[:4], stream=s), c[4]) for c in cases]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        got += [(q.attend(*c[:4]), c[4]) for c in cases]
+    for _ in range(3):
+        g.replay()
+        got += [(q.attend(*c[:4]), c[4]) for c in cases]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got)
