@@ -13,54 +13,70 @@ namespace attend {
 // divide its 8 x dim values evenly, so an item of many parts has as many
 // blocks. Threads take the parts in a fixed order: the sum is the same on
 // every call.
+constexpr int kBatch = 4;  // parts that a thread loads at once
 __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendParams a) {
     pdl_wait_prev();
     pdl_launch_dependents();
     const Join x = a.joins[blockIdx.x];
     if (x.parts < 2) return;
-    const int dim = a.c.dim, quads = kRows * dim / 4, blocks = x.parts - 1;
-    const int me = (int)blockIdx.x - x.first;
-    const int f0 = (int)((int64_t)me * quads / blocks), f1 = (int)((int64_t)(me + 1) * quads / blocks);
+    // values f0 .. f1 - 1 are this block's; all numbers here are far below 2^32
+    const unsigned dim = a.c.dim, quads = kRows * dim / 4, blocks = x.parts - 1, me = blockIdx.x - x.first;
+    const int f0 = (int)(me * quads / blocks), f1 = (int)((me + 1) * quads / blocks);
     if (f0 >= f1) return;
     // `wide` neighbouring lanes share a value and take its parts in turn
-    int wide = 1;
-    while (wide < 32 && 2 * wide * (f1 - f0) <= kThreads) wide *= 2;
-    const int l = threadIdx.x % wide;
-    for (int f = f0 + threadIdx.x / wide; f - (int)threadIdx.x / wide < f1; f += kThreads / wide) {
-        const int row = f / (dim / 4), d = (f - row * (dim / 4)) * 4;
+    int log_wide = 0;
+    while (log_wide < 5 && (f1 - f0) << (log_wide + 1) <= kThreads) ++log_wide;
+    const int wide = 1 << log_wide, l = threadIdx.x & (wide - 1), f_of = f0 + (int)(threadIdx.x >> log_wide);
+    for (int f = f_of; f - f_of + f0 < f1; f += kThreads >> log_wide) {
+        const int row = (unsigned)f / (dim / 4), d = (f - row * ((int)dim / 4)) * 4;
         float m = -INFINITY, total = 0.0f;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (f < f1) {
-#pragma unroll 4
-            for (int k = l; k < x.parts; k += wide) {
-                // the first part is its CTA's last item, the others their CTAs' first
-                const float *p = a.parts + (int64_t)(2 * (x.first + k) + (k == 0)) * part_floats(dim);
-                const float mk = p[row], lk = p[kRows + row];
-                const float4 v = *reinterpret_cast<const float4 *>(p + 2 * kRows + row * dim + d);
-                if (mk == -INFINITY) continue;
-                const float top = fmaxf(m, mk);
-                const float fo = exp2f(m - top), fn = exp2f(mk - top);
-                total = total * fo + lk * fn;
-                s.x = s.x * fo + v.x * fn;
-                s.y = s.y * fo + v.y * fn;
-                s.z = s.z * fo + v.z * fn;
-                s.w = s.w * fo + v.w * fn;
-                m = top;
+        for (int k0 = l; k0 < x.parts; k0 += kBatch * wide) {
+            float mk[kBatch], lk[kBatch];
+            float4 v[kBatch];
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int k = k0 + i * wide;
+                mk[i] = -INFINITY;
+                lk[i] = 0.0f;
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (f < f1 && k < x.parts) {
+                    // the first part is its CTA's last item, the others their CTAs' first
+                    const float *p = a.parts + (int64_t)(2 * (x.first + k) + (k == 0)) * part_floats(dim);
+                    mk[i] = p[row];
+                    lk[i] = p[kRows + row];
+                    v[i] = *reinterpret_cast<const float4 *>(p + 2 * kRows + row * dim + d);
+                }
             }
-        }
-        for (int o = 1; o < wide; o <<= 1) {
-            const float mo = __shfl_xor_sync(~0u, m, o), to = __shfl_xor_sync(~0u, total, o);
-            const float4 so = make_float4(__shfl_xor_sync(~0u, s.x, o), __shfl_xor_sync(~0u, s.y, o),
-                                          __shfl_xor_sync(~0u, s.z, o), __shfl_xor_sync(~0u, s.w, o));
-            const float top = fmaxf(m, mo);
-            const float fa = m == -INFINITY ? 0.0f : exp2f(m - top);
-            const float fb = mo == -INFINITY ? 0.0f : exp2f(mo - top);
-            total = total * fa + to * fb;
-            s.x = s.x * fa + so.x * fb;
-            s.y = s.y * fa + so.y * fb;
-            s.z = s.z * fa + so.z * fb;
-            s.w = s.w * fa + so.w * fb;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) top = fmaxf(top, mk[i]);
+            const float base = top == -INFINITY ? 0.0f : top;
+            const float fo = exp2f(m - base);
+            total *= fo;
+            s = make_float4(s.x * fo, s.y * fo, s.z * fo, s.w * fo);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float fn = exp2f(mk[i] - base);
+                total = fmaf(fn, lk[i], total);
+                s.x = fmaf(fn, v[i].x, s.x);
+                s.y = fmaf(fn, v[i].y, s.y);
+                s.z = fmaf(fn, v[i].z, s.z);
+                s.w = fmaf(fn, v[i].w, s.w);
+            }
             m = top;
+        }
+        float top = m;
+        for (int o = 1; o < wide; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        const float fo = m == -INFINITY ? 0.0f : exp2f(m - top);
+        total *= fo;
+        s = make_float4(s.x * fo, s.y * fo, s.z * fo, s.w * fo);
+        for (int o = 1; o < wide; o <<= 1) {
+            total += __shfl_xor_sync(~0u, total, o);
+            s.x += __shfl_xor_sync(~0u, s.x, o);
+            s.y += __shfl_xor_sync(~0u, s.y, o);
+            s.z += __shfl_xor_sync(~0u, s.z, o);
+            s.w += __shfl_xor_sync(~0u, s.w, o);
         }
         if (f < f1 && l == 0) put_out<true>(a, x, row, d, dim, s, total);
     }

@@ -12,8 +12,8 @@
 // joined by attend_join_kernel from partial results (maximum, total, weighted
 // sum).
 //
-// A CTA is kWarps warps that take an item's strips in turn, two at a time
-// where the ring has room. Each warp streams its strips through a ring of its
+// A CTA is kWarps warps that take an item's strips in turn, up to four at a
+// time where the ring has room. Each warp streams its strips through a ring of its
 // own in shared memory with bulk copies (one or two per strip, issued by one
 // lane, no barrier between warps) and keeps totals and weighted sums in
 // registers, fp32.
@@ -54,11 +54,12 @@
 // 131071 (285 MB) 56 us, 75 %, of which 6 us are the join and 4 the way to the
 // first strip (with the arithmetic left out the same copies take 49 us, without
 // the copies the arithmetic 47). 4-bit caches: the unpacking's integer and fp16
-// instructions, about 310 warp instructions for a strip of 64 dims (1152
-// bytes): 16 sequences with 16 kv heads (129 MB) take 50 us, 38 %, 45 of
-// them without any copy. Several new positions: the same instructions, shared
-// by up to eight query rows: 8 positions of 16 heads over 4-bit caches take
-// 19.5 us, where one position at a time took 78.
+// instructions, about 300 warp instructions for a strip of 64 dims (1152
+// bytes): 16 sequences with 16 kv heads (129 MB) take 46 us, 41 %; before
+// strips were taken four at a time 50, 45 of them with no copies at all.
+// Several new positions: the same instructions, shared by up to eight query
+// rows: 8 positions of 16 heads over 4-bit caches take 20 us, where one
+// position at a time took 78.
 #pragma once
 
 #include <cfloat>
@@ -901,7 +902,8 @@ cudaError_t launch_one(const AttendParams &a, int grid, cudaStream_t s) {
 
 // One new position per sequence (decoding) has a kernel without the rows'
 // separate ranges: 48 ragged Q8_0 sequences take 62.8 us with it and 64.8
-// without, 16 Q4_0 ones with 16 kv heads of 64 dims 50.0 and 51.5.
+// without, 16 Q4_0 ones with 16 kv heads of 64 dims (two strips at a time) 50.0
+// and 51.5.
 template <int FK, int FV, int D>
 cudaError_t launch_dim(const AttendParams &a, int grid, cudaStream_t s) {
     return a.n_new == 1 ? launch_one<FK, FV, D, false>(a, grid, s) : launch_one<FK, FV, D, true>(a, grid, s);
