@@ -6,9 +6,9 @@ a time.
       attention --(Q4_K product, added)--> x
 
 The norm is torch; the other steps are calls of the library: matmul, kv_append,
-attend, matmul. The
-decoding step is captured into a CUDA graph once and replayed per token; page
-table and lengths live on the device, so the graph does not change.
+attend, matmul. The decoding step is captured into a CUDA graph once and
+replayed per token; page table and lengths live on the device, so the graph does
+not change.
 
     python examples/attention_block.py [--tokens 64] [--cache q8_0]
 """

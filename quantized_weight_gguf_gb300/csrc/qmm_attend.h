@@ -1,6 +1,6 @@
 // qmm_attend.h -- parameters, work division and partial results of the
-// attention kernels (qmm_attend_kernel.cuh: a strip at a time; qmm_attend.cu:
-// the join of split items and the host side).
+// attention kernels (qmm_attend_kernel.cuh: the strips; qmm_attend.cu: the join of
+// split items and the host side).
 #pragma once
 
 #include "qmm_kv.cuh"

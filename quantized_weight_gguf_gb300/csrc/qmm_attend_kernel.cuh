@@ -25,12 +25,12 @@
 //    significant bits, after a power-of-two scale per row), a strip's 16
 //    positions are two n-tiles. A block's scale multiplies its fp32 sum.
 //  - O^T = V^T P^T: 16 dims are the rows of A, the eight query rows the columns
-//    of B. The weights p enter as two fp16 terms as well (two products into
-//    one accumulator). For quantised V a block's scale d is folded into the
-//    weight's terms first, w = p d = h + r: h = fl(p_h d), and with one fma
-//    each r = fl(p_r d + (p_h d - h)), where the bracket is exact. The product
-//    over the strips taken together starts from zero and is added to the
-//    running sums in fp32, so their rounding is to nearest.
+//    of B. The weights p enter as two fp16 terms as well (two products). For
+//    quantised V a block's scale d is folded into the weight's terms first,
+//    w = p d = h + r: h = fl(p_h d), and with one fma each
+//    r = fl(p_r d + (p_h d - h)), where the bracket is exact. The product over
+//    the strips taken together starts from zero and is added to the running
+//    sums in fp32, so their rounding is to nearest.
 //  - Integer codes enter as exact fp16 integers: the code with its offset
 //    under the exponent of 1024 (a byte permute or a mask), less 1024 and the
 //    offset. (Leaving the offset in, to be subtracted from the sums, or taking
@@ -49,17 +49,17 @@
 // weights that matter stay far from the fp16 terms' subnormal range.
 //
 // What bounds it (fractions are of a copy's 6.8 TB/s; device times in a graph).
-// 16-bit caches and long 8-bit ones: DRAM. 64 ragged F16 sequences of up to
-// 8190 positions (1.18 GB) take 183 us, 6.5 TB/s, 95 %; one Q8_0 sequence of
-// 131071 (285 MB) 56 us, 75 %, of which 6 us are the join and 4 the way to the
-// first strip (with the arithmetic left out the same copies take 49 us, without
-// the copies the arithmetic 47). 4-bit caches: the unpacking's integer and fp16
+// 16-bit caches and 8-bit ones: DRAM, and for short work the way to the first
+// strip (about 4 us: lengths, page table and strip wait for one another) and
+// the join (3 to 4 us). 64 ragged F16 sequences of up to 8190 positions (1.18 GB)
+// take 182 us, 6.5 TB/s, 96 %, with the arithmetic left out 177; one Q8_0
+// sequence of 131071 (285 MB) 52 us, 81 %, 49 without the arithmetic, 45
+// without the copies. 4-bit caches: the unpacking's integer and fp16
 // instructions, about 300 warp instructions for a strip of 64 dims (1152
-// bytes): 16 sequences with 16 kv heads (129 MB) take 46 us, 41 %; before
-// strips were taken four at a time 50, 45 of them with no copies at all.
-// Several new positions: the same instructions, shared by up to eight query
-// rows: 8 positions of 16 heads over 4-bit caches take 20 us, where one
-// position at a time took 78.
+// bytes): 16 sequences with 16 kv heads (129 MB) take 45.5 us, 42 %, 41 without
+// the copies, 28 without the arithmetic. Several new positions: the same
+// instructions, shared by up to eight query rows: 8 positions of 16 heads over
+// 4-bit caches take 20 us, where one position at a time took 78.
 #pragma once
 
 #include <cfloat>
@@ -347,6 +347,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
     using C = Cfg<FK, FV, D>;
     constexpr bool kBfK = FK == F_BF16, kBfV = FV == F_BF16;
     constexpr int kPlanesK = D / kv_plane_dims(FK), kPlanesV = D / kv_plane_dims(FV);
+    // planes of 16-bit K that are summed by the tensor cores, which cut rather
+    // than round, before they are added to a score in fp32: with 4 (64 dims)
+    // outputs of 128 F16 dims are off by 5.0e-7 of their norm and of 256 BF16 dims
+    // by 5.7e-7, with all planes 7.9e-7 and 15e-7; the shorter chains also take
+    // 44.4 instead of 47.6 us for 3 positions over 8 BF16 sequences of 16000
+    constexpr int kSumPlanes = 4;
     constexpr int kStepsPerPlane = kv_plane_dims(FK) / 16;  // 2 for quantised K
     constexpr int kTilesPerPlane = kv_plane_dims(FV) / 16;  // 2 for quantised V
     constexpr int S = C::kStep;                             // strips taken at a time
@@ -581,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                         k_frag<FK>(sk + t * C::kSlotBytes, p, k_row + 8 * kv_row_bytes(FK), kk0,
                                    kk1, b[t][1]);
                     }
-                    if (kv_quantised(FK) || p == 0) {
+                    if (kv_quantised(FK) || p % kSumPlanes == 0) {
 #pragma unroll
                         for (int t = 0; t < S; ++t)
 #pragma unroll
@@ -606,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                                     acc[t][x] = mma<kBfK>(q3, b[t][x][0], b[t][x][1], acc[t][x]);
                         }
                     }
-                    if (kv_quantised(FK) || p == kPlanesK - 1) {
+                    if (kv_quantised(FK) || p % kSumPlanes == kSumPlanes - 1 || p == kPlanesK - 1) {
 #pragma unroll
                         for (int t = 0; t < S; ++t)
 #pragma unroll
@@ -618,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                                         sk + t * C::kSlotBytes + kv_code_bytes(FK, D) + (p * kStrip + 8 * x + 2 * j) * 2));
                                     sum[t][x] = fma2(pack_f2(d.x, d.y), both, sum[t][x]);
                                 } else {
-                                    sum[t][x] = both;
+                                    sum[t][x] = add2(sum[t][x], both);
                                 }
                             }
                     }
@@ -760,7 +766,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
             auto weigh = [&](auto by_row) {
 #pragma unroll
                 for (int p = 0; p < kPlanesV; ++p) {
-                    float4 acc[2] = {zero, zero};
+                    // products with the weights' low terms have sums of their own
+                    // where unpacking is what takes time (shorter chains: 48
+                    // ragged Q4_0 sequences 62.7 us, 64.2 in one sum)
+                    float4 acc[2] = {zero, zero}, low[2] = {zero, zero};
 #pragma unroll
                     for (int t = 0; t < S; ++t) {
                         uint32_t b0[3], b1[3];
@@ -779,9 +788,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                         }
                         uint4 v[2];
                         v_frag<FV>(sv + t * C::kSlotBytes, p, v_row, vk0, vk1, v);
-                        auto product = [&](const uint4 &of, float4 &to) {
-                            if constexpr (kBfV) to = mma<kBfV>(of, b0[2], b1[2], to);
-                            to = mma<kBfV>(of, b0[1], b1[1], to);
+                        auto product = [&](const uint4 &of, float4 &to, float4 &lo) {
+                            if constexpr (kBfV) lo = mma<kBfV>(of, b0[2], b1[2], lo);
+                            lo = mma<kBfV>(of, b0[1], b1[1], lo);
                             to = mma<kBfV>(of, b0[0], b1[0], to);
                         };
                         if constexpr (by_row.value) {
@@ -792,13 +801,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                                 const int at = first + t * kStrip + 2 * j;
                                 const uint32_t m0 = seen_pair(seen[r], at), m1 = seen_pair(seen[r], at + 8);
                                 float4 x = acc[0];
-                                product(make_uint4(v[0].x & m0, v[0].y & m0, v[0].z & m1, v[0].w & m1), x);
+                                product(make_uint4(v[0].x & m0, v[0].y & m0, v[0].z & m1, v[0].w & m1), x, x);
                                 if (r == 2 * j) acc[0].x = x.x, acc[0].z = x.z;
                                 if (r == 2 * j + 1) acc[0].y = x.y, acc[0].w = x.w;
                             }
                         } else {
 #pragma unroll
-                            for (int u = 0; u < kTilesPerPlane; ++u) product(v[u], acc[u]);
+                            for (int u = 0; u < kTilesPerPlane; ++u)
+                                product(v[u], acc[u], kv_quantised(FV) ? low[u] : acc[u]);
                         }
                     }
 #pragma unroll
@@ -806,6 +816,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                         uint64_t(&to)[2] = o[p * kTilesPerPlane + u];
                         to[0] = add2(to[0], pack_f2(acc[u].x, acc[u].y));
                         to[1] = add2(to[1], pack_f2(acc[u].z, acc[u].w));
+                        if constexpr (kv_quantised(FV)) {
+                            to[0] = add2(to[0], pack_f2(low[u].x, low[u].y));
+                            to[1] = add2(to[1], pack_f2(low[u].z, low[u].w));
+                        }
                     }
                 }
             };

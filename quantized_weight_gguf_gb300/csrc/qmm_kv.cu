@@ -3,10 +3,11 @@
 //
 // Both kernels move each value once and do a few operations on it, so memory
 // bounds them: 8000 rows of 48 heads of 128 rotated and appended in F16 take
-// 55 us (6.5 TB/s), 16 sequences of up to 8111 positions of 8 heads of 128 read
-// back from Q8_0 / Q4_0 183 us (6.6 TB/s). A lane takes four dims, so that fp32 loads and stores are 16
-// bytes wide; the 32 dims of a block are eight neighbouring lanes, so that its
-// maximum takes three shuffles and its codes are one 32-byte sector.
+// 55 us (6.6 TB/s, 96 % of a copy's rate), 16 sequences of up to 8111 positions of
+// 8 heads of 128 read back from Q8_0 / Q4_0 182 us (6.6 TB/s). A lane takes four
+// dims, so that fp32 loads and stores are 16 bytes wide; the 32 dims of a block
+// are eight neighbouring lanes, so that its maximum takes three shuffles and its
+// codes are one 32-byte sector.
 #include "qmm_kv.cuh"
 #include "qmm_kv_launch.h"
 
@@ -253,8 +254,8 @@ __global__ void __launch_bounds__(kKvThreads) append_kernel(const KvAppend a) {
 }
 
 // LPU lanes read positions t0, t0 + step, ... < kStrip (a warp's lanes and SPLIT
-// warps share a strip) of a strip half in format F (those whose row is in [lo, hi); others up to the row count are
-// zeros): K's or V's rows of one head, `stride` floats apart in out.
+// warps share a strip) of a strip half in format F: K's or V's rows of one head,
+// `stride` floats apart in out; rows outside [from, to) are zeros.
 template <int F, int LPU, int NI, int SPLIT>
 __device__ __forceinline__ void read_half(const uint8_t *half, float *out, int64_t stride, int dim,
                                           int t0, int from, int to, int rows, int l, bool vec) {
