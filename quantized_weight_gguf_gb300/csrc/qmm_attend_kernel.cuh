@@ -409,6 +409,32 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
             }
             continue;
         }
+        // ---- query rows on their way (before the page table's entries are waited for) ----
+        const int q_row = threadIdx.x >> 4, q_part = threadIdx.x & 15;
+        float x[(D + 127) / 128][8];
+        {
+            int64_t q_at;
+            const bool there = row_offset<MANY>(a, it, q_row, D, a.q_stride, q_at);
+            const float *q = a.q + q_at;
+#pragma unroll
+            for (int i = 0; i < (D + 127) / 128; ++i) {
+                const int d = 8 * (q_part + 16 * i);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[i][k] = 0.0f;
+                if (there && d < D) {
+                    if (a.vec) {
+                        const float4 u = *reinterpret_cast<const float4 *>(q + d);
+                        const float4 v = *reinterpret_cast<const float4 *>(q + d + 4);
+                        x[i][0] = u.x; x[i][1] = u.y; x[i][2] = u.z; x[i][3] = u.w;
+                        x[i][4] = v.x; x[i][5] = v.y; x[i][6] = v.z; x[i][7] = v.w;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) x[i][k] = q[d + k];
+                    }
+                }
+            }
+        }
+
         // ---- copies of the first strips ----
         // The warps take runs of S strips in turn.
         const int runs = (it.end - it.begin + S - 1) / S;
@@ -475,31 +501,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
 
         // ---- query rows as A fragments ----
         {
-            const int row = threadIdx.x >> 4, part = threadIdx.x & 15;
-            int64_t q_at;
-            const bool there = row_offset<MANY>(a, it, row, D, a.q_stride, q_at);
-            const float *q = a.q + q_at;
-            float x[(D + 127) / 128][8];
             float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < (D + 127) / 128; ++i) {
-                const int d = 8 * (part + 16 * i);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[i][k] = 0.0f;
-                if (there && d < D) {
-                    if (a.vec) {
-                        const float4 u = *reinterpret_cast<const float4 *>(q + d);
-                        const float4 v = *reinterpret_cast<const float4 *>(q + d + 4);
-                        x[i][0] = u.x; x[i][1] = u.y; x[i][2] = u.z; x[i][3] = u.w;
-                        x[i][4] = v.x; x[i][5] = v.y; x[i][6] = v.z; x[i][7] = v.w;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) x[i][k] = q[d + k];
-                    }
-                }
+            for (int i = 0; i < (D + 127) / 128; ++i)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[i][k]));
-            }
             float up = 1.0f, down = 1.0f;
             if constexpr (!kBfK) {  // largest |q| of the row into [2^13, 2^14)
 #pragma unroll
@@ -510,13 +516,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                 // 2^-126 for k = 126 is the smallest normal number
                 down = __uint_as_float((uint32_t)(127 - k) << 23);
             }
-            if (part == 0) {
-                row_scale[row] = a.scale_log2 * down;
-                if (MANY) seen[row] = seen_from(a, it.pos0 + new_of<MANY>(a, it.tile * kRows + row));
+            if (q_part == 0) {
+                row_scale[q_row] = a.scale_log2 * down;
+                if (MANY) seen[q_row] = seen_from(a, it.pos0 + new_of<MANY>(a, it.tile * kRows + q_row));
             }
 #pragma unroll
             for (int i = 0; i < (D + 127) / 128; ++i) {
-                const int d = 8 * (part + 16 * i);
+                const int d = 8 * (q_part + 16 * i);
                 if (d < D) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -537,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                         uint32_t s[3], t[3];
                         split<kBfK>(v0, v1, s);
                         split<kBfK>(v2, v3, t);
-                        const int at = step * 32 + row * 4 + jj;
+                        const int at = step * 32 + q_row * 4 + jj;
                         sts128(qf + at * 16, s[0], s[1], t[0], t[1]);
                         if constexpr (kBfK) {
                             uint32_t *p = reinterpret_cast<uint32_t *>(q_frag + C::kSteps * 512) + 2 * at;
