@@ -62,7 +62,8 @@ __host__ __device__ constexpr Shape shape_of(int fk, int fv, int dim) {
 // way, query rows converted, the warps' results joined; about 5 us, where a
 // strip takes the CTA its share of an SM's 45 GB/s (at least 0.25 us: the
 // arithmetic on a strip of Q4_0). With 4 strips for every format, CTAs with
-// several items finished 6 us (of 63) after the others on 48 ragged sequences.
+// several items finished 6 us (of 63) after the others on 48 ragged sequences;
+// with 3 us instead of 5 they take 1 us longer, with 4 or 6.5 the same.
 __host__ __device__ constexpr int item_cost_of(int fk, int fv, int dim, int ctas) {
     const int ns = kv_strip_bytes(fk, fv, dim) * ctas / 45;
     return 5000 / (ns > 250 ? ns : 250);
