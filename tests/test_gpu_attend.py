@@ -341,3 +341,47 @@ def test_scratch_of_streams_and_of_a_capture():
         got += [(q.attend(*c[:4]), c[4]) for c in cases]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in got)
+
+
+@pytest.mark.parametrize("fmt", range(len(ref.FORMATS)))
+@pytest.mark.parametrize("n_new", [1, 3])
+def test_a_bad_page_among_strips_taken_together(fmt, n_new):
+    """A page id out of range inside a run of strips: its positions are absent, the others stay."""
+    fk, fv = ref.FORMATS[fmt]
+    rng = np.random.default_rng(20 + fmt)
+    n, page = 400, 16
+    table, host, cache = _setup(rng, fk, fv, [n], page, 1, 64)
+    xq = rng.standard_normal((1, n_new, 3, 64)).astype(np.float32)
+    broken = table.copy()
+    bad = [1, 6, 7, 12, 24]
+    broken[0, bad] = [host.raw.shape[0], -5, 1 << 30, -1, host.raw.shape[0] + 7]
+    out = q.attend(cache, _dev(xq), _dev(broken), _dev(np.array([n], np.int32))).cpu().numpy()
+    with pytest.raises(q.QmmError) as e:
+        q.qmm_device_status()
+    assert e.value.status == 12 and q.qmm_device_status() == 0
+    k, v = host.values(0, table[0], n), host.values(1, table[0], n)
+    for i in range(n_new):
+        keep = [p for p in range(n - n_new + 1 + i) if p // page not in bad]
+        want, tol = ref.attention(xq[0, i], k[keep], v[keep], 0, len(keep) - 1, np.float64(np.float32(0.125)))
+        assert (np.abs(out[0, i] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", [0, 2])
+def test_pages_past_32_bits(fmt):
+    """The pages in use lie beyond 4 GiB of the pool."""
+    fk, fv = ref.FORMATS[fmt]
+    rng = np.random.default_rng(30)
+    n, page, n_kv, dim = 90, 16, 2, 128
+    per = q.qmm_kv_page_bytes(fk, fv, page, n_kv, dim)
+    table, n_pages = ref.make_table(rng, [n], page)
+    host = ref.Pages(fk, fv, n_pages, page, n_kv, dim)
+    _fill(host, table, [n], rng)
+    first = (1 << 32) // per + 1
+    pages = torch.empty((first + n_pages, per), dtype=torch.uint8, device=DEV)
+    pages[first:] = _dev(host.raw)
+    cache = q.KvCache(fk, fv, pages, page, n_kv, dim)
+    xq = rng.standard_normal((1, 1, 6, dim)).astype(np.float32)
+    out = q.attend(cache, _dev(xq), _dev(table + first), _dev(np.array([n], np.int32))).cpu().numpy()
+    want, tol = ref.attention(xq[0, 0], host.values(0, table[0], n), host.values(1, table[0], n), 0, n - 1,
+                              np.float64(np.float32(dim ** -0.5)))
+    assert (np.abs(out[0, 0] - want) <= tol).all() and q.qmm_device_status() == 0
