@@ -516,7 +516,8 @@ typedef struct qmm_attend_args {
  * for qmm_matmul_ex (calls that can run concurrently pass their own). */
 int qmm_attend(const qmm_attend_args *a);
 
-/* Device scratch bytes qmm_attend needs for *a; 0 when *a is not accepted.
+/* Device scratch bytes qmm_attend needs for *a; 0 when it needs none (tables
+ * or a window of few positions) or *a is not accepted.
  * Host only (reads the device's SM count). */
 size_t qmm_attend_workspace_bytes(const qmm_attend_args *a);
 

@@ -94,16 +94,31 @@ int cost_of(const Attend &a) {
 // Tiles of a sequence and kv head; n_new * group is below 2^31.
 int tiles_of(const Attend &a) { return (int)((a.n_new * (a.n_heads / a.c.n_kv) + kRows - 1) / kRows); }
 
-// CTAs of a launch: one resident wave, or fewer when even the longest rows
-// that the tables can hold make less work than that.
-int grid_of(const Attend &a, const DeviceInfo &dev) {
-    const int wave = dev.sm_count * shape_of(a.c.fmt_k, a.c.fmt_v, a.c.dim).ctas;
+// Strips of the longest rows that the tables can hold.
+int64_t most_strips(const Attend &a) {
     int64_t most = a.c.capacity;
     if (a.window && a.window < most) most = a.window + kRows + kStrip - 1;  // of a tile's rows
-    const int64_t strips = (most + kStrip - 1) / kStrip + 1;
-    const int64_t items = (int64_t)a.c.n_seqs * tiles_of(a) * a.c.n_kv;
+    return (most + kStrip - 1) / kStrip;
+}
+
+int64_t items_of(const Attend &a) { return (int64_t)a.c.n_seqs * tiles_of(a) * a.c.n_kv; }
+
+int wave_of(const Attend &a, const DeviceInfo &dev) {
+    return dev.sm_count * shape_of(a.c.fmt_k, a.c.fmt_v, a.c.dim).ctas;
+}
+
+bool is_whole(const Attend &a, const DeviceInfo &dev) {
+    return most_strips(a) <= whole_strips(items_of(a), wave_of(a, dev), cost_of(a));
+}
+
+// CTAs of a launch: one resident wave, or fewer when even the longest rows
+// make less work than that.
+int grid_of(const Attend &a, const DeviceInfo &dev) {
+    const int wave = wave_of(a, dev);
+    const int64_t items = items_of(a);
     if (items >= wave) return wave;  // also keeps the product in range
-    const int64_t shares = (items * (strips + cost_of(a)) + kMinShare - 1) / kMinShare;
+    if (is_whole(a, dev)) return (int)items;
+    const int64_t shares = (items * (most_strips(a) + 1 + cost_of(a)) + kMinShare - 1) / kMinShare;
     return shares < wave ? (int)shares : wave;
 }
 
@@ -120,6 +135,7 @@ bool attend_supports(int dim) {
 }
 
 size_t attend_workspace_bytes(const Attend &a, const DeviceInfo &dev) {
+    if (attend::is_whole(a, dev)) return 0;
     const int grid = attend::grid_of(a, dev);
     return attend::parts_bytes(a.c.dim, grid) + sizeof(attend::Join) * grid;
 }
@@ -130,9 +146,11 @@ cudaError_t launch_attend(const Attend &a, const DeviceInfo &dev, cudaStream_t s
     p.c = a.c;
     p.q = a.q;
     p.out = a.out;
+    p.whole = attend::is_whole(a, dev);
     p.parts = static_cast<float *>(a.workspace);
-    p.joins = reinterpret_cast<attend::Join *>(static_cast<uint8_t *>(a.workspace) +
-                                               attend::parts_bytes(a.c.dim, grid));
+    p.joins = p.whole ? nullptr
+                      : reinterpret_cast<attend::Join *>(static_cast<uint8_t *>(a.workspace) +
+                                                         attend::parts_bytes(a.c.dim, grid));
     p.q_stride = a.q_stride;
     p.out_stride = a.out_stride;
     p.window = a.window;
@@ -149,7 +167,7 @@ cudaError_t launch_attend(const Attend &a, const DeviceInfo &dev, cudaStream_t s
     else if (a.c.fmt_k == F_Q4_0) e = attend::launch_q4(p, grid, s);
     else if (a.c.fmt_v == F_Q4_0) e = attend::launch_q8q4(p, grid, s);
     else e = attend::launch_q8(p, grid, s);
-    if (e != cudaSuccess || grid < 2) return e;
+    if (e != cudaSuccess || p.whole || grid < 2) return e;
     return attend::launch_programmatic(attend::attend_join_kernel, p, grid - 1, attend::kThreads, 0, s);
 }
 

@@ -73,6 +73,17 @@ __host__ __device__ constexpr int item_cost_of(int fk, int fv, int dim, int ctas
 // strips per warp.
 constexpr int kMinShare = 8;
 
+// Where no row can see more strips than a few item costs (by the tables' size
+// and the window), items are not split: CTA c takes items c, c + grid, ... as
+// they are, and no join is launched. 16 sequences of up to 400 positions over 8
+// kv heads of 128 in Q8_0 take 7.4 us so, 11.8 split, 96 of them 22.4 and 27.4.
+// The limit is 2 costs (one sequence of 400 positions over 8 kv heads of 256 in
+// Q8_0: 13.8 us whole, 11.5 split), 4 where items are an eighth of the CTAs or
+// more (96 sequences of it: 37 whole, 45 split; 800 positions are about equal).
+__host__ __device__ constexpr int whole_strips(int64_t items, int wave, int item_cost) {
+    return (8 * items >= wave ? 4 : 2) * item_cost;
+}
+
 // A split item, written by each CTA whose share ends inside one: the CTAs
 // first .. first + parts - 1 hold its partial results.
 struct Join {
@@ -93,6 +104,7 @@ struct AttendParams {
     int item_cost;           // see item_cost_of
     float scale_log2;  // scale * log2(e)
     bool vec;
+    bool whole;        // items are not split (see whole_strips); then parts and joins are not used
 };
 
 // a partial result: [kRows] maxima, [kRows] totals, [kRows][dim] sums
@@ -155,7 +167,8 @@ struct WorkSearch {
     int tile;
 };
 struct Work {
-    int64_t at, end;     // the share, in strips and item costs of all items end to end
+    int64_t at, end;     // the share, in strips and item costs of all items end to end; of whole items:
+                         // the next item and the number of all
     int64_t total;
     int shares;          // CTAs that have one
     int tile;            // the tile of all sequences' that `at` is in
@@ -173,6 +186,11 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int b) {
 // tiles each: a few loads for a decoding batch.
 template <bool MANY>
 __device__ __forceinline__ bool find_work(const AttendParams &a, int cta, WorkSearch *sh, Work &w) {
+    if (a.whole) {
+        w.at = cta;
+        w.end = (int64_t)a.all_tiles * a.c.n_kv;
+        return w.at < w.end;
+    }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.all_tiles + kThreads - 1) / kThreads;
     const int r0 = min(tid * per, a.all_tiles), r1 = min(r0 + per, a.all_tiles);
@@ -240,24 +258,32 @@ struct Item {
 template <bool MANY>
 __device__ __forceinline__ bool next_item(const AttendParams &a, Work &w, Item &it) {
     while (w.at < w.end) {
+        if (a.whole) w.tile = (int)(w.at / a.c.n_kv);
         const TileRange x = tile_range<MANY>(a, w.tile);
-        const int n = item_strips(x), cost = item_weight(a, x);
-        const int64_t all = (int64_t)cost * a.c.n_kv;
-        if (w.at >= w.base + all) {
-            w.base += all;
-            ++w.tile;
-            continue;
+        const int n = item_strips(x);
+        if (a.whole) {
+            it.head = (int)(w.at - (int64_t)w.tile * a.c.n_kv);
+            it.begin = 0;
+            it.end = n;
+            w.at += gridDim.x;
+        } else {
+            const int cost = item_weight(a, x);
+            const int64_t all = (int64_t)cost * a.c.n_kv;
+            if (w.at >= w.base + all) {
+                w.base += all;
+                ++w.tile;
+                continue;
+            }
+            it.head = (int)quotient(w.at - w.base, cost);
+            it.base = w.base + (int64_t)it.head * cost;
+            const int64_t stop = it.base + cost < w.end ? it.base + cost : w.end;
+            it.begin = (int)(w.at - it.base);
+            it.end = stop - it.base < n ? (int)(stop - it.base) : n;
+            w.at = stop;
+            if (it.begin >= it.end) continue;  // only of the item's cost
         }
-        const int k = (int)quotient(w.at - w.base, cost);
-        it.base = w.base + (int64_t)k * cost;
-        const int64_t stop = it.base + cost < w.end ? it.base + cost : w.end;
-        it.begin = (int)(w.at - it.base);
-        it.end = stop - it.base < n ? (int)(stop - it.base) : n;
-        w.at = stop;
-        if (it.begin >= it.end) continue;  // only of the item's cost
         it.pos0 = x.pos0;
         it.seq = x.seq;
-        it.head = k;
         it.tile = x.tile;
         it.lo = x.lo;
         it.hi = x.hi;

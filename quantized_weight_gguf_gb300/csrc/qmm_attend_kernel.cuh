@@ -10,7 +10,7 @@
 // items, laid end to end, are divided evenly among the CTAs of one resident
 // wave, whatever the lengths are; an item whose strips fall to several CTAs is
 // joined by attend_join_kernel from partial results (maximum, total, weighted
-// sum).
+// sum). Short items are dealt out whole (see whole_strips).
 //
 // A CTA is kWarps warps that take an item's strips in turn, up to four at a
 // time where the ring has room. Each warp streams its strips through a ring of its
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
 
     Work w;
     if (!find_work<MANY>(a, (int)blockIdx.x, search, w)) {
-        if (threadIdx.x == 0) a.joins[blockIdx.x].parts = 0;
+        if (threadIdx.x == 0 && !a.whole) a.joins[blockIdx.x].parts = 0;
         return;
     }
     Join next_join;
@@ -909,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
         fence_proxy_async_smem();  // the merge buffers' accesses, before copies land there again
         __syncthreads();
     }
-    if (threadIdx.x == 0) a.joins[blockIdx.x] = next_join;
+    if (threadIdx.x == 0 && !a.whole) a.joins[blockIdx.x] = next_join;
     pdl_launch_dependents();
 }
 

@@ -84,6 +84,22 @@ def test_formats_and_head_dims(fmt, dim):
     _check(host, cache, table, LENS, xq)
 
 
+@pytest.mark.parametrize("fmt", range(len(ref.FORMATS)))
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("n_new,window", [(1, 0), (3, 0), (1, 650)])
+def test_items_split_over_blocks(fmt, dim, n_new, window):
+    """Tables much wider than the lengths, as a server holds them: long and short items, an empty one."""
+    fk, fv = ref.FORMATS[fmt]
+    rng = np.random.default_rng(1000 * fmt + dim + n_new)
+    lens, page = [700, 0, 17, 260], 32
+    table, n_pages = ref.make_table(rng, lens, page, width=4096)
+    host = ref.Pages(fk, fv, n_pages, page, 2, dim, _garbage(rng))
+    _fill(host, table, lens, rng)
+    cache = q.KvCache(fk, fv, _dev(host.raw), page, 2, dim)
+    xq = rng.standard_normal((len(lens), n_new, 8, dim)).astype(np.float32)
+    _check(host, cache, table, lens, xq, window=window)
+
+
 @pytest.mark.parametrize("n_heads,n_kv", [(1, 1), (3, 3), (6, 2), (5, 1), (8, 1), (9, 1), (16, 1), (34, 2)])
 @pytest.mark.parametrize("fmt", [0, 2])
 def test_head_layouts(n_heads, n_kv, fmt):
