@@ -489,7 +489,8 @@ class KvCache:
     """A pool of cache pages: `pages` is a uint8 CUDA tensor [n_pages, page bytes]
     (one page holds page_size positions of every kv head), the formats are
     "f16", "bf16", "q8_0" or "q4_0" (the same for K and V, or K "q8_0" and V
-    "q4_0"). Page tables and lengths belong to the calls."""
+    "q4_0"). Page tables and lengths belong to the calls. Every tensor of a call
+    is on the pool's device: the kernels follow the addresses that they are given."""
 
     def __init__(self, fmt_k, fmt_v, pages, page_size: int, n_kv_heads: int, head_dim: int):
         self.fmt_k, self.fmt_v, self.pages = _fmt(fmt_k), _fmt(fmt_v), pages
@@ -501,6 +502,7 @@ class KvCache:
                 or pages.element_size() != 1:
             raise ValueError(f"pages must be contiguous bytes [n_pages, {self.page_bytes}], "
                              f"got {tuple(pages.shape)}")
+        self._device = pages.get_device()    # -1: host memory
         # each call starts from a copy of its arguments with the pool filled in
         pool = qmm_kv_cache(self.fmt_k, self.fmt_v, pages.data_ptr(), pages.numel(), pages.shape[0],
                             page_size, n_kv_heads, head_dim)
@@ -522,6 +524,8 @@ class KvCache:
     def _args(self, template, page_table, lens):
         """A call's arguments with its int32 page_table [n_seqs, max_pages] (rows may be strided)
         and lens [n_seqs], and n_seqs."""
+        self._same_device("page_table", page_table)
+        self._same_device("lens", lens)
         int32 = _torch().int32
         shape, count = page_table.shape, lens.shape
         if len(shape) != 2 or len(count) != 1 or shape[0] != count[0] \
@@ -540,6 +544,11 @@ class KvCache:
         c.n_seqs = n_seqs
         return a, n_seqs
 
+    def _same_device(self, name, t):
+        if t.get_device() != self._device or self._device < 0:
+            raise ValueError(f"{name} ({t.device}) and the cache's pages ({self.pages.device}) must be on "
+                             "one CUDA device")
+
     def view(self, page_table, lens) -> qmm_kv_cache:
         """The C description of this pool with a call's page_table and lens."""
         return self._args(self._read, page_table, lens)[0].cache
@@ -550,6 +559,7 @@ class KvCache:
         if len(shape) != 4 or shape[0] != n_seqs or shape[3] != dim or t.dtype is not _torch().float32:
             raise ValueError(f"{name} must be float32 [{n_seqs}, n_new, heads, {dim}], "
                              f"got {tuple(shape)}")
+        self._same_device(name, t)
         s0, s1, s2, s3 = t.stride()
         n_new, heads = shape[1], shape[2]
         row = s1 if n_new > 1 else s0 if n_seqs > 1 else heads * dim
@@ -592,6 +602,7 @@ def kv_append(cache: KvCache, k, v, page_table, lens, *, q=None, q_out=None, rop
         if len(shape) != 3 or shape[2] != 2 or not rope.is_contiguous() \
                 or rope.dtype is not _torch().float32:
             raise ValueError("rope must be contiguous float32 [positions, n_rot / 2, 2]")
+        cache._same_device("rope", rope)
         a.rope, a.rope_len, a.n_rot = rope.data_ptr(), shape[0], 2 * shape[1]
     a.rope_style = ROPE_STYLES[rope_style] if isinstance(rope_style, str) else int(rope_style)
     a.stream = _stream_of(stream, cache.pages)
@@ -609,8 +620,11 @@ def kv_read(cache: KvCache, page_table, lens, count: int, *, first=None, k=None,
     a.first, a.count = -1 if first is None else first, count
     given, torch = (("k", k), ("v", v)), _torch()
     for name, t in given:
-        if t is not None and (t.shape != shape or not t.is_contiguous() or t.dtype is not torch.float32):
+        if t is None:
+            continue
+        if t.shape != shape or not t.is_contiguous() or t.dtype is not torch.float32:
             raise ValueError(f"{name} must be contiguous float32 {shape}")
+        cache._same_device(name, t)
     if k is None:
         k = torch.empty(shape, dtype=torch.float32, device=cache.pages.device)
     if v is None:
@@ -649,7 +663,10 @@ def attend(cache: KvCache, q, page_table, lens, *, scale=None, window=0, out=Non
         elif need:
             ws = workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     if workspace is not None:
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        cache._same_device("workspace", workspace)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     qmm_attend(a)
     if stream is not None:
         _keep_until_done(ws, stream)
