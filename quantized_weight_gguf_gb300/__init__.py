@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqmm.so")
@@ -471,17 +472,20 @@ def _stream_of(stream, tensor):
     return torch.cuda.current_stream(tensor.device).cuda_stream
 
 
-# Scratch of attend calls on torch's current stream, kept per device and stream
-# and grown as needed. The calls of a stream run one after the other, so they
-# can share it; an allocation per call took 6 of a small call's 15 us.
-_attend_scratch = {}
+# Scratch of attend calls on torch's current stream, kept per host thread, device
+# and stream and grown as needed; an allocation per call took 6 of a small call's
+# 15 us. The kernels of a stream run one after the other, so the calls that one
+# thread makes on it can share scratch. Calls of two threads cannot: a call is two
+# launches, which another thread's may come between on a stream that both use.
+_attend_scratch = threading.local()
 
 
 def _scratch_of_stream(need: int, device, handle: int):
+    held = _attend_scratch.__dict__          # of this thread
     key = (device.index, handle)
-    ws = _attend_scratch.get(key)
+    ws = held.get(key)
     if ws is None or ws.numel() < need:
-        ws = _attend_scratch[key] = _torch().empty(max(need, 1 << 20), dtype=_torch().uint8, device=device)
+        ws = held[key] = _torch().empty(max(need, 1 << 20), dtype=_torch().uint8, device=device)
     return ws
 
 
@@ -642,7 +646,7 @@ def attend(cache: KvCache, q, page_table, lens, *, scale=None, window=0, out=Non
     heads), scale 1 / sqrt(head_dim) unless given, window 0 (all positions) or
     the number of last positions that a row sees. Returns out, shaped like q
     (the given one when passed). Scratch is `workspace` (uint8) when given;
-    else one that is kept for torch's current stream, or (on another `stream`,
+    else one that the host thread keeps for torch's current stream, or (on another `stream`,
     or under graph capture) a torch allocation of the call."""
     a, n_seqs = cache._args(cache._attend, page_table, lens)
     a.q_stride, n_new, n_heads = cache.rows("q", q, n_seqs)

@@ -54,3 +54,58 @@ def test_tensors_in_host_memory_are_refused(call, names):
     CALLS[call](cache, here)
     torch.cuda.synchronize()
     assert q.qmm_device_status() == 0
+
+
+def test_host_threads_do_not_share_attention_scratch():
+    """One call is two launches (strips, then their join), so calls of two threads can interleave on
+    a stream that both use."""
+    import threading
+
+    def scratch():
+        mine = [q._scratch_of_stream(n, torch.device("cpu"), 0) for n in (1000, 500, 3 << 20, 7)]
+        assert mine[0] is mine[1] and mine[2] is mine[3] and mine[2].numel() >= 3 << 20
+        return mine
+
+    here, there = scratch(), []
+    other = threading.Thread(target=lambda: there.extend(scratch()))
+    other.start()
+    other.join()
+    assert len(there) == 4
+    assert not {t.data_ptr() for t in here} & {t.data_ptr() for t in there}
+
+
+@pytest.mark.gpu
+def test_two_host_threads_on_one_stream():
+    """Split items of different inputs from two threads on the default stream: every result is the
+    serial one, bit for bit."""
+    import threading
+    torch.manual_seed(5)
+    n_kv, dim, page, n = 2, 64, 16, 4000
+    jobs = []
+    for seed in range(2):
+        per = -(-n // page)
+        cache = q.KvCache.empty("q8_0", "q8_0", per, page, n_kv, dim, device="cuda:0")
+        table = torch.randperm(per).to(torch.int32).view(1, per).cuda()
+        lens = torch.tensor([n], dtype=torch.int32, device="cuda:0")
+        k, v = torch.randn((2, 1, n, n_kv, dim), device="cuda:0")
+        q.kv_append(cache, k, v, table, lens)
+        x = torch.randn((1, 1, 8, dim), device="cuda:0")
+        ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda:0")
+        jobs.append((cache, x, table, lens, q.attend(cache, x, table, lens, workspace=ws)))
+    torch.cuda.synchronize()
+    start, bad = threading.Barrier(2), []
+
+    def run(job):
+        start.wait()
+        for _ in range(300):
+            out = q.attend(*job[:4])
+            bad.append((out != job[4]).any())
+
+    threads = [threading.Thread(target=run, args=(job,)) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert len(bad) == 600 and not torch.stack(bad).any()
+    assert q.qmm_device_status() == 0
