@@ -110,16 +110,20 @@ struct AttendParams {
 // a partial result: [kRows] maxima, [kRows] totals, [kRows][dim] sums
 __host__ __device__ constexpr int part_floats(int dim) { return kRows * (dim + 2); }
 
-// The positions [lo, hi) that the row of position pos sees.
+// The positions [lo, hi) that the row of position pos sees. Both ends grow with
+// pos, also where nothing is seen (before the sequence's start lo = hi = 0, with
+// the window past the tables' end lo = hi = capacity), so that a tile's ends are
+// its first row's lo and its last row's hi.
 struct Range {
     int lo, hi;
 };
+__device__ __forceinline__ int within(int64_t pos, int64_t capacity) {
+    return (int)(pos < 0 ? 0 : pos < capacity ? pos : capacity);
+}
 __device__ __forceinline__ Range seen_from(const AttendParams &a, int64_t pos) {
-    const int64_t hi = pos + 1 < a.c.capacity ? pos + 1 : a.c.capacity;
-    const int64_t lo = a.window && pos + 1 > a.window ? pos + 1 - a.window : 0;
     Range x;
-    x.lo = hi > lo ? (int)lo : 0;
-    x.hi = hi > lo ? (int)hi : 0;
+    x.lo = a.window ? within(pos + 1 - a.window, a.c.capacity) : 0;
+    x.hi = within(pos + 1, a.c.capacity);
     return x;
 }
 
@@ -147,7 +151,7 @@ __device__ __forceinline__ TileRange tile_range(const AttendParams &a, int r) {
     const int64_t last = x.pos0 + new_of<MANY>(a, x.tile * kRows + kRows - 1);
     if (last + 1 > a.c.capacity) record_error(a.c.err, DERR_BAD_PAGE);
     const Range l = seen_from(a, last);
-    x.lo = MANY ? seen_from(a, x.pos0 + new_of<MANY>(a, x.tile * kRows)).lo : l.lo;  // 0 for padding
+    x.lo = MANY ? seen_from(a, x.pos0 + new_of<MANY>(a, x.tile * kRows)).lo : l.lo;
     x.hi = l.hi;
     x.first = x.lo / kStrip;
     x.strips = x.hi > x.lo ? (x.hi + kStrip - 1) / kStrip - x.first : 0;

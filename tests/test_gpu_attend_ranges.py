@@ -1,0 +1,86 @@
+"""Attention over the paged key-value cache, on the GPU, at the ends of what its
+numbers can hold: small and very unequal V scales, infinities, values near
+fp32's limits, lengths beyond the table. Against the formula in 64 bits with
+kv_reference's tolerance."""
+import numpy as np
+import pytest
+
+import kv_reference as ref
+
+torch = pytest.importorskip("torch")
+import quantized_weight_gguf_gb300 as q  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from quantized_weight_gguf_gb300 import build_lib
+    build_lib.build()
+    q.load()
+    yield
+    q.qmm_device_status()
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def _appended(rng, fk, fv, k, v, page=32):
+    """A cache that holds rows k, v [n, n_kv, dim] of one sequence, its table on the host, and the
+    values that its bytes stand for."""
+    n, n_kv, dim = k.shape
+    table, n_pages = ref.make_table(rng, [n], page)
+    cache = q.KvCache.empty(fk, fv, n_pages, page, n_kv, dim, device=DEV)
+    q.kv_append(cache, _dev(k[None].astype(np.float32)), _dev(v[None].astype(np.float32)), _dev(table),
+                _dev(np.array([n], np.int32)))
+    host = ref.Pages(fk, fv, n_pages, page, n_kv, dim)
+    host.raw[:] = cache.pages.cpu().numpy()
+    return cache, table, host.values(0, table[0], n), host.values(1, table[0], n)
+
+
+def _attend(cache, table, n, xq, **kw):
+    out = q.attend(cache, _dev(xq[None]), _dev(table), _dev(np.array([n], np.int32)), **kw)
+    return out.cpu().numpy()[0]
+
+
+def _check(cache, table, k, v, xq, window=0):
+    """xq [n_new, n_heads, dim] at the last positions of k and v."""
+    n, dim, n_new = len(k), k.shape[2], len(xq)
+    out = _attend(cache, table, n, xq, window=window)
+    assert q.qmm_device_status() == 0
+    for i in range(n_new):
+        last = n - n_new + i
+        first = max(0, last + 1 - window) if window else 0
+        want, tol = ref.attention(xq[i], k, v, first, last, np.float64(np.float32(dim ** -0.5)))
+        bad = ~(np.abs(out[i] - want) <= tol)
+        assert not bad.any(), (i, np.abs(out[i] - want)[bad][:4], tol[bad][:4], (np.abs(out[i] - want) / tol).max())
+    return out
+
+
+@pytest.mark.parametrize("fmt", range(len(ref.FORMATS)))
+@pytest.mark.parametrize("width", [4, 64])
+@pytest.mark.parametrize("over,n_new,window,n_heads", [(2, 4, 2, 1), (5, 8, 3, 1), (1, 3, 0, 4), (30, 40, 20, 2),
+                                                       (9, 3, 2, 1), (750, 200, 650, 1)])
+def test_rows_beyond_the_table_leave_the_others_theirs(fmt, width, over, n_new, window, n_heads):
+    """A length past the table's capacity with several new rows (short tables: whole items, wide
+    ones: split): a row sees what of its range lies within the table, zeros where nothing does."""
+    fk, fv = ref.FORMATS[fmt]
+    rng = np.random.default_rng(over)
+    page, dim = 16, 64
+    cap = width * page
+    k, v = rng.standard_normal((2, cap, 1, dim))
+    cache, table, k, v = _appended(rng, fk, fv, k, v, page)
+    assert table.shape[1] == width
+    xq = rng.standard_normal((n_new, n_heads, dim)).astype(np.float32)
+    n = cap + over
+    out = _attend(cache, table, n, xq, window=window)
+    with pytest.raises(q.QmmError) as e:
+        q.qmm_device_status()
+    assert e.value.status == 12 and q.qmm_device_status() == 0
+    for i in range(n_new):
+        last = n - n_new + i
+        first = max(0, last + 1 - window) if window else 0
+        want, tol = ref.attention(xq[i], k, v, first, min(last, cap - 1), np.float64(np.float32(0.125)))
+        assert (np.abs(out[i] - want) <= tol).all(), (i, first, last)
