@@ -511,8 +511,9 @@ typedef struct qmm_attend_args {
  * no position gives zeros. Cache bytes outside the range, whatever they hold,
  * do not reach the result; one that is Inf or NaN within the range makes the
  * row's outputs Inf or NaN. Sums, the softmax's maximum and its total are
- * fp32; q and the weights enter the tensor cores as sums of 16-bit terms that keep
- * at least 22 bits. The same call gives the same result each time. Scratch as
+ * fp32; q and the weights (times V's scales) enter the tensor cores as sums of
+ * 16-bit terms that keep 22 bits of the largest among each 11 binades of scales.
+ * The same call gives the same result each time. Scratch as
  * for qmm_matmul_ex (calls that can run concurrently pass their own). */
 int qmm_attend(const qmm_attend_args *a);
 

@@ -28,7 +28,8 @@
 //    of B. The weights p enter as two fp16 terms as well (two products). For
 //    quantised V a block's scale d is folded into the weight's terms first,
 //    w = p d = h + r: h = fl(p_h d), and with one fma each
-//    r = fl(p_r d + (p_h d - h)), where the bracket is exact. The product over
+//    r = fl(p_r d + (p_h d - h)), where the bracket is exact unless it falls
+//    below 2^-24, fp16's last place (see the spans below). The product over
 //    the strips taken together starts from zero and is added to the running
 //    sums in fp32, so their rounding is to nearest.
 //  - Integer codes enter as exact fp16 integers: the code with its offset
@@ -42,11 +43,22 @@
 // them for the second, so p stays in registers.
 //
 // The softmax subtracts a reference R per row that is not the exact running
-// maximum: a weight 2^(s - R) may grow to 2^lim, lim = 15, less where scales d
-// of 1 and more would take w = p d past 2^15. Only when a score (or a scale)
-// passes that limit is R moved, to 4 below the limit for the largest score
-// seen, and the sums rescaled; so a strip normally takes no shuffles, and the
-// weights that matter stay far from the fp16 terms' subnormal range.
+// maximum: a weight p = 2^(s - R) may grow to 2^15 (2^12 over Q4_0 V, whose
+// scales are larger). Only when a score passes that limit is R moved, to 4 below
+// the limit for the largest score seen, and the sums rescaled; so a strip
+// normally takes no shuffles.
+//
+// The terms of w = p d reach from 2^15 down to 2^-24. For scales d between 2^-11
+// and 1 (2^-8 and 8 for Q4_0) they hold the largest weight's product to 22 bits
+// and more. A run of strips with a scale outside goes through the second product
+// lifted: d times a power of two (exact) that brings the run's largest scale to
+// the top of that range, and the product's sums brought down again in fp32. Where
+// its scales spread over more than 2^11 that is done once per span of 2^11, with
+// that span's scales alone. Without lifts 4000 positions of V of size 1e-5 in Q8_0
+// were off by 1.2e-3. Looking for such scales costs 1 us of 45 with 64 dims in
+// Q4_0 and nothing that shows elsewhere; lifted, 16 sequences of 8000 positions
+// over 16 kv heads of 64 in Q4_0 take 61 us (49 without) and with two spans in
+// every run 93.
 //
 // What bounds it (fractions are of a copy's 6.8 TB/s; device times in a graph).
 // 16-bit caches and 8-bit ones: DRAM, and for short work the way to the first
@@ -320,6 +332,32 @@ __device__ __forceinline__ void v_frag(uint32_t base, int p, uint32_t row, uint3
     }
 }
 
+// ------------------------------------------------------- spans of V scales ----
+// f16 scales up to the binade `top` (a biased exponent, 1 to 30) fall into spans
+// of 11 binades: span 0 is top and the ten below it (and Inf and NaN), span 1 the
+// next eleven, span 2 the rest.
+
+// The spans of a pair of scales, as bits; a scale of 0 is in none.
+__device__ __forceinline__ uint32_t spans_of(uint32_t d, int top) {
+    uint32_t spans = 0;
+#pragma unroll
+    for (int e = 0; e < 32; e += 16) {
+        const uint32_t one = d >> e & 0x7fffu;
+        if (one) spans |= 1u << max(0, top - (int)(one >> 10)) / 11;
+    }
+    return spans;
+}
+// A pair of scales: 0 for one that is not in `span`.
+__device__ __forceinline__ uint32_t in_span(uint32_t d, int top, int span) {
+    const uint32_t from = max(1, (top - 11 * span - 10) << 10), to = span ? ((top - 11 * span + 1) << 10) - 1 : 0x7fff;
+    const uint32_t size = d & 0x7fff7fffu;
+    return d & __vcmpgeu2(size, from * 0x10001u) & __vcmpleu2(size, to * 0x10001u);
+}
+// 2^e (-16 <= e <= 15) as an fp16 pair
+__device__ __forceinline__ uint32_t power_f16(int e) {
+    return (e < -14 ? 1u << (e + 24) : (uint32_t)(e + 15) << 10) * 0x10001u;
+}
+
 // ----------------------------------------------------------------- config ----
 
 template <int FK, int FV, int D>
@@ -357,6 +395,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
     constexpr int kSumPlanes = 4;
     constexpr int kStepsPerPlane = kv_plane_dims(FK) / 16;  // 2 for quantised K
     constexpr int kTilesPerPlane = kv_plane_dims(FV) / 16;  // 2 for quantised V
+    // the weights' limit, and the f16 patterns of the smallest and the largest of
+    // V's scales that do without a lift (see the top of the file)
+    constexpr float kLim = FV == F_Q4_0 ? 12.0f : 15.0f;
+    constexpr uint32_t kLeast = FV == F_Q4_0 ? 7 << 10 : 4 << 10, kMost = kLeast + (11 << 10) - 1;
     constexpr int S = C::kStep;                             // strips taken at a time
     extern __shared__ __align__(128) uint8_t smem[];
     // fixed part: barriers, flags, row scales, softmax states, work search
@@ -566,12 +608,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = 0;
         // the reference of the row's weights and their total (of positions
-        // 2 j and 2 j + 1 of the n-tiles); the limit lim of s - ref, and the f16
-        // pattern of the largest scale that lim allows for
+        // 2 j and 2 j + 1 of the n-tiles)
         float ref = -FLT_MAX;
         uint64_t l = 0;
-        float lim = 15.0f;
-        uint32_t d_bound = 0x3bffu;  // below 1
         for (int n = 0; n < mine; ++n) {
             const int first = (it.first + it.begin + S * (warp + kWarps * n)) * kStrip;
             int group = await();
@@ -679,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                         uint16_t *d = reinterpret_cast<uint16_t *>(v + kv_code_bytes(FV, D));
                         for (int i = lane; i < D / 2; i += 32) {
                             const int at = from + (i & 15);
-                            if (nobody(at)) d[i] = 0;
+                            if (nobody(at)) d[i] = 0x3800u;  // 1/2; its weight is 0
                             else if (MANY && somebody(at) && (d[i] & 0x7c00u) == 0x7c00u) apart = true;
                         }
                     } else {
@@ -699,53 +738,52 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
             float mx = s[0][0][0];
 #pragma unroll
             for (int i = 1; i < 4 * S; ++i) mx = fmaxf(mx, s[i >> 2][(i >> 1) & 1][i & 1]);
-            bool over = mx - ref > lim;
-            uint32_t dv[S][kv_quantised(FV) ? kPlanesV : 1][2], big = 0;  // V's scales
+            bool over = mx - ref > kLim, far = false;
+            uint32_t dv[S][kv_quantised(FV) ? kPlanesV : 1][2];  // V's scales
+            auto scales = [&](int t, int p, int x) {  // of positions 8 x + 2 j and + 1
+                return lds32(sv + t * C::kSlotBytes + kv_code_bytes(FV, D) + (p * kStrip + 8 * x + 2 * j) * 2);
+            };
+            // for the limits each lane looks at a few of them, two at a time
+            constexpr int kWords = kPlanesV * 8, kLook = (S * kWords + 31) / 32;
+            auto look = [&](int i) {
+                const int at = min(lane + 32 * i, S * kWords - 1), t = at / kWords;
+                return lds32(sv + t * C::kSlotBytes + kv_code_bytes(FV, D) + (at - t * kWords) * 4);
+            };
             if constexpr (kv_quantised(FV)) {
+                uint32_t big = 0, small = ~0u;
+#pragma unroll
+                for (int i = 0; i < kLook; ++i) {
+                    // Q8_0's scales have no sign
+                    const uint32_t d = look(i) & (FV == F_Q8_0 ? ~0u : 0x7fff7fffu);
+                    big = __vmaxu2(big, d);
+                    small = __vminu2(small, d);
+                }
+                far = max(big & 0xffffu, big >> 16) > kMost || min(small & 0xffffu, small >> 16) < kLeast;
 #pragma unroll
                 for (int t = 0; t < S; ++t)
 #pragma unroll
                     for (int p = 0; p < kPlanesV; ++p)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            dv[t][p][x] = lds32(sv + t * C::kSlotBytes + kv_code_bytes(FV, D) +
-                                                (p * kStrip + 8 * x + 2 * j) * 2);
-                            // Q8_0's scales have no sign
-                            big = __vmaxu2(big, FV == F_Q8_0 ? dv[t][p][x] : dv[t][p][x] & 0x7fff7fffu);
-                        }
-                big = max(big & 0xffffu, big >> 16);
-                over = over || big > d_bound || (MANY && apart);
+                        for (int x = 0; x < 2; ++x) dv[t][p][x] = scales(t, p, x);
             }
-            if (__any_sync(~0u, over)) {
-                if constexpr (MANY && kv_quantised(FV)) {
-                    if (apart) {  // a scale multiplies the weights of the lane's own row
-                        big = 0;
+            uint32_t spans = 0;  // that V's scales fall into, where they need lifts; from bit 8 on: top
+            if (__any_sync(~0u, over || far)) {
+                if constexpr (kv_quantised(FV)) {
+                    if (__any_sync(~0u, far)) {
+                        uint32_t all = 0;
 #pragma unroll
-                        for (int t = 0; t < S; ++t)
+                        for (int i = 0; i < kLook; ++i) all = __vmaxu2(all, look(i) & 0x7fff7fffu);
+                        int top = (int)__reduce_max_sync(~0u, max(all & 0xffffu, all >> 16)) >> 10;
+                        top = max(1, min(30, top));
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const uint32_t m = seen_pair(seen[g], first + t * kStrip + 8 * x + 2 * j);
-#pragma unroll
-                                for (int p = 0; p < kPlanesV; ++p) {
-                                    dv[t][p][x] &= m;
-                                    big = __vmaxu2(big, dv[t][p][x] & 0x7fff7fffu);
-                                }
-                            }
-                        big = max(big & 0xffffu, big >> 16);
+                        for (int i = 0; i < kLook; ++i) spans |= spans_of(look(i), top);
+                        spans = __reduce_or_sync(~0u, spans);
+                        if (spans) spans |= (uint32_t)top << 8;
                     }
                 }
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-                if constexpr (kv_quantised(FV)) {
-                    big = max(big, __shfl_xor_sync(~0u, big, 1));
-                    big = max(big, __shfl_xor_sync(~0u, big, 2));
-                    if (big > d_bound) {
-                        d_bound = big | 0x3ffu;  // all scales of this exponent
-                        const float top = f16_bits_to_f32(d_bound < 0x7c00u ? d_bound : 0x7bffu);
-                        lim = (float)(14 - ((int)(__float_as_uint(top) >> 23) - 127));
-                    }
-                }
-                const float r = mx - ref > lim ? mx - (lim - 4.0f) : ref;
+                const float r = mx - ref > kLim ? mx - (kLim - 4.0f) : ref;
                 const float f = exp2_fast(ref - r);
                 ref = r;
                 l = mul2(l, pack_f2(f, f));
@@ -770,7 +808,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                 split<kBfV>(x0.x, x0.y, w0[t]);
                 split<kBfV>(x1.x, x1.y, w1[t]);
             }
-            // weighted sum of V
+            // weighted sum of V, `down`: without the scales' lift
+            uint64_t down = pack_f2(1.0f, 1.0f);
             auto weigh = [&](auto by_row) {
 #pragma unroll
                 for (int p = 0; p < kPlanesV; ++p) {
@@ -801,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                             lo = mma<kBfV>(of, b0[1], b1[1], lo);
                             to = mma<kBfV>(of, b0[0], b1[0], to);
                         };
-                        if constexpr (by_row.value) {
+                        if constexpr (by_row.value && !kv_quantised(FV)) {
                             // columns 2 j and 2 j + 1 of the sum are rows: each
                             // is kept from the product with the V that it sees
 #pragma unroll 1
@@ -822,11 +861,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
 #pragma unroll
                     for (int u = 0; u < kTilesPerPlane; ++u) {
                         uint64_t(&to)[2] = o[p * kTilesPerPlane + u];
-                        to[0] = add2(to[0], pack_f2(acc[u].x, acc[u].y));
-                        to[1] = add2(to[1], pack_f2(acc[u].z, acc[u].w));
-                        if constexpr (kv_quantised(FV)) {
+                        if constexpr (kv_quantised(FV) && !by_row.value) {
+                            to[0] = add2(to[0], pack_f2(acc[u].x, acc[u].y));
+                            to[1] = add2(to[1], pack_f2(acc[u].z, acc[u].w));
                             to[0] = add2(to[0], pack_f2(low[u].x, low[u].y));
                             to[1] = add2(to[1], pack_f2(low[u].z, low[u].w));
+                        } else if constexpr (kv_quantised(FV)) {
+                            to[0] = fma2(pack_f2(acc[u].x, acc[u].y), down, to[0]);
+                            to[1] = fma2(pack_f2(acc[u].z, acc[u].w), down, to[1]);
+                            to[0] = fma2(pack_f2(low[u].x, low[u].y), down, to[0]);
+                            to[1] = fma2(pack_f2(low[u].z, low[u].w), down, to[1]);
+                        } else {
+                            to[0] = add2(to[0], pack_f2(acc[u].x, acc[u].y));
+                            to[1] = add2(to[1], pack_f2(acc[u].z, acc[u].w));
                         }
                     }
                 }
@@ -834,6 +881,35 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
             if constexpr (MANY && !kv_quantised(FV)) {
                 if (apart) weigh(Flag<true>());
                 else weigh(Flag<false>());
+            } else if constexpr (kv_quantised(FV)) {
+                if (__builtin_expect(!spans, 1)) {
+                    weigh(Flag<false>());
+                } else {
+                    const bool some = (MANY && apart) || (spans & (spans - 1) & 7u) != 0;
+                    const int top = (int)(spans >> 8);
+                    spans &= 7u;
+                    do {  // the next span's scales, lifted
+                        const int span = __ffs(spans) - 1, lift = min(15, (int)(kMost >> 10) - top + 11 * span);
+                        const uint32_t up = power_f16(lift);
+                        const float d = __uint_as_float((uint32_t)(127 - lift) << 23);
+                        down = pack_f2(d, d);
+                        spans &= spans - 1;
+#pragma unroll
+                        for (int t = 0; t < S; ++t)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const uint32_t m =
+                                    MANY && apart ? seen_pair(seen[g], first + t * kStrip + 8 * x + 2 * j) : ~0u;
+#pragma unroll
+                                for (int p = 0; p < kPlanesV; ++p) {
+                                    dv[t][p][x] = scales(t, p, x);
+                                    if (some) dv[t][p][x] = m & in_span(dv[t][p][x], top, span);
+                                    dv[t][p][x] = hmul2(dv[t][p][x], up);
+                                }
+                            }
+                        weigh(Flag<true>());
+                    } while (spans);
+                }
             } else {
                 weigh(Flag<false>());
             }

@@ -84,3 +84,79 @@ def test_rows_beyond_the_table_leave_the_others_theirs(fmt, width, over, n_new, 
         first = max(0, last + 1 - window) if window else 0
         want, tol = ref.attention(xq[i], k, v, first, min(last, cap - 1), np.float64(np.float32(0.125)))
         assert (np.abs(out[i] - want) <= tol).all(), (i, first, last)
+
+
+QUANTISED_V = [("q8_0", "q8_0"), ("q4_0", "q4_0"), ("q8_0", "q4_0")]
+
+
+@pytest.mark.parametrize("fk,fv", QUANTISED_V)
+@pytest.mark.parametrize("n_new", [1, 3])
+@pytest.mark.parametrize("size", [1.0, 1e-3, 1e-4, 3e-5, 1e-5])
+def test_small_values_under_a_peaked_softmax(fk, fv, n_new, size):
+    """V from 1 down to where its f16 scales are subnormal, 4000 positions, a few of which weigh
+    nearly everything."""
+    rng = np.random.default_rng(int(-100 * np.log10(size)) + n_new)
+    k, v = rng.standard_normal((2, 4000, 1, 64))
+    cache, table, k, v = _appended(rng, fk, fv, 4 * k, size * v)
+    _check(cache, table, k, v, rng.standard_normal((n_new, 4, 64)).astype(np.float32))
+
+
+@pytest.mark.parametrize("fk,fv", QUANTISED_V)
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_blocks_of_very_different_size(fk, fv, dim):
+    """The 32-dim blocks of a head differ by up to 2^18, each of them held to its own size; the
+    positions' sizes grow and shrink by 2^4 along the sequence."""
+    rng = np.random.default_rng(dim)
+    n = 700
+    k, v = rng.standard_normal((2, n, 2, dim))
+    size = 2.0 ** np.linspace(2, -16, dim // 32).repeat(32) * 2.0 ** (2 * np.sin(np.arange(n) / 40.0))[:, None, None]
+    cache, table, k, v = _appended(rng, fk, fv, k, size * v)
+    xq = rng.standard_normal((2, 6, dim)).astype(np.float32)
+    _check(cache, table, k, v, xq)
+    _check(cache, table, k, v, xq[:1])
+    _check(cache, table, k, v, xq, window=301)
+
+
+@pytest.mark.parametrize("fk,fv", QUANTISED_V)
+@pytest.mark.parametrize("n_new", [1, 5])
+def test_scales_up_to_the_largest(fk, fv, n_new):
+    """V grows along the sequence from 1e-4 to values whose f16 scales are the largest there are,
+    and falls again; rows of several new positions see different ends of it."""
+    rng = np.random.default_rng(n_new)
+    n = 600
+    k, v = rng.standard_normal((2, n, 1, 64))
+    up = np.concatenate((np.linspace(-4, 5, n - 40), np.linspace(5, 3, 40)))
+    cache, table, k, v = _appended(rng, fk, fv, 0.1 * k, 10.0 ** up[:, None, None] * v)
+    xq = rng.standard_normal((n_new, 3, 64)).astype(np.float32)
+    _check(cache, table, k, v, xq)
+    _check(cache, table, k, v, xq, window=30)
+
+
+@pytest.mark.parametrize("fk,fv", QUANTISED_V)
+def test_a_large_position_that_only_later_rows_see(fk, fv):
+    """Rows that do not see the one huge value keep their precision for small ones."""
+    rng = np.random.default_rng(3)
+    n, n_new = 90, 6
+    k, v = rng.standard_normal((2, n, 1, 64))
+    v[:n - 3] *= 1e-4
+    v[n - 3:] *= 1e5
+    cache, table, k, v = _appended(rng, fk, fv, k, v)
+    _check(cache, table, k, v, rng.standard_normal((n_new, 1, 64)).astype(np.float32))
+
+
+@pytest.mark.parametrize("fk,fv", QUANTISED_V)
+@pytest.mark.parametrize("n_new", [1, 3])
+def test_zero_blocks_and_zero_values(fk, fv, n_new):
+    """Blocks of zeros (a scale of 0) beside others, positions of zeros, and V of zeros alone."""
+    rng = np.random.default_rng(11)
+    n = 300
+    k, v = rng.standard_normal((2, n, 1, 96))
+    v[:, :, 32:64] = 0
+    v[::3] = 0
+    v[150:] *= 1e-4
+    xq = rng.standard_normal((n_new, 3, 96)).astype(np.float32)
+    cache, table, kk, vv = _appended(rng, fk, fv, k, v)
+    out = _check(cache, table, kk, vv, xq)
+    assert not out[:, :, 32:64].any()
+    cache, table, kk, vv = _appended(rng, fk, fv, k, np.zeros_like(v))
+    assert not _attend(cache, table, n, xq).any()
