@@ -509,8 +509,10 @@ typedef struct qmm_attend_args {
  * t over max(0, pos + 1 - window) .. pos of the row's position pos (the row's
  * own position included, so its k and v are appended first). A row that sees
  * no position gives zeros. Cache bytes outside the range, whatever they hold,
- * do not reach the result; one that is Inf or NaN within the range makes the
- * row's outputs Inf or NaN. Sums, the softmax's maximum and its total are
+ * do not reach the result. Within the range a value of K (or a scale) that is Inf
+ * or NaN, or a sum q . k that fp32 cannot hold, makes all of the row's outputs
+ * NaN, whatever the sign; one of V makes the outputs of its dim (of a scale: its
+ * 32 dims) Inf or NaN, whatever the weight. Sums, the softmax's maximum and its total are
  * fp32; q and the weights (times V's scales) enter the tensor cores as sums of
  * 16-bit terms that keep 22 bits of the largest among each 11 binades of scales.
  * The same call gives the same result each time. Scratch as

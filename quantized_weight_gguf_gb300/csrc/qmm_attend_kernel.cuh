@@ -680,7 +680,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
                 for (int t = 0; t < S; ++t)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float2 v = unpack2(mul2(sum[t][x], pack_f2(rs, rs)));
+                        // 0 times a sum that is not finite is NaN: a K value of Inf
+                        // makes the row NaN whatever its sign, not by the signs of
+                        // the query's terms
+                        const uint64_t f = fma2(sum[t][x], pack_f2(0.0f, 0.0f), pack_f2(rs, rs));
+                        const float2 v = unpack2(mul2(sum[t][x], f));
                         s[t][x][0] = v.x;
                         s[t][x][1] = v.y;
                     }

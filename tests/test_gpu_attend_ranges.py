@@ -160,3 +160,77 @@ def test_zero_blocks_and_zero_values(fk, fv, n_new):
     assert not out[:, :, 32:64].any()
     cache, table, kk, vv = _appended(rng, fk, fv, k, np.zeros_like(v))
     assert not _attend(cache, table, n, xq).any()
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("n_new", [1, 3])
+def test_infinite_k_that_is_seen_makes_the_row_nan(fmt, sign, n_new):
+    """Whatever the query's sign and last bits are: exact in 16 bits, rounded up, rounded down. Rows
+    that do not see the position are as without it."""
+    rng = np.random.default_rng(4)
+    n, at = 70, 68
+    k, v = rng.standard_normal((2, n, 1, 64))
+    k[at, 0, 7] = sign * np.inf
+    cache, table, k, v = _appended(rng, fmt, fmt, k, v)
+    assert np.isinf(k[at, 0, 7])
+    xq = rng.standard_normal((n_new, 8, 64)).astype(np.float32)
+    xq[:, :, 7] = np.array([1.0, -1.0, 1.0 + 2.0 ** -13, 1.0 - 2.0 ** -13, -1.0 - 2.0 ** -13, -1.0 + 2.0 ** -13,
+                            0.0, 1.0 + 2.0 ** -23], np.float32)
+    out = _attend(cache, table, n, xq)
+    assert q.qmm_device_status() == 0
+    for i in range(n_new):
+        last = n - n_new + i
+        if last >= at:
+            assert np.isnan(out[i]).all(), i
+        else:
+            want, tol = ref.attention(xq[i], k, v, 0, last, np.float64(np.float32(0.125)))
+            assert (np.abs(out[i] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("fk,fv", [f for f in ref.FORMATS if f[0] != "f16" and f[0] != "bf16"])
+@pytest.mark.parametrize("which", [0, 1])
+def test_infinite_scales(fk, fv, which):
+    """A scale of Inf, which kv_append does not write: in K it makes rows that see the position NaN,
+    in V the 32 dims of its block Inf or NaN and no others."""
+    rng = np.random.default_rng(5)
+    n, at = 50, 20
+    k, v = rng.standard_normal((2, n, 1, 64)).astype(np.float32)
+    table, n_pages = ref.make_table(rng, [n], 16)
+    host = ref.Pages(fk, fv, n_pages, 16, 1, 64)
+    for p in range(n):
+        host.put(0, table[0, p // 16], 0, p % 16, k[p, 0])
+        host.put(1, table[0, p // 16], 0, p % 16, v[p, 0])
+    clean = host.values(1, table[0], n)
+    kk = host.values(0, table[0], n)
+    start = 0 if which == 0 else sum(ref.half_bytes(fk, 64))
+    codes = ref.half_bytes((fk, fv)[which], 64)[0]
+    strip = host.strips[table[0, at // 16], 0, 0]
+    strip[start + codes:start + codes + 64].view(np.uint16).reshape(2, 16)[1, at % 16] = 0x7C00
+    cache = q.KvCache(fk, fv, _dev(host.raw), 16, 1, 64)
+    xq = rng.standard_normal((1, 8, 64)).astype(np.float32)
+    out = _attend(cache, table, n, xq)
+    if which == 0:
+        assert np.isnan(out).all()
+    else:
+        assert not np.isfinite(out[0, :, 32:]).any()
+        want, tol = ref.attention(xq[0], kk, clean, 0, n - 1, np.float64(np.float32(0.125)))
+        assert (np.abs(out[0] - want) <= tol)[:, :32].all()
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_infinite_v_stays_in_its_dim(fmt, sign):
+    rng = np.random.default_rng(6)
+    n = 70
+    k, v = rng.standard_normal((2, n, 1, 64))
+    clean = v.copy()
+    v[33, 0, 9] = sign * np.inf
+    cache, table, k, got = _appended(rng, fmt, fmt, k, v)
+    clean = np.where(np.isinf(got), 0.0, got)
+    xq = rng.standard_normal((1, 8, 64)).astype(np.float32)
+    out = _attend(cache, table, n, xq)
+    assert not np.isfinite(out[0, :, 9]).any()
+    want, tol = ref.attention(xq[0], k, clean, 0, n - 1, np.float64(np.float32(0.125)))
+    others = np.arange(64) != 9
+    assert (np.abs(out[0] - want) <= tol)[:, others].all()
