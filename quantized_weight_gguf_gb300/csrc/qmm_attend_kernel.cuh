@@ -44,7 +44,9 @@
 //
 // The softmax subtracts a reference R per row that is not the exact running
 // maximum: a weight p = 2^(s - R) may grow to 2^15 (2^12 over Q4_0 V, whose
-// scales are larger). Only when a score passes that limit is R moved, to 4 below
+// scales are larger; 2^-12 over BF16 V, whose values may be as large as fp32's,
+// so that thousands of them can be summed before the division by the total).
+// Only when a score passes that limit is R moved, to 4 below
 // the limit for the largest score seen, and the sums rescaled; so a strip
 // normally takes no shuffles.
 //
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
     constexpr int kTilesPerPlane = kv_plane_dims(FV) / 16;  // 2 for quantised V
     // the weights' limit, and the f16 patterns of the smallest and the largest of
     // V's scales that do without a lift (see the top of the file)
-    constexpr float kLim = FV == F_Q4_0 ? 12.0f : 15.0f;
+    constexpr float kLim = kBfV ? -12.0f : FV == F_Q4_0 ? 12.0f : 15.0f;
     constexpr uint32_t kLeast = FV == F_Q4_0 ? 7 << 10 : 4 << 10, kMost = kLeast + (11 << 10) - 1;
     constexpr int S = C::kStep;                             // strips taken at a time
     extern __shared__ __align__(128) uint8_t smem[];

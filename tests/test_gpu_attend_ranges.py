@@ -234,3 +234,14 @@ def test_infinite_v_stays_in_its_dim(fmt, sign):
     want, tol = ref.attention(xq[0], k, clean, 0, n - 1, np.float64(np.float32(0.125)))
     others = np.arange(64) != 9
     assert (np.abs(out[0] - want) <= tol)[:, others].all()
+
+
+@pytest.mark.parametrize("n", [1, 40, 3000])
+@pytest.mark.parametrize("size", [1e-30, 1e34, 1e37])
+def test_bf16_values_near_the_ends_of_fp32(n, size):
+    """Averages of values up to 1e37 (under 5.4 of a deviation) and down to 1e-30."""
+    rng = np.random.default_rng(n)
+    k, v = rng.standard_normal((2, n, 1, 64))
+    cache, table, k, v = _appended(rng, "bf16", "bf16", k, size * v)
+    assert np.isfinite(v).all()
+    _check(cache, table, k, v, rng.standard_normal((1, 4, 64)).astype(np.float32))
