@@ -998,8 +998,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FK, FV, D>::kShape.ctas)
 template <int FK, int FV, int D, bool MANY>
 cudaError_t launch_one(const AttendParams &a, int grid, cudaStream_t s) {
     using C = Cfg<FK, FV, D>;
-    static const cudaError_t ready = cudaFuncSetAttribute(
-        attend_kernel<FK, FV, D, MANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static OncePerDevice once;
+    const cudaError_t ready = allow_smem(once, attend_kernel<FK, FV, D, MANY>, C::kSmem);
     if (ready != cudaSuccess) return ready;
     return launch_programmatic(attend_kernel<FK, FV, D, MANY>, a, grid, kThreads, C::kSmem, s);
 }

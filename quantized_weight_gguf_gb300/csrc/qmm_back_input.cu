@@ -23,7 +23,6 @@
 #include "qmm_internal.h"
 
 #include <algorithm>
-#include <mutex>
 
 namespace qmm {
 
@@ -445,12 +444,8 @@ __global__ void __launch_bounds__(256) back_input_sum_kernel(const float *__rest
 
 template <int FMT>
 cudaError_t launch_bw_t(const BackParams &p, int grid, size_t smem, cudaStream_t s, bool overlap) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(back_input_kernel<FMT>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-    });
+    static OncePerDevice once;
+    const cudaError_t attr_err = allow_smem(once, back_input_kernel<FMT>, 200 * 1024);
     if (attr_err != cudaSuccess) return attr_err;
     if (!overlap) {
         back_input_kernel<FMT><<<grid, kBwThreads, smem, s>>>(p);

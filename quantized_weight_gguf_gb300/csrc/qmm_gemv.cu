@@ -29,7 +29,6 @@
 #include "qmm_internal.h"
 
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 namespace qmm {
@@ -797,12 +796,8 @@ template <int FMT, int UPT, int VAR>
 static cudaError_t launch_e(const GemvHostParams &h, dim3 grid, size_t smem, cudaStream_t s,
                             bool overlap) {
     const GemvParamsOf<FMT, VAR> p = params_of<FMT, VAR>(h);
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(gemv_kernel<FMT, UPT, VAR>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-    });
+    static OncePerDevice once;
+    const cudaError_t attr_err = allow_smem(once, gemv_kernel<FMT, UPT, VAR>, 200 * 1024);
     if (attr_err != cudaSuccess) return attr_err;
     // Every launch is a programmatic dependent of the preceding kernel, so its
     // CTAs are resident by the time that kernel ends. Without `overlap` the

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "qmm_once.h"
+
 namespace qmm {
 
 struct DeviceInfo {
@@ -14,6 +16,18 @@ struct DeviceInfo {
     size_t smem_optin = 0;   // max dynamic shared memory per block
     unsigned int *err = nullptr;  // device error word
 };
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device; the
+// limit belongs to the kernel on one device (`once`: the kernel's own).
+template <class Kernel>
+cudaError_t allow_smem(OncePerDevice &once, Kernel kernel, size_t bytes) {
+    int device = 0;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    return once.run(device, cudaSuccess, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    });
+}
 
 // One GEMV launch: y[j] (+)= sum_i w[j][i] x[i] for j in [j0, j1), one token.
 struct GemvLaunch {

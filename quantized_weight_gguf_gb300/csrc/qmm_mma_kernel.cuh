@@ -1370,9 +1370,9 @@ static cudaError_t launch_t(const Maps &mp, const MmaHostParams &h, const Device
     }
     using C = MmaCfg<BN, mma_ring_bytes(FMT, MODE, GRP),
                      mma_tma_epilogue(MODE, GRP) ? kEpiStageBytes : 0, mma_ssable(FMT, MODE, GRP)>;
+    static OncePerDevice limit;
     static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    static int max_clusters = 0;
+    static int max_clusters = 0;  // the same on every device that is accepted
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kMmaThreads);
     cfg.dynamicSmemBytes = C::kSmem;
@@ -1384,10 +1384,9 @@ static cudaError_t launch_t(const Maps &mp, const MmaHostParams &h, const Device
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    const cudaError_t attr_err = allow_smem(limit, mma_kernel<FMT, BN, MODE, GRP>, C::kSmem);
+    if (attr_err != cudaSuccess) return attr_err;
     std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(mma_kernel<FMT, BN, MODE, GRP>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-        if (attr_err != cudaSuccess) return;
         cudaLaunchConfig_t q = cfg;
         q.gridDim = dim3(2 * (unsigned)(dev.sm_count / 2));
         int n = 0;
@@ -1398,7 +1397,6 @@ static cudaError_t launch_t(const Maps &mp, const MmaHostParams &h, const Device
         }
         max_clusters = std::min(n, mma_clusters(dev));
     });
-    if (attr_err != cudaSuccess) return attr_err;
     const int P = p.pairs * p.tiles_n;
     // grouped products: n_units is an upper bound (the routed count is on the device)
     const int clusters = MODE == 3 ? P : std::min(p.n_units, max_clusters);
