@@ -514,6 +514,12 @@ class KvCache:
         self._read = qmm_kv_read_args(cache=pool)
         self._attend = qmm_attend_args(cache=pool)
 
+    def __setattr__(self, name, value):
+        # the filled-in arguments hold the pool's address and shape
+        if name in self.__dict__:
+            raise AttributeError(f"a cache's {name} does not change")
+        super().__setattr__(name, value)
+
     @classmethod
     def empty(cls, fmt_k, fmt_v, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
               device="cuda"):

@@ -109,3 +109,13 @@ def test_two_host_threads_on_one_stream():
     torch.cuda.synchronize()
     assert len(bad) == 600 and not torch.stack(bad).any()
     assert q.qmm_device_status() == 0
+
+
+def test_a_cache_keeps_its_pool():
+    """The calls' arguments hold the pool's address, so another tensor cannot take its place unseen."""
+    cache = _cache("cpu")
+    with pytest.raises(AttributeError):
+        cache.pages = torch.zeros_like(cache.pages)
+    for name in ("page_size", "n_kv_heads", "head_dim"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, 64)
