@@ -534,8 +534,10 @@ class KvCache:
     def _args(self, template, page_table, lens):
         """A call's arguments with its int32 page_table [n_seqs, max_pages] (rows may be strided)
         and lens [n_seqs], and n_seqs."""
-        self._same_device("page_table", page_table)
-        self._same_device("lens", lens)
+        here = self._device
+        if here < 0 or page_table.get_device() != here or lens.get_device() != here:
+            lens_only = page_table.get_device() == here >= 0
+            self._other_device(*(("lens", lens) if lens_only else ("page_table", page_table)))
         int32 = _torch().int32
         shape, count = page_table.shape, lens.shape
         if len(shape) != 2 or len(count) != 1 or shape[0] != count[0] \
@@ -554,10 +556,8 @@ class KvCache:
         c.n_seqs = n_seqs
         return a, n_seqs
 
-    def _same_device(self, name, t):
-        if t.get_device() != self._device or self._device < 0:
-            raise ValueError(f"{name} ({t.device}) and the cache's pages ({self.pages.device}) must be on "
-                             "one CUDA device")
+    def _other_device(self, name, t):
+        raise ValueError(f"{name} ({t.device}) and the cache's pages ({self.pages.device}) must be on one CUDA device")
 
     def view(self, page_table, lens) -> qmm_kv_cache:
         """The C description of this pool with a call's page_table and lens."""
@@ -569,7 +569,8 @@ class KvCache:
         if len(shape) != 4 or shape[0] != n_seqs or shape[3] != dim or t.dtype is not _torch().float32:
             raise ValueError(f"{name} must be float32 [{n_seqs}, n_new, heads, {dim}], "
                              f"got {tuple(shape)}")
-        self._same_device(name, t)
+        if t.get_device() != self._device:
+            self._other_device(name, t)
         s0, s1, s2, s3 = t.stride()
         n_new, heads = shape[1], shape[2]
         row = s1 if n_new > 1 else s0 if n_seqs > 1 else heads * dim
@@ -612,7 +613,8 @@ def kv_append(cache: KvCache, k, v, page_table, lens, *, q=None, q_out=None, rop
         if len(shape) != 3 or shape[2] != 2 or not rope.is_contiguous() \
                 or rope.dtype is not _torch().float32:
             raise ValueError("rope must be contiguous float32 [positions, n_rot / 2, 2]")
-        cache._same_device("rope", rope)
+        if rope.get_device() != cache._device:
+            cache._other_device("rope", rope)
         a.rope, a.rope_len, a.n_rot = rope.data_ptr(), shape[0], 2 * shape[1]
     a.rope_style = ROPE_STYLES[rope_style] if isinstance(rope_style, str) else int(rope_style)
     a.stream = _stream_of(stream, cache.pages)
@@ -634,7 +636,8 @@ def kv_read(cache: KvCache, page_table, lens, count: int, *, first=None, k=None,
             continue
         if t.shape != shape or not t.is_contiguous() or t.dtype is not torch.float32:
             raise ValueError(f"{name} must be contiguous float32 {shape}")
-        cache._same_device(name, t)
+        if t.get_device() != cache._device:
+            cache._other_device(name, t)
     if k is None:
         k = torch.empty(shape, dtype=torch.float32, device=cache.pages.device)
     if v is None:
@@ -675,7 +678,8 @@ def attend(cache: KvCache, q, page_table, lens, *, scale=None, window=0, out=Non
     if workspace is not None:
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        cache._same_device("workspace", workspace)
+        if workspace.get_device() != cache._device:
+            cache._other_device("workspace", workspace)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     qmm_attend(a)
     if stream is not None:
