@@ -401,8 +401,10 @@ int qmm_matmul_noalloc(const qmm_args *a);
  * Q4_0: codes [head_dim / 32][16 positions][16 bytes] (byte i: dim 2i in the
  *       low nibble, dim 2i + 1 in the high one), scales as for Q8_0;
  *       value = d * (code - 8).
- * Values are quantised over blocks of 32 dims of one position and head like
- * the ggml formats of the same names, from the fp32 row x:
+ * Values are quantised over blocks of 32 dims of one position and head, with
+ * the value ranges of the ggml formats of the same names but a layout and a
+ * rounding of their own (the order of nibbles differs, and codes are taken with
+ * the rounded scale), so packed blocks cannot be moved over. From the fp32 row x:
  * Q8_0: d = f16(max|x| / 127), code = rint(x * (1 / d)) within +-127;
  * Q4_0: m = the value of largest magnitude (the maximum, if the minimum is
  *       no further from 0), d = f16(-m / 8), code = rint(x * (1 / d)) + 8
@@ -429,7 +431,7 @@ typedef struct qmm_kv_cache {
     int64_t n_pages;           /* pages in the pool */
     int64_t page_size;         /* positions per page: a multiple of 16, at most 65536 */
     int64_t n_kv_heads;
-    int64_t head_dim;          /* a multiple of 32, at most 512 */
+    int64_t head_dim;          /* a multiple of 32, at most 512 (qmm_attend: 64, 96, 128, 192 or 256) */
     const int32_t *page_table; /* device, [n_seqs][table_stride] page ids; entries past a sequence's
                                   length are not read */
     int64_t table_stride;      /* int32 entries from one sequence's row to the next, >= max_pages */
@@ -450,7 +452,8 @@ typedef struct qmm_kv_append_args {
     const float *k, *v;        /* device, row r at k + r * k_stride: [n_kv_heads][head_dim] */
     int64_t k_stride, v_stride;/* floats, >= n_kv_heads * head_dim */
     const float *q;            /* device, row r at q + r * q_stride: [n_heads][head_dim]; NULL: none */
-    float *q_out;              /* device, rotated q (zeros for padding rows); may be q itself */
+    float *q_out;              /* device, rotated q (zeros for padding rows); q itself, or memory that
+                                  overlaps none of q, k and v */
     int64_t q_stride, q_out_stride, n_heads;
     const float *rope;         /* device, [rope_len][n_rot / 2][2]: cos and sin of each pair's angle at each
                                   position, 16-byte aligned; NULL: nothing is rotated */

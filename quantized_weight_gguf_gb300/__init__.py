@@ -493,7 +493,8 @@ class KvCache:
     """A pool of cache pages: `pages` is a uint8 CUDA tensor [n_pages, page bytes]
     (one page holds page_size positions of every kv head), the formats are
     "f16", "bf16", "q8_0" or "q4_0" (the same for K and V, or K "q8_0" and V
-    "q4_0"). Page tables and lengths belong to the calls. Every tensor of a call
+    "q4_0"). head_dim is a multiple of 32 up to 512; attend takes 64, 96, 128, 192
+    and 256 of them. Page tables and lengths belong to the calls. Every tensor of a call
     is on the pool's device: the kernels follow the addresses that they are given."""
 
     def __init__(self, fmt_k, fmt_v, pages, page_size: int, n_kv_heads: int, head_dim: int):
@@ -625,8 +626,8 @@ def kv_append(cache: KvCache, k, v, page_table, lens, *, q=None, q_out=None, rop
 def kv_read(cache: KvCache, page_table, lens, count: int, *, first=None, k=None, v=None,
             stream=None):
     """fp32 k and v [n_seqs, count, n_kv_heads, head_dim] of the positions
-    first .. first + count - 1 of every sequence (first None: its last `count`
-    positions); zeros where a sequence has no such position."""
+    first .. first + count - 1 of every sequence (first None or -1: its last
+    `count` positions); zeros where a sequence has no such position."""
     a, n_seqs = cache._args(cache._read, page_table, lens)
     shape = (n_seqs, count, cache.n_kv_heads, cache.head_dim)
     a.first, a.count = -1 if first is None else first, count

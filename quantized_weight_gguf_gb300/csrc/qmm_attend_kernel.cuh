@@ -70,7 +70,7 @@
 // sequence of 131071 (285 MB) 52 us, 81 %, 49 without the arithmetic, 45
 // without the copies. 4-bit caches: the unpacking's integer and fp16
 // instructions, about 300 warp instructions for a strip of 64 dims (1152
-// bytes): 16 sequences with 16 kv heads (129 MB) take 44 us, 43 % (when it was
+// bytes): 16 sequences with 16 kv heads (129 MB) take 46 us, 41 % (when it was
 // 45.4: 41 without the copies, 28 without the arithmetic); the schedulers
 // issue in 59 % of their cycles, the tensor pipe is busy in 31 %. Several new
 // positions: the same instructions, shared by up to eight query rows: 8
