@@ -516,9 +516,10 @@ typedef struct qmm_attend_args {
  * or NaN, or a sum q . k that fp32 cannot hold, makes all of the row's outputs
  * NaN, whatever the sign; one of V makes the outputs of its dim (of a scale: its
  * 32 dims) Inf or NaN, whatever the weight. Sums, the softmax's maximum and its total are
- * fp32; q and the weights (times V's scales) enter the tensor cores as sums of
- * 16-bit terms that keep 22 bits of the largest among each 11 binades of scales.
- * The same call gives the same result each time. Scratch as
+ * fp32. q and the weights enter the tensor cores as sums of 16-bit terms: a weight
+ * is kept to 22 bits or 2^-33 of the row's largest weight, its product with a scale
+ * of V to 22 bits or 2^-25 of the largest weight's, whichever is more; F16 values
+ * of V below 2^-14 are summed to about 2^-37. The same call gives the same result each time. Scratch as
  * for qmm_matmul_ex (calls that can run concurrently pass their own). */
 int qmm_attend(const qmm_attend_args *a);
 
