@@ -528,6 +528,85 @@ int qmm_attend(const qmm_attend_args *a);
  * Host only (reads the device's SM count). */
 size_t qmm_attend_workspace_bytes(const qmm_attend_args *a);
 
+/* ---- Mixture-of-experts layers -------------------------------------------
+ *
+ * The two steps around the router's product (moeflux tests/graph_diff_oracle.rs,
+ * the ops MoeSoftmaxTopK, its normalisation and MoeCombineResidualNTokens, and
+ * the expert matmuls of rullama src/backend/dispatch/mod.rs that
+ * qmm_matmul_experts offers one by one): which experts a position takes, and
+ * what they make of it. */
+
+/* What a router's logits are turned into. */
+typedef enum qmm_score {
+    QMM_SCORE_SOFTMAX = 0,   /* e^l over the sum of all of the position's e^l */
+    QMM_SCORE_SIGMOID = 1    /* 1 / (1 + e^-l) */
+} qmm_score;
+
+typedef struct qmm_route_args {
+    const float *logits;       /* device, row p at logits + p * logits_stride: [n_experts] */
+    int64_t logits_stride;     /* floats, >= n_experts */
+    int64_t n_pos;
+    int64_t n_experts;         /* 1 to 4096 */
+    int64_t top_k;             /* 1 to 64, at most n_experts */
+    int score;                 /* qmm_score */
+    int normalize;             /* the chosen experts' scores are divided by their sum */
+    float scale;               /* multiplies the weights at the end */
+    int32_t *ids;              /* device, [n_pos][top_k] */
+    float *weights;            /* device, [n_pos][top_k] */
+    void *stream;
+    int flags;                 /* 0 */
+} qmm_route_args;
+
+/* The top_k experts of every position by their logits, in descending order,
+ * the lowest index first among equals, and their weights. An expert whose
+ * logit is -Inf is never taken (a router's way to switch one off): where too few
+ * are left, the last slots get id -1 and weight 0. A NaN is not taken either,
+ * and makes the weights of the position's taken experts NaN (with softmax, so
+ * does +Inf). Normalised weights are formed from differences of logits (of their
+ * logarithm, for the logistic function), so they are right where all
+ * scores are tiny. fp32 throughout. One launch; stream-ordered, no
+ * synchronization. */
+int qmm_route_experts(const qmm_route_args *a);
+
+typedef struct qmm_experts_ffn_args {
+    int act;                   /* qmm_act */
+    int fmt, fmt_down;         /* qmm_format of gate and up, and of down: the GGUF ones */
+    const void *w_gate, *w_up; /* device, 16-byte aligned: n_experts slices of n_ff rows of k weights */
+    const void *w_down;        /* device, 16-byte aligned: n_experts slices of k rows of n_ff weights */
+    size_t w_len, w_down_len;  /* bytes the caller holds at w_gate and w_up (each), and at w_down; 0 = not checked */
+    const float *x;            /* device, [n_pos][k] */
+    const int32_t *ids;        /* device, [n_pos][top_k] */
+    const float *weights;      /* device, [n_pos][top_k] */
+    float *y;                  /* device, [n_pos][k]; may be x */
+    int64_t k, n_ff;           /* up to 2^20 */
+    int64_t n_experts;         /* 1 to 4096 */
+    int64_t n_pos, top_k;      /* top_k 1 to 64, n_pos * top_k at most 65535 */
+    int accumulate;            /* 0: y = the sum; else y += the sum (a residual) */
+    void *workspace;           /* device scratch, 256-byte aligned, or NULL (library-owned grow-only buffer) */
+    size_t workspace_bytes;
+    void *stream;
+    int flags;                 /* 0 */
+} qmm_experts_ffn_args;
+
+/* The experts' gated feed-forward network and the sum over a position's experts:
+ *     y[p] (+)= sum_s weights[p][s] * Wd_e (act(Wg_e x[p]) * (Wu_e x[p])),  e = ids[p][s].
+ * ids may repeat in a position (each slot counts). A slot of id -1 adds nothing,
+ * whatever its weight; one of any other id outside [0, n_experts) adds
+ * nothing either and is reported by qmm_device_status (QMM_ERR_BAD_ID). A
+ * position without experts gives zeros. Slices that no id names are not read.
+ * Weights enter the tensor cores as their integer codes (or 16-bit values), x and
+ * the activated products as sums of 16-bit terms: of a value, 22 bits or
+ * 2^-38 of the largest among 32 neighbours, whichever is more (BF16 weights:
+ * 24 bits). Sums are fp32; the same call gives the same result each time. An Inf or NaN in x
+ * makes that position's outputs Inf or NaN. Stream-ordered, no
+ * synchronization; scratch as for qmm_matmul_ex (calls that can run
+ * concurrently pass their own). */
+int qmm_experts_ffn(const qmm_experts_ffn_args *a);
+
+/* Device scratch bytes qmm_experts_ffn needs for *a; 0 when there is nothing to
+ * do or *a is not accepted. Host only. */
+size_t qmm_experts_ffn_workspace_bytes(const qmm_experts_ffn_args *a);
+
 /* Message for the last non-OK status on this host thread ("" if none): the
  * text that the rullama matmul_* dispatchers (src/backend/matmul.rs) carry
  * in their `Err(RullamaError::Inference(..))` returns, here beside the

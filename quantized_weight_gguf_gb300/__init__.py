@@ -8,7 +8,8 @@ functions carry the C names (``qmm_matmul``, ``qmm_matmul_ex``,
 tensors; ``matmul``, ``dequant``, ``matmul_backward_input``,
 ``matmul_experts``, ``matmul_affine``, ``dequant_affine`` and ``matmul_glu``
 are tensor-level conveniences over them, and so are ``KvCache``,
-``kv_append``, ``kv_read`` and ``attend`` over the paged key-value cache.
+``kv_append``, ``kv_read`` and ``attend`` over the paged key-value cache, and
+``route_experts`` and ``experts_ffn`` of mixture-of-experts layers.
 If ``libqmm.so`` has not been built, every call raises: there is no fallback.
 """
 from __future__ import annotations
@@ -37,7 +38,8 @@ EXPORTS = ("qmm_weight_bytes", "qmm_matmul", "qmm_set_stream", "qmm_matmul_ex",
            "qmm_matmul_experts", "qmm_matmul_affine", "qmm_dequant_affine", "qmm_matmul_glu",
            "qmm_glu_workspace_bytes", "qmm_check_bounded_wait", "qmm_matmul_experts_affine",
            "qmm_experts_workspace_bytes", "qmm_kv_page_bytes", "qmm_kv_append", "qmm_kv_read",
-           "qmm_attend", "qmm_attend_workspace_bytes")
+           "qmm_attend", "qmm_attend_workspace_bytes", "qmm_route_experts", "qmm_experts_ffn",
+           "qmm_experts_ffn_workspace_bytes")
 
 
 class QmmError(RuntimeError):
@@ -88,6 +90,25 @@ class qmm_attend_args(ctypes.Structure):
                 ("flags", ctypes.c_int)]
 
 
+class qmm_route_args(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64),
+                ("n_pos", ctypes.c_int64), ("n_experts", ctypes.c_int64), ("top_k", ctypes.c_int64),
+                ("score", ctypes.c_int), ("normalize", ctypes.c_int), ("scale", ctypes.c_float),
+                ("ids", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("stream", ctypes.c_void_p),
+                ("flags", ctypes.c_int)]
+
+
+class qmm_experts_ffn_args(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int), ("fmt", ctypes.c_int), ("fmt_down", ctypes.c_int),
+                ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
+                ("w_len", ctypes.c_size_t), ("w_down_len", ctypes.c_size_t), ("x", ctypes.c_void_p),
+                ("ids", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("k", ctypes.c_int64), ("n_ff", ctypes.c_int64), ("n_experts", ctypes.c_int64),
+                ("n_pos", ctypes.c_int64), ("top_k", ctypes.c_int64), ("accumulate", ctypes.c_int),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("stream", ctypes.c_void_p), ("flags", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -130,6 +151,9 @@ def load(path: str = LIB_PATH):
         "qmm_kv_read": (i, [ctypes.POINTER(qmm_kv_read_args)]),
         "qmm_attend": (i, [ctypes.POINTER(qmm_attend_args)]),
         "qmm_attend_workspace_bytes": (sz, [ctypes.POINTER(qmm_attend_args)]),
+        "qmm_route_experts": (i, [ctypes.POINTER(qmm_route_args)]),
+        "qmm_experts_ffn": (i, [ctypes.POINTER(qmm_experts_ffn_args)]),
+        "qmm_experts_ffn_workspace_bytes": (sz, [ctypes.POINTER(qmm_experts_ffn_args)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -686,3 +710,117 @@ def attend(cache: KvCache, q, page_table, lens, *, scale=None, window=0, out=Non
     if stream is not None:
         _keep_until_done(ws, stream)
     return out
+
+
+# ------------------------------------------------------ mixture of experts ----
+
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+
+
+def qmm_route_experts(args: qmm_route_args) -> int:
+    return _check(load().qmm_route_experts(ctypes.byref(args)))
+
+
+def qmm_experts_ffn(args: qmm_experts_ffn_args) -> int:
+    return _check(load().qmm_experts_ffn(ctypes.byref(args)))
+
+
+def qmm_experts_ffn_workspace_bytes(args: qmm_experts_ffn_args) -> int:
+    return load().qmm_experts_ffn_workspace_bytes(ctypes.byref(args))
+
+
+def _on_device(first, t, name, dtype, shape=None):
+    """Refuses a tensor that is not contiguous `dtype` (of `shape`) on the CUDA device of `first`."""
+    if t.get_device() != first.get_device() or t.get_device() < 0:
+        raise ValueError(f"{name} ({t.device}) must be on one CUDA device with the other tensors ({first.device})")
+    if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be contiguous {dtype} {'' if shape is None else tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+
+
+def _give_scratch(a, need: int, workspace, first, stream):
+    """Fills in a call's scratch: `workspace`, or (as attend does) the kept one of torch's current
+    stream, or a new tensor, which is returned."""
+    ws = None
+    if workspace is None:
+        torch = _torch()
+        if need and stream is None and not torch.cuda.is_current_stream_capturing():
+            workspace = _scratch_of_stream(need, first.device, a.stream)
+        elif need:
+            ws = workspace = torch.empty(need, dtype=torch.uint8, device=first.device)
+    elif workspace.get_device() != first.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {first.device}")
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return ws
+
+
+def route_experts(logits, top_k: int, *, score="softmax", normalize=True, scale=1.0, ids=None, weights=None,
+                  stream=None):
+    """The top_k experts of each row of the router's logits (float32 [n_pos, n_experts], rows may be
+    strided) and their weights: (ids int32 [n_pos, top_k], weights float32 [n_pos, top_k]), in
+    descending order of the logits, the lowest index first among equals. score "softmax" (over all
+    experts) or "sigmoid", divided by the chosen ones' sum with `normalize`, times `scale`. Logits of
+    -inf are never taken: id -1, weight 0 where too few are left."""
+    torch = _torch()
+    if logits.dim() != 2 or logits.dtype is not torch.float32 or logits.get_device() < 0:
+        raise ValueError("logits must be float32 [n_pos, n_experts] on a CUDA device")
+    n_pos, n_experts = logits.shape
+    row, one = logits.stride()
+    if n_experts > 1 and one != 1:
+        raise ValueError("the logits of a row must be adjacent")
+    shape = (n_pos, top_k)
+    if ids is None:
+        ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    else:
+        _on_device(logits, ids, "ids", torch.int32, shape)
+    if weights is None:
+        weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    else:
+        _on_device(logits, weights, "weights", torch.float32, shape)
+    a = qmm_route_args(logits.data_ptr(), row if n_pos > 1 else n_experts, n_pos, n_experts, top_k,
+                       SCORES[score] if isinstance(score, str) else int(score), int(bool(normalize)), scale,
+                       ids.data_ptr(), weights.data_ptr(), _stream_of(stream, logits), 0)
+    qmm_route_experts(a)
+    return ids, weights
+
+
+def experts_ffn(act, fmt, w_gate, w_up, fmt_down, w_down, x, ids, weights, k: int, n_ff: int, n_experts: int, *,
+                y=None, accumulate=False, workspace=None, stream=None):
+    """The gated feed-forward network ("swiglu" / "geglu") of the experts that ids (int32 [n_pos,
+    top_k], -1: none) name, weighted and summed: x float32 [n_pos, k] to y float32 [n_pos, k] (the
+    given y when passed, which may be x; added to with `accumulate`). w_gate and w_up hold n_experts
+    slices of n_ff rows of k weights in `fmt`, w_down of k rows of n_ff weights in `fmt_down`, uint8.
+    Scratch is `workspace` (uint8) when given; else as for attend."""
+    torch = _torch()
+    if x.dim() == 1:
+        x = x.unsqueeze(0)
+    if ids.dim() == 1:
+        ids, weights = ids.unsqueeze(0), weights.reshape(1, -1)
+    n_pos, top_k = ids.shape
+    _on_device(x, x, "x", torch.float32, (n_pos, k))
+    _on_device(x, ids, "ids", torch.int32)
+    _on_device(x, weights, "weights", torch.float32, (n_pos, top_k))
+    for name, w in (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)):
+        if w.get_device() != x.get_device() or not w.is_contiguous():
+            raise ValueError(f"{name} ({w.device}) must be contiguous and on x's device ({x.device})")
+    w_len = w_gate.numel() * w_gate.element_size()
+    if w_up.numel() * w_up.element_size() != w_len:
+        raise ValueError("w_gate and w_up must have the same size")
+    if y is None:
+        y = (torch.zeros if accumulate else torch.empty)((n_pos, k), dtype=torch.float32, device=x.device)
+    else:
+        _on_device(x, y, "y", torch.float32)
+        if y.numel() != n_pos * k:
+            raise ValueError(f"y must have x's {n_pos} x {k} values")
+    a = qmm_experts_ffn_args(
+        ACTS[act] if isinstance(act, str) else int(act), _fmt(fmt), _fmt(fmt_down), w_gate.data_ptr(),
+        w_up.data_ptr(), w_down.data_ptr(), w_len, w_down.numel() * w_down.element_size(), x.data_ptr(),
+        ids.data_ptr(), weights.data_ptr(), y.data_ptr(), k, n_ff, n_experts, n_pos, top_k,
+        int(bool(accumulate)), None, 0, _stream_of(stream, x), 0)
+    ws = _give_scratch(a, qmm_experts_ffn_workspace_bytes(a), workspace, x, stream)
+    qmm_experts_ffn(a)
+    if stream is not None:
+        _keep_until_done(ws, stream)
+    return y

@@ -1,0 +1,344 @@
+// qmm_experts.cu -- the experts' feed-forward network over packed weights:
+//     y[p] (+)= sum_s w[p][s] Wd_e (act(Wg_e x[p]) * (Wu_e x[p])),  e = ids[p][s].
+// Four launches, each a programmatic dependent of the one before: the pairs
+// (position, slot) are sorted by expert while x becomes 16-bit terms (one
+// launch); the gate and up products with the activation; the down product, a
+// row per pair; the sum of each position's rows. This file holds the first and
+// the last, and the host side.
+#include <algorithm>
+
+#include "qmm_experts.h"
+#include "qmm_experts_frag.cuh"
+
+namespace qmm {
+
+namespace experts {
+
+// one translation unit per group of formats
+#define QMM_EXPERTS_FORMAT(FMT) \
+    extern template cudaError_t launch_product<FMT>(bool, int, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
+QMM_EXPERTS_FORMAT(F_BF16)
+QMM_EXPERTS_FORMAT(F_F16)
+QMM_EXPERTS_FORMAT(F_Q4_0)
+QMM_EXPERTS_FORMAT(F_Q4_K)
+QMM_EXPERTS_FORMAT(F_Q6_K)
+QMM_EXPERTS_FORMAT(F_Q8_0)
+QMM_EXPERTS_FORMAT(F_Q5_0)
+#undef QMM_EXPERTS_FORMAT
+
+namespace {
+
+constexpr int kPrepareThreads = 256, kPrepareWarps = kPrepareThreads / 32;
+
+struct PrepareParams {
+    const int32_t *ids;
+    int pairs, n_experts, columns;
+    Tile *tiles;
+    int *n_tiles, *order;
+    const float *x;
+    int n_pos, k, x_blocks, bf16;
+    uint8_t *terms;
+    float2 *scales;
+    int64_t x_row_bytes;
+    unsigned int *err;
+};
+
+// Exclusive prefix sum of `v` over the block's threads; *total: the sum of all.
+__device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += a;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < kPrepareWarps; ++w) {
+        before += w < warp ? warp_sums[w] : 0;
+        all += warp_sums[w];
+    }
+    __syncthreads();
+    *total = all;
+    return before + inc - v;
+}
+
+// The pairs in the order of their experts, and the tiles of up to `columns` of
+// them. Which place a pair takes among its expert's is up to the atomics; no
+// result depends on it (a pair's sums are its column's alone).
+__device__ void sort_pairs(const PrepareParams &p) {
+    __shared__ int count[kMaxExperts];
+    __shared__ int warp_sums[kPrepareWarps];
+    const int tid = threadIdx.x;
+    for (int e = tid; e < p.n_experts; e += kPrepareThreads) count[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < p.pairs; i += kPrepareThreads) {
+        const int e = p.ids[i];
+        if (e >= 0 && e < p.n_experts) atomicAdd(&count[e], 1);
+        else if (e != -1) record_error(p.err, DERR_BAD_ID);
+    }
+    __syncthreads();
+    const int per = (p.n_experts + kPrepareThreads - 1) / kPrepareThreads;
+    const int e0 = min(tid * per, p.n_experts), e1 = min(e0 + per, p.n_experts);
+    int rows = 0, tiles = 0;
+    for (int e = e0; e < e1; ++e) {
+        rows += count[e];
+        tiles += (count[e] + p.columns - 1) / p.columns;
+    }
+    int all_rows, all_tiles;
+    int row = block_scan(rows, warp_sums, &all_rows);
+    int tile = block_scan(tiles, warp_sums, &all_tiles);
+    for (int e = e0; e < e1; ++e) {
+        const int n = count[e];
+        count[e] = row;  // becomes the place of the expert's next pair
+        for (int at = 0; at < n; at += p.columns) {
+            Tile x;
+            x.expert = e;
+            x.start = row + at;
+            x.count = min(p.columns, n - at);
+            x.pad = 0;
+            p.tiles[tile++] = x;
+        }
+        row += n;
+    }
+    if (tid == 0) *p.n_tiles = all_tiles;
+    __syncthreads();
+    for (int i = tid; i < p.pairs; i += kPrepareThreads) {
+        const int e = p.ids[i];
+        if (e >= 0 && e < p.n_experts) p.order[atomicAdd(&count[e], 1)] = i;
+    }
+}
+
+// Block 0 sorts the pairs, the others turn x into terms, a block of 32 values
+// per warp.
+__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ PrepareParams p) {
+    pdl_wait_prev();
+    if (blockIdx.x == 0) {
+        sort_pairs(p);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const int64_t all = (int64_t)p.n_pos * p.x_blocks, step = (int64_t)(gridDim.x - 1) * kPrepareWarps;
+    for (int64_t i = (int64_t)(blockIdx.x - 1) * kPrepareWarps + (threadIdx.x >> 5); i < all; i += step) {
+        const int64_t row = i / p.x_blocks;
+        const int b = (int)(i % p.x_blocks), e = 32 * b + lane;
+        const float v = e < p.k ? p.x[row * p.k + e] : 0.0f;
+        const float2 s = put_block(v, lane, p.bf16, p.terms + row * p.x_row_bytes + (int64_t)b * 64 * (p.bf16 ? 3 : 2));
+        if (lane == 0) p.scales[i] = s;
+    }
+}
+
+struct SumParams {
+    const float *rows;       // [pairs][k]
+    const int32_t *ids;
+    float *y;
+    int64_t values;          // n_pos * k
+    int k, top_k, n_experts;
+    int accumulate;
+};
+constexpr int kSumThreads = 256;
+
+// y[p] (+)= the sum of the position's rows, slots in order; slots without an
+// expert have no row. V values per thread.
+template <int V>
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant__ SumParams p) {
+    pdl_wait_prev();
+    pdl_launch_dependents();
+    const int64_t at = ((int64_t)blockIdx.x * kSumThreads + threadIdx.x) * V;
+    if (at >= p.values) return;
+    const int64_t pos = at / p.k;
+    const int j = (int)(at % p.k);
+    float s[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = 0.0f;
+    for (int t = 0; t < p.top_k; ++t) {
+        const int e = p.ids[pos * p.top_k + t];
+        if (e < 0 || e >= p.n_experts) continue;
+        const float *r = p.rows + (pos * p.top_k + t) * p.k + j;
+        if constexpr (V == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(r);
+            s[0] += v.x;
+            s[1] += v.y;
+            s[2] += v.z;
+            s[3] += v.w;
+        } else {
+            s[0] += *r;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (p.accumulate) s[i] += p.y[at + i];
+        p.y[at + i] = s[i];
+    }
+}
+
+template <class P>
+cudaError_t launch_next(void (*kernel)(P), const P &p, int64_t grid, int threads, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Blocks of 32 of a row of terms, padded to the largest chunk.
+int padded_blocks(int k) { return (k + 255) / 256 * 8; }
+
+// Columns of a tile: the narrowest of 8, 16 and 32 that holds an expert's rows
+// when every expert is chosen equally often.
+int columns_of(const ExpertsFfn &f) {
+    const int64_t rows = (f.n_pos * f.top_k + f.n_experts - 1) / f.n_experts;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
+
+// The most tiles that the ids can make: each expert that is chosen leaves at
+// most one tile that is not full.
+int64_t max_tiles(const ExpertsFfn &f, int columns) {
+    const int64_t pairs = f.n_pos * f.top_k;
+    return std::min<int64_t>(pairs, pairs / columns + std::min<int64_t>(f.n_experts, pairs));
+}
+
+// The parts of the workspace.
+struct Scratch {
+    size_t tiles, n_tiles, order, x, x_scale, h, h_scale, out, bytes;
+    int columns;
+    int64_t x_row_bytes, h_row_bytes;
+    int x_blocks, h_blocks;
+};
+Scratch scratch_of(const ExpertsFfn &f) {
+    Scratch s = {};
+    const size_t pairs = (size_t)(f.n_pos * f.top_k);
+    s.columns = columns_of(f);
+    s.x_blocks = padded_blocks(f.k);
+    s.h_blocks = padded_blocks(f.n_ff);
+    s.x_row_bytes = (int64_t)s.x_blocks * frag_bytes(f.fmt);
+    s.h_row_bytes = (int64_t)s.h_blocks * frag_bytes(f.fmt_down);
+    size_t at = 0;
+    auto part = [&](size_t bytes) {
+        const size_t here = at;
+        at += round256(bytes);
+        return here;
+    };
+    s.n_tiles = part(sizeof(int));
+    s.tiles = part(sizeof(Tile) * (size_t)max_tiles(f, s.columns));
+    s.order = part(sizeof(int) * pairs);
+    s.x = part((size_t)s.x_row_bytes * (size_t)f.n_pos);
+    s.x_scale = part(sizeof(float2) * (size_t)s.x_blocks * (size_t)f.n_pos);
+    s.h = part((size_t)s.h_row_bytes * pairs);
+    s.h_scale = part(sizeof(float2) * (size_t)s.h_blocks * pairs);
+    s.out = part(sizeof(float) * (size_t)f.k * pairs);
+    s.bytes = at;
+    return s;
+}
+
+cudaError_t product(int fmt, bool down, int columns, const ProductParams &p, int tiles, const DeviceInfo &dev,
+                    cudaStream_t s) {
+    switch (fmt) {
+    case F_BF16: return launch_product<F_BF16>(down, columns, p, tiles, dev, s);
+    case F_F16: return launch_product<F_F16>(down, columns, p, tiles, dev, s);
+    case F_Q4_0: return launch_product<F_Q4_0>(down, columns, p, tiles, dev, s);
+    case F_Q4_K: return launch_product<F_Q4_K>(down, columns, p, tiles, dev, s);
+    case F_Q6_K: return launch_product<F_Q6_K>(down, columns, p, tiles, dev, s);
+    case F_Q8_0: return launch_product<F_Q8_0>(down, columns, p, tiles, dev, s);
+    default: return launch_product<F_Q5_0>(down, columns, p, tiles, dev, s);
+    }
+}
+
+}  // namespace
+
+}  // namespace experts
+
+size_t experts_ffn_workspace_bytes(const ExpertsFfn &f) { return experts::scratch_of(f).bytes; }
+
+cudaError_t launch_experts_ffn(const ExpertsFfn &f, const DeviceInfo &dev, cudaStream_t s) {
+    using namespace experts;
+    const Scratch l = scratch_of(f);
+    uint8_t *const ws = static_cast<uint8_t *>(f.workspace);
+    const int pairs = (int)(f.n_pos * f.top_k);
+    const int tiles = (int)max_tiles(f, l.columns);
+
+    PrepareParams a = {};
+    a.ids = f.ids;
+    a.pairs = pairs;
+    a.n_experts = f.n_experts;
+    a.columns = l.columns;
+    a.tiles = reinterpret_cast<Tile *>(ws + l.tiles);
+    a.n_tiles = reinterpret_cast<int *>(ws + l.n_tiles);
+    a.order = reinterpret_cast<int *>(ws + l.order);
+    a.x = f.x;
+    a.n_pos = (int)f.n_pos;
+    a.k = f.k;
+    a.x_blocks = l.x_blocks;
+    a.bf16 = f.fmt == F_BF16;
+    a.terms = ws + l.x;
+    a.scales = reinterpret_cast<float2 *>(ws + l.x_scale);
+    a.x_row_bytes = l.x_row_bytes;
+    a.err = dev.err;
+    const int64_t warps = f.n_pos * l.x_blocks;
+    const int64_t blocks = std::min<int64_t>((warps + kPrepareWarps - 1) / kPrepareWarps, (int64_t)dev.sm_count * 8);
+    cudaError_t e = launch_next(prepare_kernel, a, 1 + blocks, kPrepareThreads, s);
+    if (e != cudaSuccess) return e;
+
+    ProductParams p = {};
+    p.w[0] = f.gate;
+    p.w[1] = f.up;
+    p.row_bytes = f.row_bytes;
+    p.slice_bytes = f.row_bytes * f.n_ff;
+    p.rows = f.n_ff;
+    p.k = f.k;
+    p.blocks = (f.k + 31) / 32;
+    p.x = a.terms;
+    p.x_scale = a.scales;
+    p.x_row_bytes = l.x_row_bytes;
+    p.x_blocks = l.x_blocks;
+    p.tiles = a.tiles;
+    p.n_tiles = a.n_tiles;
+    p.order = a.order;
+    p.top_k = f.top_k;
+    p.weights = f.weights;
+    p.h = ws + l.h;
+    p.h_scale = reinterpret_cast<float2 *>(ws + l.h_scale);
+    p.h_row_bytes = l.h_row_bytes;
+    p.h_blocks = l.h_blocks;
+    p.h_bf16 = f.fmt_down == F_BF16;
+    p.act = f.act;
+    e = product(f.fmt, false, l.columns, p, tiles, dev, s);
+    if (e != cudaSuccess) return e;
+
+    p.w[0] = p.w[1] = f.down;
+    p.row_bytes = f.down_row_bytes;
+    p.slice_bytes = f.down_row_bytes * f.k;
+    p.rows = f.k;
+    p.k = f.n_ff;
+    p.blocks = (f.n_ff + 31) / 32;
+    p.x = p.h;
+    p.x_scale = p.h_scale;
+    p.x_row_bytes = l.h_row_bytes;
+    p.x_blocks = l.h_blocks;
+    p.out = reinterpret_cast<float *>(ws + l.out);
+    e = product(f.fmt_down, true, l.columns, p, tiles, dev, s);
+    if (e != cudaSuccess) return e;
+
+    SumParams q = {};
+    q.rows = p.out;
+    q.ids = f.ids;
+    q.y = f.y;
+    q.values = f.n_pos * f.k;
+    q.k = f.k;
+    q.top_k = f.top_k;
+    q.n_experts = f.n_experts;
+    q.accumulate = f.accumulate;
+    if (f.k % 4 == 0)
+        return launch_next(sum_kernel<4>, q, (q.values / 4 + kSumThreads - 1) / kSumThreads, kSumThreads, s);
+    return launch_next(sum_kernel<1>, q, (q.values + kSumThreads - 1) / kSumThreads, kSumThreads, s);
+}
+
+}  // namespace qmm

@@ -1,0 +1,9 @@
+// qmm_experts_inst_16.cu -- the experts' products over weights of these formats.
+#include "qmm_experts_kernel.cuh"
+
+namespace qmm {
+namespace experts {
+template cudaError_t launch_product<F_BF16>(bool, int, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
+template cudaError_t launch_product<F_F16>(bool, int, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
+}  // namespace experts
+}  // namespace qmm

@@ -1,0 +1,8 @@
+// qmm_experts_inst_k6.cu -- the experts' products over weights of these formats.
+#include "qmm_experts_kernel.cuh"
+
+namespace qmm {
+namespace experts {
+template cudaError_t launch_product<F_Q6_K>(bool, int, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
+}  // namespace experts
+}  // namespace qmm
