@@ -607,6 +607,64 @@ int qmm_experts_ffn(const qmm_experts_ffn_args *a);
  * do or *a is not accepted. Host only. */
 size_t qmm_experts_ffn_workspace_bytes(const qmm_experts_ffn_args *a);
 
+/* ---- Linear attention ----------------------------------------------------
+ *
+ * Attention whose memory is one matrix per head, with a decay for each head
+ * (moeflux tests/graph_diff_oracle.rs, GatedDeltaNetStep and its chunked form,
+ * without their delta rule): the layers that stand beside those of qmm_attend in
+ * hybrid models. One call serves prompts and single tokens:
+ *     S_t = e^(g_t) S_(t-1) + k_t v_t^T,    o_t = scale * S_t^T q_t
+ * for every sequence and head, rows t in order. Heads share q and k in groups:
+ * head h takes those of q / k head h / (n_heads / n_qk_heads).
+ *
+ * Rows: as for the cache calls above, a call works on the last n_new positions of every
+ * sequence; row i of sequence s is position lens[s] - n_new + i, lens counts them
+ * already, rows of negative position are padding: their q, k, v and decays are
+ * not used and their outputs are zeros. A sequence whose first position is
+ * among the rows (lens[s] <= n_new) starts from a state of zeros, whatever
+ * `state` holds; one of no position (lens[s] <= 0) keeps its state. Without lens
+ * every row is a position and every sequence continues from its state. */
+typedef struct qmm_linear_args {
+    const float *q, *k;        /* device, row r of sequence s at q + (s * n_new + r) * q_stride: [n_qk_heads][dk] */
+    const float *v;            /* device, likewise: [n_heads][dv] */
+    int64_t q_stride, k_stride, v_stride; /* floats, >= the heads' floats */
+    const float *decay;        /* device, logarithms g of the factors: row at decay + row * decay_stride: [n_heads];
+                                  with decay_stride 0 one [n_heads] for all rows */
+    int64_t decay_stride;
+    const float *state;        /* device, [n_seqs][n_heads][dk][dv], 16-byte aligned */
+    float *state_out;          /* device, likewise: the states after the last row; state itself, or memory that
+                                  overlaps none of the inputs */
+    float *out;                /* device, row at out + row * out_stride: [n_heads][dv]; overlaps no input */
+    int64_t out_stride;
+    const int32_t *lens;       /* device, [n_seqs], or NULL */
+    int64_t n_seqs, n_new;     /* n_new >= 1 */
+    int64_t n_heads, n_qk_heads; /* n_heads a multiple of n_qk_heads; n_seqs * n_heads at most 2^24 */
+    int64_t dk, dv;            /* dk 32, 64, 96 or 128; dv a multiple of 32 up to 256 */
+    float scale;
+    void *workspace;           /* device scratch, 256-byte aligned, or NULL (library-owned grow-only buffer) */
+    size_t workspace_bytes;
+    void *stream;
+    int flags;                 /* 0 */
+} qmm_linear_args;
+
+/* Decays are at most 0: greater ones count as 0, and -Inf clears the state
+ * before its row (so do decays below -110, whose factor fp32 holds as 0). A NaN decay or a
+ * k that is not finite makes the head's rows from its own on, and its state, NaN;
+ * a v that is not finite those of its dim; a q that is not finite its row's outputs Inf or NaN.
+ * Rows before are not touched by it. Sums and states are fp32 (sums of decays 64 bits). Up to 8 rows are taken one by one in
+ * fp32; more in chunks of 32 on the tensor cores, where q, k, v and the state enter as two fp16
+ * terms: of a value, 22 bits or 2^-38 of the largest of its row (q, k), of its dim in
+ * the chunk (v, and v times its row's largest k as it adds to the state) or of its dim of the state, whichever is
+ * more; of a score q . k, 22 bits or 2^-31 of
+ * the product of the row's largest q and the chunk's largest k. The same call
+ * gives the same result each time. Stream-ordered, no synchronization; scratch
+ * as for qmm_matmul_ex (calls that can run concurrently pass their own). */
+int qmm_linear_attend(const qmm_linear_args *a);
+
+/* Device scratch bytes qmm_linear_attend needs for *a; 0 when it needs none or
+ * *a is not accepted. Host only (reads the device's SM count). */
+size_t qmm_linear_attend_workspace_bytes(const qmm_linear_args *a);
+
 /* Message for the last non-OK status on this host thread ("" if none): the
  * text that the rullama matmul_* dispatchers (src/backend/matmul.rs) carry
  * in their `Err(RullamaError::Inference(..))` returns, here beside the

@@ -8,8 +8,9 @@ functions carry the C names (``qmm_matmul``, ``qmm_matmul_ex``,
 tensors; ``matmul``, ``dequant``, ``matmul_backward_input``,
 ``matmul_experts``, ``matmul_affine``, ``dequant_affine`` and ``matmul_glu``
 are tensor-level conveniences over them, and so are ``KvCache``,
-``kv_append``, ``kv_read`` and ``attend`` over the paged key-value cache, and
-``route_experts`` and ``experts_ffn`` of mixture-of-experts layers.
+``kv_append``, ``kv_read`` and ``attend`` over the paged key-value cache, 
+``route_experts`` and ``experts_ffn`` of mixture-of-experts layers, and
+``linear_attend``.
 If ``libqmm.so`` has not been built, every call raises: there is no fallback.
 """
 from __future__ import annotations
@@ -39,7 +40,7 @@ EXPORTS = ("qmm_weight_bytes", "qmm_matmul", "qmm_set_stream", "qmm_matmul_ex",
            "qmm_glu_workspace_bytes", "qmm_check_bounded_wait", "qmm_matmul_experts_affine",
            "qmm_experts_workspace_bytes", "qmm_kv_page_bytes", "qmm_kv_append", "qmm_kv_read",
            "qmm_attend", "qmm_attend_workspace_bytes", "qmm_route_experts", "qmm_experts_ffn",
-           "qmm_experts_ffn_workspace_bytes")
+           "qmm_experts_ffn_workspace_bytes", "qmm_linear_attend", "qmm_linear_attend_workspace_bytes")
 
 
 class QmmError(RuntimeError):
@@ -109,6 +110,17 @@ class qmm_experts_ffn_args(ctypes.Structure):
                 ("stream", ctypes.c_void_p), ("flags", ctypes.c_int)]
 
 
+class qmm_linear_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("decay", ctypes.c_void_p), ("decay_stride", ctypes.c_int64), ("state", ctypes.c_void_p),
+                ("state_out", ctypes.c_void_p), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("n_seqs", ctypes.c_int64), ("n_new", ctypes.c_int64),
+                ("n_heads", ctypes.c_int64), ("n_qk_heads", ctypes.c_int64), ("dk", ctypes.c_int64),
+                ("dv", ctypes.c_int64), ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("stream", ctypes.c_void_p), ("flags", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -154,6 +166,8 @@ def load(path: str = LIB_PATH):
         "qmm_route_experts": (i, [ctypes.POINTER(qmm_route_args)]),
         "qmm_experts_ffn": (i, [ctypes.POINTER(qmm_experts_ffn_args)]),
         "qmm_experts_ffn_workspace_bytes": (sz, [ctypes.POINTER(qmm_experts_ffn_args)]),
+        "qmm_linear_attend": (i, [ctypes.POINTER(qmm_linear_args)]),
+        "qmm_linear_attend_workspace_bytes": (sz, [ctypes.POINTER(qmm_linear_args)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -824,3 +838,75 @@ def experts_ffn(act, fmt, w_gate, w_up, fmt_down, w_down, x, ids, weights, k: in
     if stream is not None:
         _keep_until_done(ws, stream)
     return y
+
+
+# -------------------------------------------------------- linear attention ----
+
+def qmm_linear_attend(args: qmm_linear_args) -> int:
+    return _check(load().qmm_linear_attend(ctypes.byref(args)))
+
+
+def qmm_linear_attend_workspace_bytes(args: qmm_linear_args) -> int:
+    return load().qmm_linear_attend_workspace_bytes(ctypes.byref(args))
+
+
+def _head_rows(name, t, first):
+    """Row stride of fp32 rows [n_seqs, n_new, heads, dim] on the device of `first`."""
+    if t.dim() != 4 or t.dtype is not _torch().float32 or t.get_device() != first.get_device() or t.get_device() < 0:
+        raise ValueError(f"{name} must be float32 [n_seqs, n_new, heads, dim] on one CUDA device with the other "
+                         f"tensors, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    n_seqs, n_new, heads, dim = t.shape
+    s0, s1, s2, s3 = t.stride()
+    row = s1 if n_new > 1 else s0 if n_seqs > 1 else heads * dim
+    if (dim > 1 and s3 != 1) or (heads > 1 and s2 != dim) or (n_new > 1 and n_seqs > 1 and s0 != n_new * s1):
+        raise ValueError(f"{name}: the heads of a row must be adjacent and rows equally spaced")
+    return row
+
+
+def linear_attend(q, k, v, decay, state, lens=None, *, scale=None, out=None, state_out=None, workspace=None,
+                  stream=None):
+    """Linear attention with a decay for each head, S = e^decay S + k v^T and out = scale S^T q row by row:
+    q, k float32 [n_seqs, n_new, n_qk_heads, dk], v [n_seqs, n_new, n_heads, dv] (rows may be strided), decay
+    [n_seqs, n_new, n_heads] (rows may be strided) or [n_heads], state [n_seqs, n_heads, dk, dv], scale
+    1 / sqrt(dk) unless given. With `lens` (int32 [n_seqs], the new rows counted) rows are each sequence's last
+    positions, and a sequence that begins among them begins at a state of zeros. Returns out, shaped like v (the
+    given one when passed); the states after the last row go to state_out, by default over `state`. Scratch is
+    `workspace` (uint8) when given; else as for attend."""
+    torch = _torch()
+    q_row, k_row, v_row = _head_rows("q", q, v), _head_rows("k", k, v), _head_rows("v", v, v)
+    n_seqs, n_new, n_heads, dv = v.shape
+    n_qk, dk = q.shape[2:]
+    if k.shape != q.shape or q.shape[:2] != v.shape[:2]:
+        raise ValueError(f"q, k and v must have the same rows, and q and k the same heads: got {tuple(q.shape)}, "
+                         f"{tuple(k.shape)}, {tuple(v.shape)}")
+    if decay.dtype is not torch.float32 or decay.get_device() != v.get_device():
+        raise ValueError("decay must be float32 on the other tensors' device")
+    if decay.shape == (n_heads,):
+        decay_row = 0
+        if n_heads > 1 and decay.stride(0) != 1:
+            raise ValueError("decay's heads must be adjacent")
+    elif decay.shape == v.shape[:3]:
+        decay_row = _head_rows("decay", decay.unsqueeze(-1), v)
+    else:
+        raise ValueError(f"decay must be {tuple(v.shape[:3])} or ({n_heads},), got {tuple(decay.shape)}")
+    shape = (n_seqs, n_heads, dk, dv)
+    _on_device(v, state, "state", torch.float32, shape)
+    if state_out is None:
+        state_out = state
+    else:
+        _on_device(v, state_out, "state_out", torch.float32, shape)
+    if lens is not None:
+        _on_device(v, lens, "lens", torch.int32, (n_seqs,))
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    elif out.shape != v.shape:
+        raise ValueError("out must have v's shape")
+    a = qmm_linear_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, k_row, v_row, decay.data_ptr(), decay_row,
+                        state.data_ptr(), state_out.data_ptr(), out.data_ptr(), _head_rows("out", out, v),
+                        None if lens is None else lens.data_ptr(), n_seqs, n_new, n_heads, n_qk, dk, dv,
+                        dk ** -0.5 if scale is None else scale, None, 0, _stream_of(stream, v), 0)
+    ws = _give_scratch(a, qmm_linear_attend_workspace_bytes(a), workspace, v, stream)
+    qmm_linear_attend(a)
+    if stream is not None:
+        _keep_until_done(ws, stream)
+    return out

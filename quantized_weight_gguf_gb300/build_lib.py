@@ -21,7 +21,8 @@ SOURCES = ["qmm_mma_inst_q4k.cu", "qmm_mma_inst_16.cu", "qmm_mma_inst_q.cu", "qm
            "qmm_back_input.cu", "qmm_attend_inst_bf16.cu", "qmm_attend_inst_f16.cu",
            "qmm_attend_inst_q8.cu", "qmm_attend_inst_q4.cu", "qmm_attend_inst_q8q4.cu", "qmm_attend.cu", "qmm_kv.cu", "qmm_kv_api.cu",
            "qmm_experts_inst_16.cu", "qmm_experts_inst_q4.cu", "qmm_experts_inst_k4.cu", "qmm_experts_inst_k6.cu",
-           "qmm_experts_inst_q8.cu", "qmm_experts.cu", "qmm_route.cu", "qmm_experts_api.cu"]
+           "qmm_experts_inst_q8.cu", "qmm_experts.cu", "qmm_route.cu", "qmm_experts_api.cu",
+           "qmm_linear_chunk.cu", "qmm_linear.cu", "qmm_linear_api.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 

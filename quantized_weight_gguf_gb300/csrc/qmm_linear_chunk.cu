@@ -1,0 +1,648 @@
+// qmm_linear_chunk.cu -- linear attention over many rows of a sequence, in
+// chunks of C = 32. With G_i the sum of the chunk's decays up to row i and S the
+// state before the chunk,
+//     o_i = e^(G_i) S^T q_i + sum_(j <= i) e^(G_i - G_j) (q_i . k_j) v_j,
+//     S' = e^(G_C) S + sum_j e^(G_C - G_j) k_j v_j^T :
+// four products per chunk, on the tensor cores.
+//
+// A warp owns 16 dims of v for the whole run and keeps S^T (16 x dk) as the
+// accumulator fragments of m16n8k16, which are A fragments of S^T Q^T as they
+// stand. The 32 x 32 scores are shared: one 16 x 8 tile a warp. fp32 values enter
+// as two fp16 terms (22 bits) under powers of two per row of q and k and per
+// dim of v and S, three products of terms each; accumulators start fresh after at most
+// 32 values of depth and the small products come first, since the
+// tensor cores cut what they add. Sums of decays are formed in 64 bits and kept as
+// two floats, so that differences of long sums stay exact.
+//
+// Bound by the tensor cores: per row and head 60 clocks' worth of mma.sync on an
+// SM quarter at dk = dv = 128, against 2 KB of rows. A prompt too short of
+// sequences and heads to fill the GPU is cut into segments: their own end states
+// first (one product of the four), a scan over the segments, then everything.
+#include "qmm_device.cuh"
+#include "qmm_linear.h"
+
+#include <cuda_fp16.h>
+
+namespace qmm {
+
+namespace linear {
+
+namespace {
+
+constexpr int C = kChunk;
+constexpr int kMaxWarps = 8;
+
+struct ChunkParams {
+    Linear l;
+    Split split;
+    float *starts;        // [segments][n_seqs][n_heads][dk][dv]: the state before each segment (one segment: not used)
+    float *seg_decay;     // [segments][n_seqs][n_heads]: sum of a segment's decays (log2 of the factor)
+};
+
+// Shared memory, in bytes from its start: q and k as they come, v of two
+// chunks, q and k as terms, the scores as terms, small arrays.
+struct Plan {
+    int raw_q, raw_k, raw_v, v_bytes, q16, k16, term, p16, p_term, small, bytes;
+};
+__host__ __device__ constexpr int pitch_of(int dk) { return (dk + 8) * 2; }  // 8 rows of 16 bytes on different banks
+constexpr int kPPitch = (C + 8) * 2;
+__host__ __device__ constexpr Plan plan_of(int dk, int tile) {
+    Plan p = {};
+    p.raw_q = 0;
+    p.raw_k = p.raw_q + C * dk * 4;
+    p.raw_v = p.raw_k + C * dk * 4;
+    p.v_bytes = C * (tile + 4) * 4;  // rows 4 floats apart beyond their length: fragments' loads meet no bank twice
+    p.term = C * pitch_of(dk);
+    p.q16 = p.raw_v + 2 * p.v_bytes;
+    p.k16 = p.q16 + 2 * p.term;
+    p.p_term = C * kPPitch;
+    p.p16 = p.k16 + 2 * p.term;
+    p.small = p.p16 + 2 * p.p_term;
+    p.bytes = p.small + 5 * C * 4;
+    return p;
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldm4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldm2(uint32_t (&r)[2], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const float *src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const float *src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+
+// Two values as fp16 pairs: the rounded ones and what is left of them.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    const __half2 r = __floats2half2_rn(x - f.x, y - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&r);
+}
+// The exponent that brings values whose largest has this biased exponent to
+// [2^14, 2^15) is -e; it stays in what 2^e and 2^-e can be as normal numbers.
+__device__ __forceinline__ int exponent_for(uint32_t biased) {
+    const int e = (int)biased - 127 - 14;
+    return biased == 255 ? 0 : e < -126 ? -126 : e;
+}
+// 2^n, 0 below the normal numbers, Inf above
+__device__ __forceinline__ float pow2(int n) {
+    return n < -126 ? 0.0f : __uint_as_float((uint32_t)((n > 127 ? 128 : n) + 127) << 23);
+}
+__device__ __forceinline__ uint32_t exponent_bits(float v) { return (__float_as_uint(v) >> 23) & 255u; }
+
+// OUT: outputs and, of the last segment, the state; else the end states of all
+// segments but the last, from zeros (the first: from the call's state).
+template <int DK, bool OUT>
+__global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr int KS = DK / 16;    // 16-deep steps over dk; pairs of 8-wide tiles
+    constexpr int PITCH = pitch_of(DK);
+    extern __shared__ __align__(128) uint8_t smem[];
+    const Linear &l = p.l;
+    const int tile_cols = p.split.tile, nw = tile_cols / 16;
+    const Plan plan = plan_of(DK, tile_cols);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = nw * 32;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t base = smem_addr(smem);
+    float *const gh = reinterpret_cast<float *>(smem + plan.small), *const gl = gh + C;
+    int *const q_exp = reinterpret_cast<int *>(gl + C), *const k_exp = q_exp + C, *const k_bad = k_exp + C;
+
+    pdl_wait_prev();
+    pdl_launch_dependents();
+    int at = blockIdx.x;
+    const int tile = at % p.split.tiles;
+    at /= p.split.tiles;
+    const int head = at % l.n_heads;
+    at /= l.n_heads;
+    const int seq = at % l.n_seqs, seg = at / l.n_seqs;
+    const Span span = span_of(l, seq);
+    const int64_t row0 = seg * p.split.rows, row1 = min(l.n_new, row0 + p.split.rows);
+    const bool last = seg == p.split.segments - 1;
+    const int64_t which = (int64_t)seq * l.n_heads + head, states = (int64_t)l.n_seqs * l.n_heads;
+    const int64_t size = (int64_t)DK * l.dv;
+    const int cols = head * l.dv + tile * tile_cols;      // first column of the tile in rows of v and out
+    const int mine = tile * tile_cols + warp * 16 + g;    // this lane's dims of the state: mine, mine + 8
+
+    if (OUT) {
+        // rows before the sequence's first
+        const int64_t n = min(span.first, row1) - row0;
+        for (int64_t i = tid; i < n * tile_cols; i += threads)
+            l.out[(seq * l.n_new + row0 + i / tile_cols) * l.out_stride + cols + i % tile_cols] = 0.0f;
+    }
+    if (span.idle) {
+        if (OUT && last && l.state_out != l.state)
+            for (int i = tid; i < DK * tile_cols; i += threads) {
+                const int64_t x = which * size + (int64_t)(i / tile_cols) * l.dv + tile * tile_cols + i % tile_cols;
+                l.state_out[x] = l.state[x];
+            }
+        return;
+    }
+
+    // S^T: [8-wide tile of dk][fragment]
+    float s[2 * KS][4];
+    const float *from = nullptr;
+    // several segments: the first pass keeps a copy of the call's state, since the last segment may write over it
+    // while the first one has yet to start
+    const bool copied = OUT && p.split.segments > 1;
+    if (seg == 0 && !span.begins) from = copied ? p.starts + which * size : l.state + which * size;
+    if (OUT && seg > 0) from = p.starts + (seg * states + which) * size;
+#pragma unroll
+    for (int n = 0; n < 2 * KS; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s[n][i] = from ? from[(int64_t)(8 * n + 2 * t + (i & 1)) * l.dv + mine + 8 * (i >> 1)] : 0.0f;
+    auto store = [&](float *to) {
+#pragma unroll
+        for (int n = 0; n < 2 * KS; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[(int64_t)(8 * n + 2 * t + (i & 1)) * l.dv + mine + 8 * (i >> 1)] = s[n][i];
+    };
+    if (!OUT && from) store(p.starts + which * size);
+
+    const int64_t begin = span.first > row0 ? row0 + (span.first - row0) / C * C : row0;
+    const float *const qk_of[2] = {l.q + head / (l.n_heads / l.n_qk) * DK, l.k + head / (l.n_heads / l.n_qk) * DK};
+    auto load = [&](int64_t row, int buffer) {
+        const int64_t x0 = seq * l.n_new + row;
+        auto rows = [&](uint32_t dst, int pitch, const float *src, int64_t stride, int width) {
+            if (l.vec) {
+                for (int i = tid; i < C * width / 4; i += threads) {
+                    const int r = i / (width / 4), c = i % (width / 4) * 4;
+                    const bool on = row + r >= span.first && row + r < row1;
+                    copy16(dst + (r * pitch + c) * 4, on ? src + (x0 + r) * stride + c : src, on);
+                }
+            } else {
+                for (int i = tid; i < C * width; i += threads) {
+                    const int r = i / width, c = i % width;
+                    const bool on = row + r >= span.first && row + r < row1;
+                    copy4(dst + (r * pitch + c) * 4, on ? src + (x0 + r) * stride + c : src, on);
+                }
+            }
+        };
+        if (OUT) rows(base + plan.raw_q, DK, qk_of[0], l.q_stride, DK);
+        rows(base + plan.raw_k, DK, qk_of[1], l.k_stride, DK);
+        rows(base + plan.raw_v + buffer * plan.v_bytes, tile_cols + 4, l.v + cols, l.v_stride, tile_cols);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto load_decay = [&](int64_t row) {
+        const int64_t r = row + lane;
+        return r >= span.first && r < row1 ? decay_of(l.decay[(seq * l.n_new + r) * l.decay_stride + head]) : 0.0f;
+    };
+
+    double seg_total = 0.0;
+    if (begin < row1) load(begin, 0);
+    float next_decay = begin < row1 ? load_decay(begin) : 0.0f;
+    int buffer = 0;
+    for (int64_t row = begin; row < row1; row += C, buffer ^= 1) {
+        // sums of decays, lane j row j (log2 of the factors)
+        const float decay = next_decay;
+        double total = (double)decay * 1.4426950408889634;
+#pragma unroll
+        for (int o = 1; o < C; o <<= 1) {
+            const double a = __shfl_up_sync(~0u, total, o);
+            if (lane >= o) total += a;
+        }
+        const double chunk_total = __shfl_sync(~0u, total, C - 1);
+        const float high = (float)total, low = (float)(total - (double)high);
+        const float to_end = exp2f((float)(chunk_total - total));
+        seg_total += chunk_total;
+
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // the rows are there, and the chunk before has been used up
+        if (warp == 0) {
+            gh[lane] = high;
+            gl[lane] = low;
+        }
+        // q and k as terms, a row per warp
+#pragma unroll 1
+        for (int r = warp + (OUT ? 0 : C); r < 2 * C; r += nw) {
+            const bool is_k = r >= C;
+            const int i = r & (C - 1);
+            constexpr int V = DK / 32;
+            const float *raw = reinterpret_cast<const float *>(smem + (is_k ? plan.raw_k : plan.raw_q)) + i * DK + lane * V;
+            float x[V];
+            uint32_t top = 0;
+            bool bad = false;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                x[v] = raw[v];
+                // a k that is not finite must not meet the zeros of rows before it: it is taken out here, and
+                // the rows from its own on become NaN
+                if (is_k && exponent_bits(x[v]) == 255) {
+                    bad = true;
+                    x[v] = 0.0f;
+                }
+                top = max(top, exponent_bits(x[v]));
+            }
+            top = __reduce_max_sync(~0u, top);
+            const int e = exponent_for(top);
+            const float up = pow2(-e);
+            bad = __any_sync(~0u, bad);
+            __half *const hi = reinterpret_cast<__half *>(smem + (is_k ? plan.k16 : plan.q16) + i * PITCH) + lane * V;
+            __half *const lo = hi + plan.term / 2;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float y = x[v] * up;
+                const __half h = __float2half_rn(y);
+                hi[v] = h;
+                lo[v] = __float2half_rn(y - __half2float(h));
+            }
+            if (lane == 0) {
+                (is_k ? k_exp : q_exp)[i] = e;
+                if (is_k) k_bad[i] = bad;
+            }
+        }
+        __syncthreads();  // terms are there, raw q and k are free
+        if (row + C < row1) {
+            load(row + C, buffer ^ 1);
+            next_decay = load_decay(row + C);
+        }
+        const int ke = k_exp[lane];
+        const int k_top = __reduce_max_sync(~0u, ke);
+        // the first row that a k or decay makes NaN
+        const uint32_t bad_rows = __ballot_sync(~0u, k_bad[lane] || decay != decay);
+        const int bad_from = bad_rows ? __ffs(bad_rows) - 1 : C;
+
+        float o[4][4];
+        if (OUT) {
+            // scores: 16 x 8 tiles (the two right of the diagonal are never read)
+            for (int i = warp; i < 6; i += nw) {
+                const int mi = i < 2 ? 0 : 1, nj = i < 2 ? i : i - 2;
+                float cross[4] = {0, 0, 0, 0}, main[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+                const uint32_t qa = base + plan.q16 + (mi * 16 + (lane & 15)) * PITCH + (lane >> 4) * 16;
+                const uint32_t kb = base + plan.k16 + (nj * 8 + (lane & 7)) * PITCH + ((lane >> 3) & 1) * 16;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    uint32_t ah[4], al[4], bh[2], bl[2];
+                    ldm4(ah, qa + ks * 32);
+                    ldm4(al, qa + ks * 32 + plan.term);
+                    ldm2(bh, kb + ks * 32);
+                    ldm2(bl, kb + ks * 32 + plan.term);
+                    mma(cross, al, bh[0], bh[1]);
+                    mma(cross, ah, bl[0], bl[1]);
+                    mma(main[ks & 1], ah, bh[0], bh[1]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int r = mi * 16 + 8 * u + g;
+                    const float rh = gh[r], rl = gl[r];
+                    float v[2];
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const int c = nj * 8 + 2 * t + w;
+                        const float dot = main[0][2 * u + w] + main[1][2 * u + w] + cross[2 * u + w];
+                        const float d = exp2f((rh - gh[c]) + (rl - gl[c])) * pow2(k_exp[c] - k_top - 22);
+                        v[w] = c <= r ? dot * d : 0.0f;
+                    }
+                    uint32_t hi, lo;
+                    split2(v[0], v[1], hi, lo);
+                    uint8_t *const dst = smem + plan.p16 + r * kPPitch + (nj * 8 + 2 * t) * 2;
+                    *reinterpret_cast<uint32_t *>(dst) = hi;
+                    *reinterpret_cast<uint32_t *>(dst + plan.p_term) = lo;
+                }
+            }
+
+            // what the state gives: S^T Q^T
+            uint32_t top[2] = {0, 0};
+#pragma unroll
+            for (int n = 0; n < 2 * KS; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top[i >> 1] = max(top[i >> 1], exponent_bits(s[n][i]));
+            int se[2];
+            float up[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                top[u] = max(top[u], __shfl_xor_sync(~0u, top[u], 1));
+                top[u] = max(top[u], __shfl_xor_sync(~0u, top[u], 2));
+                se[u] = exponent_for(top[u]);
+                up[u] = pow2(-se[u]);
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
+#pragma unroll
+            for (int k2 = 0; k2 < KS; k2 += 2) {
+                float c[4][4] = {};
+                uint32_t ah[2][4], al[2][4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float(&x)[4] = s[2 * (k2 + k) + n];
+                            split2(x[2 * u] * up[u], x[2 * u + 1] * up[u], ah[k][2 * n + u], al[k][2 * n + u]);
+                        }
+                const uint32_t qb = base + plan.q16 + ((lane & 7) + ((lane >> 4) << 3)) * PITCH + ((lane >> 3) & 1) * 16 + k2 * 32;
+#pragma unroll
+                for (int np = 0; np < 2; ++np) {
+                    uint32_t bh[2][4], bl[2][4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        ldm4(bh[k], qb + np * 16 * PITCH + k * 32);
+                        ldm4(bl[k], qb + np * 16 * PITCH + k * 32 + plan.term);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            mma(c[2 * np + h], al[k], bh[k][2 * h], bh[k][2 * h + 1]);
+                            mma(c[2 * np + h], ah[k], bl[k][2 * h], bl[k][2 * h + 1]);
+                        }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) mma(c[2 * np + h], ah[k], bh[k][2 * h], bh[k][2 * h + 1]);
+                }
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[n][i] += c[n][i];
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int r = 8 * n + 2 * t + w, e = q_exp[r];
+                    const float a = exp2f(gh[r] + gl[r]);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) o[n][2 * u + w] *= a * pow2(e + se[u]);
+                }
+            __syncthreads();  // scores are there
+        }
+
+        // this warp's dims of v: values of rows 16 step + 2t, +1, +8, +9, dims g and g + 8
+        const float *const vp = reinterpret_cast<const float *>(smem + plan.raw_v + buffer * plan.v_bytes) + warp * 16 + g;
+        const int v_pitch = tile_cols + 4;
+        float v[2][2][4];  // [step][dim][row]
+        uint32_t top[2] = {0, 0};
+        int v_bad[2] = {C, C};  // first row of each dim that is not finite
+        bool odd = false;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 16 * k + 2 * t + (i & 1) + 8 * (i >> 1);
+                    float x = vp[r * v_pitch + 8 * u];
+                    const uint32_t b = exponent_bits(x);
+                    if (b == 255) {
+                        odd = true;
+                        v_bad[u] = min(v_bad[u], r);
+                        x = 0.0f;
+                    } else {
+                        top[u] = max(top[u], b);
+                    }
+                    v[k][u][i] = x;
+                }
+        int ve[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            top[u] = max(top[u], __shfl_xor_sync(~0u, top[u], 1));
+            top[u] = max(top[u], __shfl_xor_sync(~0u, top[u], 2));
+            ve[u] = exponent_for(top[u]);
+            const float up = pow2(-ve[u]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[k][u][i] *= up;
+        }
+        if (__any_sync(~0u, odd)) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                v_bad[u] = min(v_bad[u], __shfl_xor_sync(~0u, v_bad[u], 1));
+                v_bad[u] = min(v_bad[u], __shfl_xor_sync(~0u, v_bad[u], 2));
+            }
+        }
+
+        if (OUT) {
+            // what the chunk's own rows give: V^T P^T
+            float c[4][4] = {};
+            uint32_t ah[2][4], al[2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split2(v[k][i & 1][2 * (i >> 1)], v[k][i & 1][2 * (i >> 1) + 1], ah[k][i], al[k][i]);
+            const uint32_t pb = base + plan.p16 + ((lane & 7) + ((lane >> 4) << 3)) * kPPitch + ((lane >> 3) & 1) * 16;
+#pragma unroll
+            for (int np = 0; np < 2; ++np) {
+                uint32_t bh[2][4], bl[2][4];
+#pragma unroll
+                for (int k = 0; k <= np; ++k) {
+                    ldm4(bh[k], pb + np * 16 * kPPitch + k * 32);
+                    ldm4(bl[k], pb + np * 16 * kPPitch + k * 32 + plan.p_term);
+                }
+#pragma unroll
+                for (int k = 0; k <= np; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        mma(c[2 * np + h], al[k], bh[k][2 * h], bh[k][2 * h + 1]);
+                        mma(c[2 * np + h], ah[k], bl[k][2 * h], bl[k][2 * h + 1]);
+                    }
+#pragma unroll
+                for (int k = 0; k <= np; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) mma(c[2 * np + h], ah[k], bh[k][2 * h], bh[k][2 * h + 1]);
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int r = 8 * n + 2 * t + w;
+                    const int64_t x = row + r;
+                    if (x < span.first || x >= row1) continue;
+                    const int e = q_exp[r] + k_top + 22;
+                    float *const dst = l.out + (seq * l.n_new + x) * l.out_stride + head * l.dv + mine;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float y = fmaf(c[n][2 * u + w], pow2(e + ve[u]), o[n][2 * u + w]) * l.scale;
+                        if (r >= min(bad_from, v_bad[u])) y = NAN;
+                        dst[8 * u] = y;
+                    }
+                }
+        }
+
+        // the state: S^T e^(G_C) + (V f)^T K, f_j = e^(G_C - G_j) and k_j's power of two
+        {
+            const float f = to_end * pow2(ke - k_top);
+            uint32_t ah[2][4], al[2][4];
+            // the products' own largest sets their power of two: an old row's v may be large and forgotten
+            uint32_t most[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float fr[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fr[i] = __shfl_sync(~0u, f, 16 * k + 2 * t + (i & 1) + 8 * (i >> 1));
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[k][u][i] *= fr[i];
+                        most[u] = max(most[u], exponent_bits(v[k][u][i]));
+                    }
+            }
+            int be[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                most[u] = max(most[u], __shfl_xor_sync(~0u, most[u], 1));
+                most[u] = max(most[u], __shfl_xor_sync(~0u, most[u], 2));
+                be[u] = exponent_for(most[u]);
+                const float up = pow2(-be[u]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[k][u][i] *= up;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split2(v[k][i & 1][2 * (i >> 1)], v[k][i & 1][2 * (i >> 1) + 1], ah[k][i], al[k][i]);
+            const float keep = bad_from < C ? NAN : exp2f((float)chunk_total);
+            float gain[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) gain[u] = v_bad[u] < C ? NAN : pow2(k_top + ve[u] + be[u]);
+            const uint32_t kb = base + plan.k16 + ((lane & 7) + (((lane >> 3) & 1) << 3)) * PITCH + (lane >> 4) * 16;
+#pragma unroll
+            for (int n2 = 0; n2 < KS; ++n2) {
+                float c[2][4] = {};
+                uint32_t bh[2][4], bl[2][4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    ldm4_trans(bh[k], kb + k * 16 * PITCH + n2 * 32);
+                    ldm4_trans(bl[k], kb + k * 16 * PITCH + n2 * 32 + plan.term);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        mma(c[h], al[k], bh[k][2 * h], bh[k][2 * h + 1]);
+                        mma(c[h], ah[k], bl[k][2 * h], bl[k][2 * h + 1]);
+                    }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) mma(c[h], ah[k], bh[k][2 * h], bh[k][2 * h + 1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[2 * n2 + h][i] = fmaf(c[h][i], gain[i >> 1], s[2 * n2 + h][i] * keep);
+            }
+        }
+    }
+
+    if (OUT) {
+        if (last) store(l.state_out + which * size);
+    } else {
+        store(p.starts + ((seg + 1) * states + which) * size);
+        if (tid == 0 && tile == 0) p.seg_decay[(seg + 1) * states + which] = (float)seg_total;
+    }
+}
+
+constexpr int kScanThreads = 256;
+
+// From the end states E_i that the segments come to from zeros (in the place of
+// segment i + 1; the first one's from the call's state) to the states before
+// them: S_1 = E_0, S_(i+1) = e^(G_i) S_i + E_i. A float4 per thread.
+__global__ void __launch_bounds__(kScanThreads) scan_kernel(const __grid_constant__ ChunkParams p) {
+    pdl_wait_prev();
+    pdl_launch_dependents();
+    const int64_t states = (int64_t)p.l.n_seqs * p.l.n_heads, size = (int64_t)p.l.dk * p.l.dv;
+    const int64_t i = ((int64_t)blockIdx.x * kScanThreads + threadIdx.x) * 4;
+    if (i >= states * size) return;
+    const int64_t which = i / size;
+    if (span_of(p.l, (int)(which / p.l.n_heads)).idle) return;
+    float4 s = *reinterpret_cast<const float4 *>(p.starts + states * size + i);
+    for (int seg = 2; seg < p.split.segments; ++seg) {
+        float4 *const at = reinterpret_cast<float4 *>(p.starts + seg * states * size + i);
+        const float4 e = *at;
+        const float a = exp2f(p.seg_decay[seg * states + which]);
+        s.x = fmaf(s.x, a, e.x);
+        s.y = fmaf(s.y, a, e.y);
+        s.z = fmaf(s.z, a, e.z);
+        s.w = fmaf(s.w, a, e.w);
+        *at = s;
+    }
+}
+
+cudaError_t launch(void (*kernel)(ChunkParams), const ChunkParams &p, int64_t grid, int threads, int smem, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int DK>
+cudaError_t launch_dk(const ChunkParams &p, cudaStream_t s) {
+    constexpr int most = plan_of(DK, 16 * kMaxWarps).bytes;
+    static OncePerDevice once[2];
+    cudaError_t e = allow_smem(once[0], chunk_kernel<DK, true>, most);
+    if (e == cudaSuccess) e = allow_smem(once[1], chunk_kernel<DK, false>, most);
+    if (e != cudaSuccess) return e;
+    const int threads = p.split.tile / 16 * 32, smem = plan_of(DK, p.split.tile).bytes;
+    const int64_t ctas = (int64_t)p.l.n_seqs * p.l.n_heads * p.split.tiles;
+    if (p.split.segments > 1) {
+        e = launch(chunk_kernel<DK, false>, p, ctas * (p.split.segments - 1), threads, smem, s);
+        if (e != cudaSuccess) return e;
+        const int64_t quads = (int64_t)p.l.n_seqs * p.l.n_heads * p.l.dk * p.l.dv / 4;
+        e = launch(scan_kernel, p, (quads + kScanThreads - 1) / kScanThreads, kScanThreads, 0, s);
+        if (e != cudaSuccess) return e;
+    }
+    return launch(chunk_kernel<DK, true>, p, ctas * p.split.segments, threads, smem, s);
+}
+
+size_t starts_bytes(const Linear &l, const Split &split) {
+    return (size_t)split.segments * (size_t)l.n_seqs * (size_t)l.n_heads * (size_t)l.dk * (size_t)l.dv * 4;
+}
+
+}  // namespace
+
+size_t chunks_workspace_bytes(const Linear &l, const Split &split) {
+    if (split.segments < 2) return 0;
+    return starts_bytes(l, split) + (size_t)split.segments * (size_t)l.n_seqs * (size_t)l.n_heads * 4;
+}
+
+cudaError_t launch_chunks(const Linear &l, const Split &split, const DeviceInfo &, cudaStream_t s) {
+    ChunkParams p;
+    p.l = l;
+    p.split = split;
+    p.starts = static_cast<float *>(l.workspace);
+    p.seg_decay = split.segments > 1 ? reinterpret_cast<float *>(static_cast<uint8_t *>(l.workspace) + starts_bytes(l, split))
+                                     : nullptr;
+    switch (l.dk) {
+    case 32: return launch_dk<32>(p, s);
+    case 64: return launch_dk<64>(p, s);
+    case 96: return launch_dk<96>(p, s);
+    default: return launch_dk<128>(p, s);
+    }
+}
+
+}  // namespace linear
+
+}  // namespace qmm
