@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -746,28 +747,77 @@ def qmm_experts_ffn_workspace_bytes(args: qmm_experts_ffn_args) -> int:
 
 def _on_device(first, t, name, dtype, shape=None):
     """Refuses a tensor that is not contiguous `dtype` (of `shape`) on the CUDA device of `first`."""
-    if t.get_device() != first.get_device() or t.get_device() < 0:
+    here = t.get_device()
+    if here < 0 or here != first.get_device():
         raise ValueError(f"{name} ({t.device}) must be on one CUDA device with the other tensors ({first.device})")
     if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be contiguous {dtype} {'' if shape is None else tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
 
 
-def _give_scratch(a, need: int, workspace, first, stream):
-    """Fills in a call's scratch: `workspace`, or (as attend does) the kept one of torch's current
-    stream, or a new tensor, which is returned."""
-    ws = None
-    if workspace is None:
-        torch = _torch()
-        if need and stream is None and not torch.cuda.is_current_stream_capturing():
-            workspace = _scratch_of_stream(need, first.device, a.stream)
-        elif need:
-            ws = workspace = torch.empty(need, dtype=torch.uint8, device=first.device)
-    elif workspace.get_device() != first.get_device() or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {first.device}")
-    if workspace is not None:
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    return ws
+class _Call:
+    """A C call whose arguments' structure is packed from Python numbers in one go (a ctypes structure costs
+    2 to 3 us to fill), with its scratch as the structure's fields `workspace` and `workspace_bytes`."""
+
+    def __init__(self, name, structure):
+        codes = {ctypes.c_int: "i", ctypes.c_int64: "q", ctypes.c_size_t: "N", ctypes.c_void_p: "P", ctypes.c_float: "f"}
+        self.name, self.structure = name, structure
+        self.pack = struct.Struct("@" + "".join(codes[t] for _, t in structure._fields_) + "0P").pack
+        fields = [f for f, _ in structure._fields_]
+        self.scratch_at = fields.index("workspace") if "workspace" in fields else None
+        self.call = self.need = None
+
+    def _bind(self):
+        lib = load()
+        take = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p)
+        self.call = take((self.name, lib))
+        if self.scratch_at is not None:
+            self.need = ctypes.CFUNCTYPE(ctypes.c_size_t, ctypes.c_char_p)((self.name + "_workspace_bytes", lib))
+
+    def __call__(self, *values):
+        if self.call is None:
+            self._bind()
+        status = self.call(self.pack(*values))
+        if status:
+            _check(status)
+
+    def with_scratch(self, values, workspace, first, stream, handle):
+        """Calls with `workspace`, or (as attend does) the kept scratch of torch's current stream, or a
+        new tensor."""
+        if self.call is None:
+            self._bind()
+        at, ws = self.scratch_at, None
+        if workspace is None:
+            torch = _torch()
+            keep = stream is None and not torch.cuda.is_current_stream_capturing()
+            if keep:
+                held = _attend_scratch.__dict__.get((first.get_device(), handle))
+                if held is not None:
+                    values[at], values[at + 1] = held.data_ptr(), held.numel()
+                    status = self.call(self.pack(*values))
+                    if status != 9:               # it was large enough
+                        if status:
+                            _check(status)
+                        return
+                    values[at] = values[at + 1] = 0
+            need = self.need(self.pack(*values))
+            if need and keep:
+                workspace = _scratch_of_stream(need, first.device, handle)
+            elif need:
+                ws = workspace = torch.empty(need, dtype=torch.uint8, device=first.device)
+        elif workspace.get_device() != first.get_device() or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {first.device}")
+        if workspace is not None:
+            values[at], values[at + 1] = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        status = self.call(self.pack(*values))
+        if status:
+            _check(status)
+        if stream is not None:
+            _keep_until_done(ws, stream)
+
+
+_call_route = _Call("qmm_route_experts", qmm_route_args)
+_call_ffn = _Call("qmm_experts_ffn", qmm_experts_ffn_args)
 
 
 def route_experts(logits, top_k: int, *, score="softmax", normalize=True, scale=1.0, ids=None, weights=None,
@@ -793,10 +843,9 @@ def route_experts(logits, top_k: int, *, score="softmax", normalize=True, scale=
         weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
     else:
         _on_device(logits, weights, "weights", torch.float32, shape)
-    a = qmm_route_args(logits.data_ptr(), row if n_pos > 1 else n_experts, n_pos, n_experts, top_k,
-                       SCORES[score] if isinstance(score, str) else int(score), int(bool(normalize)), scale,
-                       ids.data_ptr(), weights.data_ptr(), _stream_of(stream, logits), 0)
-    qmm_route_experts(a)
+    _call_route(logits.data_ptr(), row if n_pos > 1 else n_experts, n_pos, n_experts, top_k,
+                SCORES[score] if isinstance(score, str) else int(score), bool(normalize), scale, ids.data_ptr(),
+                weights.data_ptr(), _stream_of(stream, logits), 0)
     return ids, weights
 
 
@@ -828,15 +877,12 @@ def experts_ffn(act, fmt, w_gate, w_up, fmt_down, w_down, x, ids, weights, k: in
         _on_device(x, y, "y", torch.float32)
         if y.numel() != n_pos * k:
             raise ValueError(f"y must have x's {n_pos} x {k} values")
-    a = qmm_experts_ffn_args(
-        ACTS[act] if isinstance(act, str) else int(act), _fmt(fmt), _fmt(fmt_down), w_gate.data_ptr(),
-        w_up.data_ptr(), w_down.data_ptr(), w_len, w_down.numel() * w_down.element_size(), x.data_ptr(),
-        ids.data_ptr(), weights.data_ptr(), y.data_ptr(), k, n_ff, n_experts, n_pos, top_k,
-        int(bool(accumulate)), None, 0, _stream_of(stream, x), 0)
-    ws = _give_scratch(a, qmm_experts_ffn_workspace_bytes(a), workspace, x, stream)
-    qmm_experts_ffn(a)
-    if stream is not None:
-        _keep_until_done(ws, stream)
+    handle = _stream_of(stream, x)
+    _call_ffn.with_scratch(
+        [ACTS[act] if isinstance(act, str) else int(act), _fmt(fmt), _fmt(fmt_down), w_gate.data_ptr(), w_up.data_ptr(),
+         w_down.data_ptr(), w_len, w_down.numel() * w_down.element_size(), x.data_ptr(), ids.data_ptr(),
+         weights.data_ptr(), y.data_ptr(), k, n_ff, n_experts, n_pos, top_k, bool(accumulate), 0, 0, handle, 0],
+        workspace, x, stream, handle)
     return y
 
 
@@ -850,17 +896,21 @@ def qmm_linear_attend_workspace_bytes(args: qmm_linear_args) -> int:
     return load().qmm_linear_attend_workspace_bytes(ctypes.byref(args))
 
 
-def _head_rows(name, t, first):
-    """Row stride of fp32 rows [n_seqs, n_new, heads, dim] on the device of `first`."""
-    if t.dim() != 4 or t.dtype is not _torch().float32 or t.get_device() != first.get_device() or t.get_device() < 0:
+_call_linear = _Call("qmm_linear_attend", qmm_linear_args)
+
+
+def _head_rows(name, t, here):
+    """Shape of fp32 rows [n_seqs, n_new, heads, dim] on CUDA device `here`, and their stride."""
+    shape = t.shape
+    if len(shape) != 4 or t.dtype is not _torch().float32 or t.get_device() != here or here < 0:
         raise ValueError(f"{name} must be float32 [n_seqs, n_new, heads, dim] on one CUDA device with the other "
                          f"tensors, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    n_seqs, n_new, heads, dim = t.shape
+    n_seqs, n_new, heads, dim = shape
     s0, s1, s2, s3 = t.stride()
     row = s1 if n_new > 1 else s0 if n_seqs > 1 else heads * dim
     if (dim > 1 and s3 != 1) or (heads > 1 and s2 != dim) or (n_new > 1 and n_seqs > 1 and s0 != n_new * s1):
         raise ValueError(f"{name}: the heads of a row must be adjacent and rows equally spaced")
-    return row
+    return shape, row
 
 
 def linear_attend(q, k, v, decay, state, lens=None, *, scale=None, out=None, state_out=None, workspace=None,
@@ -873,22 +923,24 @@ def linear_attend(q, k, v, decay, state, lens=None, *, scale=None, out=None, sta
     given one when passed); the states after the last row go to state_out, by default over `state`. Scratch is
     `workspace` (uint8) when given; else as for attend."""
     torch = _torch()
-    q_row, k_row, v_row = _head_rows("q", q, v), _head_rows("k", k, v), _head_rows("v", v, v)
-    n_seqs, n_new, n_heads, dv = v.shape
-    n_qk, dk = q.shape[2:]
-    if k.shape != q.shape or q.shape[:2] != v.shape[:2]:
-        raise ValueError(f"q, k and v must have the same rows, and q and k the same heads: got {tuple(q.shape)}, "
-                         f"{tuple(k.shape)}, {tuple(v.shape)}")
-    if decay.dtype is not torch.float32 or decay.get_device() != v.get_device():
+    here = v.get_device()
+    (q_shape, q_row), (k_shape, k_row), (v_shape, v_row) = (_head_rows(*t, here) for t in (("q", q), ("k", k), ("v", v)))
+    n_seqs, n_new, n_heads, dv = v_shape
+    n_qk, dk = q_shape[2:]
+    if k_shape != q_shape or q_shape[0] != n_seqs or q_shape[1] != n_new:
+        raise ValueError(f"q, k and v must have the same rows, and q and k the same heads: got {tuple(q_shape)}, "
+                         f"{tuple(k_shape)}, {tuple(v_shape)}")
+    d_shape = decay.shape
+    if decay.dtype is not torch.float32 or decay.get_device() != here:
         raise ValueError("decay must be float32 on the other tensors' device")
-    if decay.shape == (n_heads,):
+    if len(d_shape) == 1 and d_shape[0] == n_heads:
         decay_row = 0
         if n_heads > 1 and decay.stride(0) != 1:
             raise ValueError("decay's heads must be adjacent")
-    elif decay.shape == v.shape[:3]:
-        decay_row = _head_rows("decay", decay.unsqueeze(-1), v)
+    elif d_shape == v_shape[:3]:
+        decay_row = _head_rows("decay", decay.unsqueeze(-1), here)[1]
     else:
-        raise ValueError(f"decay must be {tuple(v.shape[:3])} or ({n_heads},), got {tuple(decay.shape)}")
+        raise ValueError(f"decay must be {tuple(v_shape[:3])} or ({n_heads},), got {tuple(d_shape)}")
     shape = (n_seqs, n_heads, dk, dv)
     _on_device(v, state, "state", torch.float32, shape)
     if state_out is None:
@@ -898,15 +950,13 @@ def linear_attend(q, k, v, decay, state, lens=None, *, scale=None, out=None, sta
     if lens is not None:
         _on_device(v, lens, "lens", torch.int32, (n_seqs,))
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-    elif out.shape != v.shape:
+        out = torch.empty(v_shape, dtype=v.dtype, device=v.device)
+    out_shape, out_row = _head_rows("out", out, here)
+    if out_shape != v_shape:
         raise ValueError("out must have v's shape")
-    a = qmm_linear_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, k_row, v_row, decay.data_ptr(), decay_row,
-                        state.data_ptr(), state_out.data_ptr(), out.data_ptr(), _head_rows("out", out, v),
-                        None if lens is None else lens.data_ptr(), n_seqs, n_new, n_heads, n_qk, dk, dv,
-                        dk ** -0.5 if scale is None else scale, None, 0, _stream_of(stream, v), 0)
-    ws = _give_scratch(a, qmm_linear_attend_workspace_bytes(a), workspace, v, stream)
-    qmm_linear_attend(a)
-    if stream is not None:
-        _keep_until_done(ws, stream)
+    handle = _stream_of(stream, v)
+    _call_linear.with_scratch(
+        [q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, k_row, v_row, decay.data_ptr(), decay_row, state.data_ptr(),
+         state_out.data_ptr(), out.data_ptr(), out_row, 0 if lens is None else lens.data_ptr(), n_seqs, n_new, n_heads,
+         n_qk, dk, dv, dk ** -0.5 if scale is None else scale, 0, 0, handle, 0], workspace, v, stream, handle)
     return out
