@@ -594,10 +594,13 @@ typedef struct qmm_experts_ffn_args {
  * whatever its weight; one of any other id outside [0, n_experts) adds
  * nothing either and is reported by qmm_device_status (QMM_ERR_BAD_ID). A
  * position without experts gives zeros. Slices that no id names are not read.
- * Weights enter the tensor cores as their integer codes (or 16-bit values), x and
- * the activated products as sums of 16-bit terms: of a value, 22 bits or
- * 2^-38 of the largest among 32 neighbours, whichever is more (BF16 weights:
- * 24 bits). Sums are fp32; the same call gives the same result each time. An Inf or NaN in x
+ * Weights enter as their integer codes (or 16-bit values). Where experts get more
+ * than about a row each, x and the activated products meet them on the tensor cores
+ * as sums of 16-bit terms: of a value, 22 bits or 2^-38 of the largest among 32
+ * neighbours, whichever is more (BF16 weights: 24 bits). One position, and few
+ * rows, are taken row by row: for quantised weights values are kept to 2^-23 of the
+ * largest among 32 neighbours, 16-bit weights are multiplied in fp32. Sums are
+ * fp32; the same call gives the same result each time. An Inf or NaN in x
  * makes that position's outputs Inf or NaN. Stream-ordered, no
  * synchronization; scratch as for qmm_matmul_ex (calls that can run
  * concurrently pass their own). */

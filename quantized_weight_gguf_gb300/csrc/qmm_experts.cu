@@ -1,14 +1,14 @@
 // qmm_experts.cu -- the experts' feed-forward network over packed weights:
 //     y[p] (+)= sum_s w[p][s] Wd_e (act(Wg_e x[p]) * (Wu_e x[p])),  e = ids[p][s].
-// Four launches, each a programmatic dependent of the one before: the pairs
-// (position, slot) are sorted by expert while x becomes 16-bit terms (one
-// launch); the gate and up products with the activation; the down product, a
-// row per pair; the sum of each position's rows. This file holds the first and
-// the last, and the host side.
+// One position takes two launches: the gate and up products with the
+// activation, and the down product over its slots. Several take four: the pairs (position, slot) are sorted
+// by expert while x becomes 16-bit terms (one launch); the gate and up products; the down product, a
+// row per pair; the sum of each position's rows. Each is a programmatic dependent of the one before. This file
+// holds the first and the last of the four, and the host side.
 #include <algorithm>
 
 #include "qmm_experts.h"
-#include "qmm_experts_frag.cuh"
+#include "qmm_experts_rows.cuh"
 
 namespace qmm {
 
@@ -16,7 +16,8 @@ namespace experts {
 
 // one translation unit per group of formats
 #define QMM_EXPERTS_FORMAT(FMT) \
-    extern template cudaError_t launch_product<FMT>(bool, int, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
+    extern template cudaError_t launch_product<FMT>(bool, int, const ProductParams &, int, const DeviceInfo &, cudaStream_t); \
+    extern template cudaError_t launch_single<FMT>(bool, bool, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
 QMM_EXPERTS_FORMAT(F_BF16)
 QMM_EXPERTS_FORMAT(F_F16)
 QMM_EXPERTS_FORMAT(F_Q4_0)
@@ -36,9 +37,9 @@ struct PrepareParams {
     Tile *tiles;
     int *n_tiles, *order;
     const float *x;
-    int n_pos, k, x_blocks, bf16;
+    int n_pos, k, x_blocks, fmt;
     uint8_t *terms;
-    float2 *scales;
+    float *scales, *sums;
     int64_t x_row_bytes;
     unsigned int *err;
 };
@@ -110,7 +111,7 @@ __device__ void sort_pairs(const PrepareParams &p) {
     }
 }
 
-// Block 0 sorts the pairs, the others turn x into terms, a block of 32 values
+// Block 0 sorts the pairs, the others turn x into terms (records), a block of 32 values
 // per warp.
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ PrepareParams p) {
     pdl_wait_prev();
@@ -124,8 +125,15 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
         const int64_t row = i / p.x_blocks;
         const int b = (int)(i % p.x_blocks), e = 32 * b + lane;
         const float v = e < p.k ? p.x[row * p.k + e] : 0.0f;
-        const float2 s = put_block(v, lane, p.bf16, p.terms + row * p.x_row_bytes + (int64_t)b * 64 * (p.bf16 ? 3 : 2));
-        if (lane == 0) p.scales[i] = s;
+        if (p.columns == 1) {
+            put_record(v, lane, p.fmt, p.terms + row * p.x_row_bytes + (int64_t)b * kRecord);
+            continue;
+        }
+        const float2 s = put_terms(v, lane, p.fmt, p.terms + row * p.x_row_bytes + (int64_t)b * frag_bytes(p.fmt));
+        if (lane == 0) {
+            p.scales[i] = s.x;
+            p.sums[i] = s.y;
+        }
     }
 }
 
@@ -144,7 +152,6 @@ constexpr int kSumThreads = 256;
 template <int V>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant__ SumParams p) {
     pdl_wait_prev();
-    pdl_launch_dependents();
     const int64_t at = ((int64_t)blockIdx.x * kSumThreads + threadIdx.x) * V;
     if (at >= p.values) return;
     const int64_t pos = at / p.k;
@@ -192,11 +199,26 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 // Blocks of 32 of a row of terms, padded to the largest chunk.
 int padded_blocks(int k) { return (k + 255) / 256 * 8; }
 
-// Columns of a tile: the narrowest of 8, 16 and 32 that holds an expert's rows
-// when every expert is chosen equally often.
+// One position whose x fits: two launches, and no sorting.
+bool is_one(const ExpertsFfn &f) { return f.n_pos == 1 && (f.k + 31) / 32 <= kOneBlocks; }
+
+// Columns of a tile, by the rows that an expert gets when all are chosen equally often. Measured at 64 experts,
+// top 8, 2048 x 768, in us (1 = row by row):
+//   rows              1            2            8             32            64
+//   Q4_K      1:53 8:72    1:89 8:92   8:147 16:142  16:308 32:322  16:551 32:509
+//   Q8_0      1:62 8:72   1:105 8:89   8:139 16:137  16:287 32:306  16:505 32:504
+//   BF16      1:85 8:93  1:144 8:106   8:146 16:154  16:310 32:366  16:542 32:602
+//   Q6_K     1:112 8:97  1:201 8:117   8:190 16:182  16:407 32:338  16:689 32:590
+// Rows of weights that are not made of whole 16 bytes (all of Q6_K among them) are copied in narrow pieces by
+// the row-by-row kernel, which then only pays for one position (Q6_K 23.5 us against 30.8). 16-bit
+// weights, which have no codes to unpack, gain nothing from 32 columns (F16 at 33 rows: 335 us, BF16 with its three
+// terms and 16 columns 312).
 int columns_of(const ExpertsFfn &f) {
-    const int64_t rows = (f.n_pos * f.top_k + f.n_experts - 1) / f.n_experts;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    if (is_one(f)) return 1;
+    const int64_t pairs = f.n_pos * f.top_k, n = f.n_experts;
+    const bool whole = f.row_bytes % 16 == 0 && f.down_row_bytes % 16 == 0 && f.fmt != F_Q6_K && f.fmt_down != F_Q6_K;
+    const bool wide = f.fmt == F_BF16 || f.fmt == F_F16 || f.fmt_down == F_BF16 || f.fmt_down == F_F16;
+    return pairs <= n && whole ? 1 : pairs <= 8 * n ? 8 : pairs <= 32 * n || wide ? 16 : 32;
 }
 
 // The most tiles that the ids can make: each expert that is chosen leaves at
@@ -208,7 +230,7 @@ int64_t max_tiles(const ExpertsFfn &f, int columns) {
 
 // The parts of the workspace.
 struct Scratch {
-    size_t tiles, n_tiles, order, x, x_scale, h, h_scale, out, bytes;
+    size_t tiles, n_tiles, order, x, x_scale, x_sum, h, h_scale, h_sum, out, bytes;
     int columns;
     int64_t x_row_bytes, h_row_bytes;
     int x_blocks, h_blocks;
@@ -219,36 +241,47 @@ Scratch scratch_of(const ExpertsFfn &f) {
     s.columns = columns_of(f);
     s.x_blocks = padded_blocks(f.k);
     s.h_blocks = padded_blocks(f.n_ff);
-    s.x_row_bytes = (int64_t)s.x_blocks * frag_bytes(f.fmt);
-    s.h_row_bytes = (int64_t)s.h_blocks * frag_bytes(f.fmt_down);
+    s.x_row_bytes = (int64_t)s.x_blocks * (s.columns == 1 ? kRecord : frag_bytes(f.fmt));
+    s.h_row_bytes = (int64_t)s.h_blocks * (s.columns == 1 ? kRecord : frag_bytes(f.fmt_down));
     size_t at = 0;
     auto part = [&](size_t bytes) {
         const size_t here = at;
         at += round256(bytes);
         return here;
     };
+    s.h = part((size_t)s.h_row_bytes * pairs);
+    if (is_one(f)) {  // h alone
+        s.bytes = at;
+        return s;
+    }
+    s.h_scale = part(sizeof(float) * (size_t)s.h_blocks * pairs);
+    s.h_sum = part(sizeof(float) * (size_t)s.h_blocks * pairs);
     s.n_tiles = part(sizeof(int));
     s.tiles = part(sizeof(Tile) * (size_t)max_tiles(f, s.columns));
     s.order = part(sizeof(int) * pairs);
     s.x = part((size_t)s.x_row_bytes * (size_t)f.n_pos);
-    s.x_scale = part(sizeof(float2) * (size_t)s.x_blocks * (size_t)f.n_pos);
-    s.h = part((size_t)s.h_row_bytes * pairs);
-    s.h_scale = part(sizeof(float2) * (size_t)s.h_blocks * pairs);
+    s.x_scale = part(sizeof(float) * (size_t)s.x_blocks * (size_t)f.n_pos);
+    s.x_sum = part(sizeof(float) * (size_t)s.x_blocks * (size_t)f.n_pos);
     s.out = part(sizeof(float) * (size_t)f.k * pairs);
     s.bytes = at;
     return s;
 }
 
+template <int FMT>
+cudaError_t product_of(bool down, int columns, const ProductParams &p, int tiles, const DeviceInfo &dev, cudaStream_t s) {
+    return columns == 1 ? launch_single<FMT>(down, p.x32 != nullptr, p, tiles, dev, s)
+                        : launch_product<FMT>(down, columns, p, tiles, dev, s);
+}
 cudaError_t product(int fmt, bool down, int columns, const ProductParams &p, int tiles, const DeviceInfo &dev,
                     cudaStream_t s) {
     switch (fmt) {
-    case F_BF16: return launch_product<F_BF16>(down, columns, p, tiles, dev, s);
-    case F_F16: return launch_product<F_F16>(down, columns, p, tiles, dev, s);
-    case F_Q4_0: return launch_product<F_Q4_0>(down, columns, p, tiles, dev, s);
-    case F_Q4_K: return launch_product<F_Q4_K>(down, columns, p, tiles, dev, s);
-    case F_Q6_K: return launch_product<F_Q6_K>(down, columns, p, tiles, dev, s);
-    case F_Q8_0: return launch_product<F_Q8_0>(down, columns, p, tiles, dev, s);
-    default: return launch_product<F_Q5_0>(down, columns, p, tiles, dev, s);
+    case F_BF16: return product_of<F_BF16>(down, columns, p, tiles, dev, s);
+    case F_F16: return product_of<F_F16>(down, columns, p, tiles, dev, s);
+    case F_Q4_0: return product_of<F_Q4_0>(down, columns, p, tiles, dev, s);
+    case F_Q4_K: return product_of<F_Q4_K>(down, columns, p, tiles, dev, s);
+    case F_Q6_K: return product_of<F_Q6_K>(down, columns, p, tiles, dev, s);
+    case F_Q8_0: return product_of<F_Q8_0>(down, columns, p, tiles, dev, s);
+    default: return product_of<F_Q5_0>(down, columns, p, tiles, dev, s);
     }
 }
 
@@ -277,14 +310,17 @@ cudaError_t launch_experts_ffn(const ExpertsFfn &f, const DeviceInfo &dev, cudaS
     a.n_pos = (int)f.n_pos;
     a.k = f.k;
     a.x_blocks = l.x_blocks;
-    a.bf16 = f.fmt == F_BF16;
+    a.fmt = f.fmt;
     a.terms = ws + l.x;
-    a.scales = reinterpret_cast<float2 *>(ws + l.x_scale);
+    a.scales = reinterpret_cast<float *>(ws + l.x_scale);
+    a.sums = reinterpret_cast<float *>(ws + l.x_sum);
     a.x_row_bytes = l.x_row_bytes;
     a.err = dev.err;
+    cudaError_t e = cudaSuccess;
     const int64_t warps = f.n_pos * l.x_blocks;
     const int64_t blocks = std::min<int64_t>((warps + kPrepareWarps - 1) / kPrepareWarps, (int64_t)dev.sm_count * 8);
-    cudaError_t e = launch_next(prepare_kernel, a, 1 + blocks, kPrepareThreads, s);
+    const bool one = is_one(f);
+    if (!one) e = launch_next(prepare_kernel, a, 1 + blocks, kPrepareThreads, s);
     if (e != cudaSuccess) return e;
 
     ProductParams p = {};
@@ -297,19 +333,26 @@ cudaError_t launch_experts_ffn(const ExpertsFfn &f, const DeviceInfo &dev, cudaS
     p.blocks = (f.k + 31) / 32;
     p.x = a.terms;
     p.x_scale = a.scales;
+    p.x_sum = a.sums;
     p.x_row_bytes = l.x_row_bytes;
     p.x_blocks = l.x_blocks;
     p.tiles = a.tiles;
     p.n_tiles = a.n_tiles;
     p.order = a.order;
     p.top_k = f.top_k;
+    p.n_experts = f.n_experts;
     p.weights = f.weights;
     p.h = ws + l.h;
-    p.h_scale = reinterpret_cast<float2 *>(ws + l.h_scale);
+    p.h_scale = reinterpret_cast<float *>(ws + l.h_scale);
+    p.h_sum = reinterpret_cast<float *>(ws + l.h_sum);
     p.h_row_bytes = l.h_row_bytes;
     p.h_blocks = l.h_blocks;
-    p.h_bf16 = f.fmt_down == F_BF16;
+    p.h_fmt = f.fmt_down;
     p.act = f.act;
+    p.x32 = one ? f.x : nullptr;
+    p.ids = f.ids;
+    p.accumulate = f.accumulate;
+    p.err = dev.err;
     e = product(f.fmt, false, l.columns, p, tiles, dev, s);
     if (e != cudaSuccess) return e;
 
@@ -321,11 +364,12 @@ cudaError_t launch_experts_ffn(const ExpertsFfn &f, const DeviceInfo &dev, cudaS
     p.blocks = (f.n_ff + 31) / 32;
     p.x = p.h;
     p.x_scale = p.h_scale;
+    p.x_sum = p.h_sum;
     p.x_row_bytes = l.h_row_bytes;
     p.x_blocks = l.h_blocks;
-    p.out = reinterpret_cast<float *>(ws + l.out);
+    p.out = one ? f.y : reinterpret_cast<float *>(ws + l.out);
     e = product(f.fmt_down, true, l.columns, p, tiles, dev, s);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || one) return e;
 
     SumParams q = {};
     q.rows = p.out;

@@ -55,29 +55,37 @@ struct ProductParams {
     int64_t slice_bytes, row_bytes;
     int rows;                // of a slice
     int k, blocks;           // contraction length, and its blocks of 32
-    const uint8_t *x;        // activations as terms: [row][padded blocks][frag_bytes]
-    const float2 *x_scale;   // [row][padded blocks] scale and sum (see put_block)
+    const uint8_t *x;        // activations as terms: [row][padded blocks][frag_bytes]; single rows: records (see put_record)
+    const float *x_scale, *x_sum; // [row][padded blocks] (see put_terms)
     int64_t x_row_bytes;
     int x_blocks;            // padded blocks of a row
     const Tile *tiles;
     const int *n_tiles;
     const int *order;        // pairs in expert order
     int top_k;
-    // first product: act(gate) up times the pair's weight, as terms for the second
+    // first product: act(gate) up times the pair's weight, as terms (records) for the second
     const float *weights;
     uint8_t *h;
-    float2 *h_scale;
+    float *h_scale, *h_sum;
     int64_t h_row_bytes;
     int h_blocks;            // padded
-    int h_bf16, act;
+    int h_fmt, act;
     // second product
-    float *out;              // [pair][rows]
+    float *out;              // [pair][rows]; one position: y
+    // single rows (see qmm_experts_rows.cuh)
+    int slices;              // set by the launch
+    const float *x32;        // one position: x, ids, and whether y is added to
+    const int32_t *ids;
+    int n_experts, accumulate;
+    unsigned int *err;
 };
 
 // columns (activation rows) of a tile: 8, 16 or 32
 template <int FMT>
-cudaError_t launch_product(bool down, int columns, const ProductParams &p, int max_units_of_tiles, const DeviceInfo &dev,
-                           cudaStream_t s);
+cudaError_t launch_product(bool down, int columns, const ProductParams &p, int max_tiles, const DeviceInfo &dev, cudaStream_t s);
+// tiles of one row; one: of a single position
+template <int FMT>
+cudaError_t launch_single(bool down, bool one, const ProductParams &p, int max_columns, const DeviceInfo &dev, cudaStream_t s);
 
 }  // namespace experts
 }  // namespace qmm

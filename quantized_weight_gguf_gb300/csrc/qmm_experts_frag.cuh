@@ -9,11 +9,9 @@
 // is as good as an fp32 dot.
 //
 // The order of the 32 values of a block inside the two 16-deep steps is free
-// as long as both operands share it. Lane (g, t) of the fragment (g = lane / 4,
-// t = lane % 4) takes, of row g and in this order,
-//     4t, 4t+2 | 4t+1, 4t+3 (first step)   16+4t, 16+4t+2 | 16+4t+1, 16+4t+3 (second):
-// one 4-byte word of codes gives what a lane needs of a step, and masks of a
-// 4-bit word leave its values in just these pairs.
+// as long as both operands share it (order_of): it is chosen so that lane (g, t) of
+// the fragment (g = lane / 4, t = lane % 4) finds its eight values of row g in few words and
+// few operations leave them in pairs.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -24,13 +22,24 @@
 namespace qmm {
 namespace experts {
 
-// 16-bit terms of an activation; bytes of a block of 32 of them (see put_block).
+// 16-bit terms of an activation; bytes of a block of 32 of them (see put_terms).
 __host__ __device__ constexpr int terms_of(int fmt) { return fmt == F_BF16 ? 3 : 2; }
 __host__ __device__ constexpr int frag_bytes(int fmt) { return 64 * terms_of(fmt); }
 
-// Place (0..31, in units of one value) of element e of a block in a term's 64 bytes.
-__host__ __device__ constexpr int place_of(int e) {
-    return (e & 15) / 4 * 8 + (e & 16) / 4 + ((e & 1) << 1) + ((e & 2) >> 1);
+// Which elements of a block lane t takes, in the order of its operand registers
+// (two pairs for the first step, two for the second):
+//   kCodes:  4t, 4t+2 | 4t+1, 4t+3 | 16+4t, 16+4t+2 | 16+4t+1, 16+4t+3 -- what masks of a
+//            word of nibbles (low ones first) or of bytes leave
+//   kHalves: 4t, 4t+1 | 4t+2, 4t+3 | 16+4t, 16+4t+1 | 16+4t+2, 16+4t+3 -- 16-bit values as they are
+// Either way the first step holds elements 0 .. 15.
+enum Order : int { kCodes, kHalves };
+__host__ __device__ constexpr Order order_of(int fmt) {
+    return fmt == F_BF16 || fmt == F_F16 ? kHalves : kCodes;
+}
+// Place (0..31, in units of one value) of element e of a block in a term's 64
+// bytes: lane t's values lie at 8t .. 8t+7.
+__host__ __device__ constexpr int place_of(int order, int e) {
+    return (e & 15) / 4 * 8 + (e & 16) / 4 + (order == kHalves ? e & 3 : ((e & 1) << 1) + ((e & 2) >> 1));
 }
 
 // Weights of a row that are copied to shared memory at a time, and the bytes
@@ -42,17 +51,30 @@ __host__ __device__ constexpr int chunk_k(int fmt) {
 __host__ __device__ constexpr int chunk_bytes(int fmt) {
     return fmt == F_Q4_K ? 80 : chunk_k(fmt) / block_elems(fmt) * block_bytes(fmt);
 }
-// 16-byte pieces that cover a chunk wherever it starts (rows start at even
-// addresses), and the distance of rows in shared memory: an odd multiple of 16
-// bytes, so that the 8 rows of a fragment's word loads fall on different banks
-// (of 32 bytes for the 16-bit formats' 8-byte loads).
-__host__ __device__ constexpr int chunk_pieces(int fmt) {
-    return fmt == F_Q4_K ? 5 : (chunk_bytes(fmt) + 14 + 15) / 16;
+// 16-byte pieces that cover a chunk (rows start at even addresses, or at
+// multiples of 16 and chunks at multiples of 8), and the distance of rows in shared memory: an odd
+// multiple of 16 bytes, so that the 8 rows of a fragment's word loads fall on different
+// banks (of 32 bytes for the 16-bit formats' 8-byte loads).
+__host__ __device__ constexpr int chunk_pieces(int fmt, bool even) {
+    return fmt == F_BF16 || fmt == F_F16 ? (even ? 9 : 8) : fmt == F_Q4_K ? 5 : (chunk_bytes(fmt) + (even ? 14 : 8) + 15) / 16 | 1;
 }
-__host__ __device__ constexpr int row_pitch(int fmt) {
-    return fmt == F_BF16 || fmt == F_F16 ? 160 : 16 * (chunk_pieces(fmt) | 1);
+__host__ __device__ constexpr int row_pitch(int fmt, bool even) {
+    return fmt == F_BF16 || fmt == F_F16 ? 160 : 16 * chunk_pieces(fmt, even);
 }
 
+// A fresh sum (c is written only), and one that goes on.
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_bf16_new(float (&c)[4], const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t *a, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
@@ -74,13 +96,31 @@ __device__ __forceinline__ uint32_t ld16(const uint8_t *p) {
 __device__ __forceinline__ uint32_t ld32(const uint8_t *p) {
     return *reinterpret_cast<const uint32_t *>(p);
 }
-// the 4 bytes at p, which is even
-__device__ __forceinline__ uint32_t ld32_even(const uint8_t *p) {
-    const uint32_t odd = (uint32_t)reinterpret_cast<uintptr_t>(p) & 2u;
-    const uint32_t w0 = ld32(p - odd), w1 = ld32(p - odd + 4);
-    return prmt(w0, w1, odd ? 0x5432u : 0x3210u);
-}
-__device__ __forceinline__ float f16_at(const uint8_t *p) { return f16_bits_to_f32(ld16(p)); }
+// A row's chunk in shared memory. EVEN: it starts at an even address, and words
+// at offsets whose value mod 4 is known come from two aligned words and a
+// permute whose selector is formed once per chunk; else it starts at a multiple of 8
+// bytes, and words at offsets 0 mod 4 are read as they are.
+template <bool EVEN>
+struct RowAt {
+    const uint8_t *p;       // the chunk
+    const uint8_t *a0, *a2; // EVEN: aligned addresses for offsets that are 0 and 2 mod 4
+    uint32_t sel0;          // EVEN: selector for offsets 0 mod 4; 2 mod 4 takes the other one
+    __device__ __forceinline__ void set(const uint8_t *chunk, uint32_t odd) {  // odd: 0 or 2
+        p = chunk;
+        if (EVEN) {
+            a0 = chunk - odd;
+            a2 = chunk + odd - 2;
+            sel0 = odd ? 0x5432u : 0x3210u;
+        }
+    }
+    // the word at offset `at` + `lane`, `at` even and known when compiled, `lane` a multiple of 4
+    __device__ __forceinline__ uint32_t word(int at, int lane) const {
+        if (!EVEN && (at & 2) == 0) return ld32(p + at + lane);
+        const uint8_t *q = (EVEN ? (at & 2) ? a2 : a0 : p - 2) + at + lane;
+        return prmt(ld32(q), ld32(q + 4), !EVEN ? 0x5432u : (at & 2) ? sel0 ^ 0x6622u : sel0);
+    }
+    __device__ __forceinline__ float f16(int at) const { return f16_bits_to_f32(ld16(p + at)); }
+};
 
 // ------------------------------------------------------------ decode ----
 
@@ -117,6 +157,12 @@ __device__ __forceinline__ void bytes(uint32_t w, uint32_t &r0, uint32_t &r1) {
     r1 = sub2(prmt(w, 0x64646464u, 0x4341u), twice(h1024(Z)));
 }
 
+// signed bytes 0, 2 and 1, 3: the sign bit turned over makes them 128 + q
+__device__ __forceinline__ void signed_bytes(uint32_t w, uint32_t &r0, uint32_t &r1) {
+    r0 = sub2((w & 0x00FF00FFu) ^ 0x64806480u, twice(h1024(128)));
+    r1 = sub2(((w >> 8) & 0x00FF00FFu) ^ 0x64806480u, twice(h1024(128)));
+}
+
 // A row's share of a group of blocks of 32: load() takes the codes from the
 // row's chunk in shared memory, pairs(sub) gives block `sub` of the group as
 // four operand registers of lane t, and the scales follow. kGroup: blocks that
@@ -131,10 +177,10 @@ struct Row<F_Q4_0> {
     static constexpr bool kMin = false;
     uint32_t w;
     float d;
-    __device__ __forceinline__ void load(const uint8_t *chunk, int group, int, int t) {
-        const uint8_t *p = chunk + 18 * group;
-        d = f16_at(p);
-        w = ld32_even(p + 2 + 4 * t);
+    template <bool EVEN>
+    __device__ __forceinline__ void load(const RowAt<EVEN> &row, int group, int, int t) {
+        d = row.f16(18 * group);
+        w = row.word(18 * group + 2, 4 * t);
     }
     __device__ __forceinline__ void pairs(int, uint32_t (&r)[4]) const {
         low_nibbles<8>(w, r[0], r[1]);
@@ -150,11 +196,11 @@ struct Row<F_Q5_0> {
     static constexpr bool kMin = false;
     uint32_t w, high;  // nibbles; the fifth bits of elements 4t .. 4t+3 (0..3) and 16+4t .. (16..19)
     float d;
-    __device__ __forceinline__ void load(const uint8_t *chunk, int group, int, int t) {
-        const uint8_t *p = chunk + 22 * group;
-        d = f16_at(p);
-        high = ld32_even(p + 2) >> (4 * t);
-        w = ld32_even(p + 6 + 4 * t);
+    template <bool EVEN>
+    __device__ __forceinline__ void load(const RowAt<EVEN> &row, int group, int, int t) {
+        d = row.f16(22 * group);
+        high = row.word(22 * group + 2, 0) >> (4 * t);
+        w = row.word(22 * group + 6, 4 * t);
     }
     // bits 0..3 to bit 4 of bytes 0..3
     static __device__ __forceinline__ uint32_t spread(uint32_t b) {
@@ -172,17 +218,17 @@ template <>
 struct Row<F_Q8_0> {
     static constexpr int kGroup = 1, kScales = 1;
     static constexpr bool kMin = false;
-    uint32_t w0, w1;
+    uint32_t w[2];
     float d;
-    __device__ __forceinline__ void load(const uint8_t *chunk, int group, int, int t) {
-        const uint8_t *p = chunk + 34 * group;
-        d = f16_at(p);
-        w0 = ld32_even(p + 2 + 4 * t);
-        w1 = ld32_even(p + 18 + 4 * t);
+    template <bool EVEN>
+    __device__ __forceinline__ void load(const RowAt<EVEN> &row, int group, int, int t) {
+        d = row.f16(34 * group);
+        w[0] = row.word(34 * group + 2, 4 * t);
+        w[1] = row.word(34 * group + 18, 4 * t);
     }
     __device__ __forceinline__ void pairs(int, uint32_t (&r)[4]) const {
-        bytes<128>(w0 ^ 0x80808080u, r[0], r[1]);
-        bytes<128>(w1 ^ 0x80808080u, r[2], r[3]);
+        signed_bytes(w[0], r[0], r[1]);
+        signed_bytes(w[1], r[2], r[3]);
     }
     __device__ __forceinline__ float scale(int, int) const { return d; }
     __device__ __forceinline__ float min(int) const { return 0.0f; }
@@ -196,7 +242,9 @@ struct Row<F_Q4_K> {
     uint32_t w0, w1;   // 32 code bytes: low nibbles the first block, high ones the second
     uint32_t sc, m;    // the group's two scales and mins, bytes 0 and 1
     float d, dmin;
-    __device__ __forceinline__ void load(const uint8_t *chunk, int group, int half, int t) {
+    template <bool EVEN>
+    __device__ __forceinline__ void load(const RowAt<EVEN> &row, int group, int half, int t) {
+        const uint8_t *const chunk = row.p;
         const uint4 h = *reinterpret_cast<const uint4 *>(chunk);
         d = f16_bits_to_f32(h.x & 0xFFFFu);
         dmin = f16_bits_to_f32(h.x >> 16);
@@ -237,15 +285,16 @@ struct Row<F_Q6_K> {
     uint32_t ql[4], qh[2];  // [32 bytes (2)][16-deep step], [step]
     uint32_t sc[2];         // the group's eight int8 scales
     float d;
-    __device__ __forceinline__ void load(const uint8_t *chunk, int group, int, int t) {
+    template <bool EVEN>
+    __device__ __forceinline__ void load(const RowAt<EVEN> &row, int group, int, int t) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ql[i] = ld32_even(chunk + 64 * group + 16 * i + 4 * t);
+        for (int i = 0; i < 4; ++i) ql[i] = row.word(16 * i, 64 * group + 4 * t);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            qh[i] = ld32_even(chunk + 128 + 32 * group + 16 * i + 4 * t);
-            sc[i] = ld32_even(chunk + 192 + 8 * group + 4 * i);
+            qh[i] = row.word(128 + 16 * i, 32 * group + 4 * t);
+            sc[i] = row.word(192, 8 * group + 4 * i);
         }
-        d = f16_at(chunk + 208);
+        d = row.f16(208);
     }
     __device__ __forceinline__ void pairs(int sub, uint32_t (&r)[4]) const {
 #pragma unroll
@@ -267,20 +316,25 @@ struct Row<F_F16> {
     static constexpr int kGroup = 1, kScales = 0;
     static constexpr bool kMin = false;
     uint32_t w[4];
-    // rows start at multiples of 4 bytes (k is even)
-    __device__ __forceinline__ void load(const uint8_t *chunk, int group, int, int t) {
-        const uint8_t *p = chunk + 64 * group + 8 * t;
-        w[0] = ld32(p);
-        w[1] = ld32(p + 4);
-        w[2] = ld32(p + 32);
-        w[3] = ld32(p + 36);
+    // EVEN: rows start at multiples of 4 bytes (k is even)
+    template <bool EVEN>
+    __device__ __forceinline__ void load(const RowAt<EVEN> &row, int group, int, int t) {
+        const uint8_t *p = row.p + 64 * group + 8 * t;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (EVEN) {
+                w[2 * i] = ld32(p + 32 * i);
+                w[2 * i + 1] = ld32(p + 32 * i + 4);
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2 *>(p + 32 * i);
+                w[2 * i] = v.x;
+                w[2 * i + 1] = v.y;
+            }
+        }
     }
     __device__ __forceinline__ void pairs(int, uint32_t (&r)[4]) const {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            r[2 * u] = prmt(w[2 * u], w[2 * u + 1], 0x5410u);
-            r[2 * u + 1] = prmt(w[2 * u], w[2 * u + 1], 0x7632u);
-        }
+        for (int i = 0; i < 4; ++i) r[i] = w[i];
     }
     __device__ __forceinline__ float scale(int, int) const { return 1.0f; }
     __device__ __forceinline__ float min(int) const { return 0.0f; }
@@ -290,19 +344,20 @@ struct Row<F_BF16> : Row<F_F16> {};
 
 // ------------------------------------------------------- activations ----
 
-// Writes a block of 32 activations (lane e holds element e) as the B operand's
-// terms: `rec` holds the terms one after the other, 64 bytes each, element e at
+// Writes a block of 32 activations (lane e holds element e) as the B operand's terms for weights of
+// format `fmt`: `rec` holds the terms one after the other, 64 bytes each, element e at
 // place_of(e). Returns, in every lane, {scale, sum}: the power of two that the
 // terms' sum is multiplied by to give the value, and the block's sum.
-// fp16: the block's largest value is brought to [2^14, 2^15), so that the low
-// term of a value 2^-17 of it is still a normal number. A block that holds an
-// Inf or NaN is taken as it is.
-__device__ __forceinline__ float2 put_block(float v, int lane, bool bf16, uint8_t *rec) {
+// fp16: the largest of the values is brought to [2^14, 2^15), so that the low
+// term of a value 2^-17 of it is still a normal number. Values among which there is an
+// Inf or NaN are taken as they are.
+__device__ __forceinline__ float2 put_terms(float v, int e, int fmt, uint8_t *rec) {
     float sum = v;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    const int at = place_of(lane);
-    if (bf16) {
+    const uint32_t top = __reduce_max_sync(~0u, (__float_as_uint(v) >> 23) & 255u);
+    const int at = place_of(order_of(fmt), e);
+    if (fmt == F_BF16) {
         float rest = v;
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
@@ -313,11 +368,10 @@ __device__ __forceinline__ float2 put_block(float v, int lane, bool bf16, uint8_
         }
         return make_float2(1.0f, sum);
     }
-    const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(v) & 0x7F800000u) >> 23;
-    const uint32_t e = top < 15 ? 15 : top;
+    const uint32_t b = top < 15 ? 15 : top;
     const bool plain = top == 255;
-    const float up = plain ? 1.0f : __uint_as_float((268u - e) << 23);   // 2^(14 + 127 - e)
-    const float down = plain ? 1.0f : __uint_as_float((e - 14u) << 23);  // 1 / up
+    const float up = plain ? 1.0f : __uint_as_float((268u - b) << 23);   // 2^(14 + 127 - b)
+    const float down = plain ? 1.0f : __uint_as_float((b - 14u) << 23);  // 1 / up
     const float x = v * up;
     const __half hi = __float2half_rn(x);
     const float f = __half2float(hi);

@@ -20,16 +20,17 @@ def magnitudes(fmt, w, k, n):
     return v, np.abs(v + mins) + mins
 
 
-def dot_error(x, mag):
+def dot_error(x, mag, digits=False):
     """Bound on the error of x . w for rows x [p, k] and weights of sizes mag [n, k]: an x value is kept to 2^-22
     of itself or 2^-38 of the largest of its block of 32; a block's products are summed by at most 6 tensor-core
     steps that cut (2^-23 each, of the sizes summed) and its scales multiplied in fp32 (a few U); at most two
-    additions per 16 values follow."""
+    additions per 16 values follow. With `digits` an x value is kept as three signed digits of 8 bits on one step
+    for its block, which is at most 2^-22 of the block's largest: half of it, 2^-23, is lost at most."""
     k = x.shape[1]
     c = 2.0 ** -22 + (k / 8 + 80) * U
     pad = np.zeros((x.shape[0], -k % 32))
     top = np.abs(np.concatenate((x, pad), 1)).reshape(x.shape[0], -1, 32).max(-1).repeat(32, 1)[:, :k]
-    return c * (np.abs(x) @ mag.T) + 2.0 ** -38 * (top @ mag.T)
+    return c * (np.abs(x) @ mag.T) + 2.0 ** (-23 if digits else -38) * (top @ mag.T)
 
 
 def act(name, g):
@@ -53,14 +54,16 @@ def ffn(name, fmt, wg, wu, fmt_down, wd, x, ids, weights, k, n_ff, n_exp, y0=Non
         (g, gm), (u, um) = magnitudes(fmt, wg[e], k, n_ff), magnitudes(fmt, wu[e], k, n_ff)
         d, dm = magnitudes(fmt_down, wd[e], n_ff, k)
         gate, up = xe @ g.T, xe @ u.T
-        eg, eu = dot_error(xe, gm), dot_error(xe, um)
+        # where experts get a row each at most, quantised weights meet x as digits
+        one = ids.size <= n_exp or n_pos == 1
+        eg, eu = (dot_error(xe, m, one and fmt not in ("bf16", "f16")) for m in (gm, um))
         w = weights[pos, slot].astype(np.float64)[:, None]
         a = act(name, gate)
         h = a * up * w
         # both activations' derivatives stay below 1.2; the activation and two products round a few times
         eh = np.abs(w) * (1.2 * eg * np.abs(up) + np.abs(a) * eu + 1.2 * eg * eu) + 32 * U * np.abs(h)
         np.add.at(y, pos, h @ d.T)
-        np.add.at(err, pos, eh @ dm.T + dot_error(np.abs(h) + eh, dm))
+        np.add.at(err, pos, eh @ dm.T + dot_error(np.abs(h) + eh, dm, one and fmt_down not in ("bf16", "f16")))
         np.add.at(size, pos, np.abs(h) @ dm.T)
     if y0 is not None:
         y, size = y + y0, size + np.abs(y0)

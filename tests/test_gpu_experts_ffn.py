@@ -99,6 +99,17 @@ def test_odd_sizes(fmt, k, n_ff, n_pos):
     Case("swiglu", fmt, fmt, n_pos, k, n_ff, 3, 2).check()
 
 
+@pytest.mark.parametrize("fmt,fmt_down", [(f, f) for f in FORMATS] + [("q4_k", "q8_0"), ("q8_0", "q6_k"), ("f16", "q5_0")])
+def test_few_rows_to_many_experts(fmt, fmt_down):
+    Case("swiglu", fmt, fmt_down, 5, 768, 512, 24, 4).check()
+
+
+@pytest.mark.parametrize("fmt,k", [("q4_k", 5120), ("q4_k", 5376), ("q8_0", 5152), ("bf16", 5130), ("q6_k", 5376)])
+@pytest.mark.parametrize("n_pos", [1, 2])
+def test_wide_rows(fmt, k, n_pos):
+    Case("geglu", fmt, "q8_0", n_pos, k, 64, 4, 2).check()
+
+
 @pytest.mark.parametrize("n_pos", [1, 12])
 def test_accumulates(n_pos):
     c = Case("geglu", "q4_k", "q6_k", n_pos, 512, 256, 6, 3)
