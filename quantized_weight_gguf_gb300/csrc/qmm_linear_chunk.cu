@@ -46,6 +46,8 @@ struct Plan {
 };
 __host__ __device__ constexpr int pitch_of(int dk) { return (dk + 8) * 2; }  // 8 rows of 16 bytes on different banks
 constexpr int kPPitch = (C + 8) * 2;
+// Of the sums G_i of a chunk's decays: high and low parts, e^(G_i), e^(G_C - G_i), and (padded) e^(G_C).
+constexpr int kDecayFloats = 4 * C + 4;
 __host__ __device__ constexpr Plan plan_of(int dk, int tile) {
     Plan p = {};
     p.raw_q = 0;
@@ -58,16 +60,23 @@ __host__ __device__ constexpr Plan plan_of(int dk, int tile) {
     p.p_term = C * kPPitch;
     p.p16 = p.k16 + 2 * p.term;
     p.small = p.p16 + 2 * p.p_term;
-    p.bytes = p.small + 5 * C * 4;
+    p.bytes = p.small + (2 * kDecayFloats + 3 * C) * 4;
     return p;
 }
 
+#define QMM_MMA "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
+    asm(QMM_MMA "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// from zero
+__device__ __forceinline__ void mma_new(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm(QMM_MMA "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+#undef QMM_MMA
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -105,10 +114,23 @@ __device__ __forceinline__ int exponent_for(uint32_t biased) {
     return biased == 255 ? 0 : e < -126 ? -126 : e;
 }
 // 2^n, 0 below the normal numbers, Inf above
-__device__ __forceinline__ float pow2(int n) {
-    return n < -126 ? 0.0f : __uint_as_float((uint32_t)((n > 127 ? 128 : n) + 127) << 23);
-}
+__device__ __forceinline__ float pow2(int n) { return __uint_as_float((uint32_t)(min(max(n, -127), 128) + 127) << 23); }
 __device__ __forceinline__ uint32_t exponent_bits(float v) { return (__float_as_uint(v) >> 23) & 255u; }
+// 2^-exponent_for()
+__device__ __forceinline__ float up_for(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
+// max(top, |v|), NaN if v is
+__device__ __forceinline__ float top_of(float top, float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(v)));
+    return r;
+}
+__device__ __forceinline__ bool finite(float top) { return __float_as_uint(top) < 0x7F800000u; }
+__device__ __forceinline__ int exponent_of(float top) { return exponent_for(__float_as_uint(top) >> 23); }
+// over the four lanes of a dim
+__device__ __forceinline__ float top_over_4(float v) {
+    v = top_of(v, __shfl_xor_sync(~0u, v, 1));
+    return top_of(v, __shfl_xor_sync(~0u, v, 2));
+}
 
 // OUT: outputs and, of the last segment, the state; else the end states of all
 // segments but the last, from zeros (the first: from the call's state).
@@ -123,8 +145,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = nw * 32;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t base = smem_addr(smem);
-    float *const gh = reinterpret_cast<float *>(smem + plan.small), *const gl = gh + C;
-    int *const q_exp = reinterpret_cast<int *>(gl + C), *const k_exp = q_exp + C, *const k_bad = k_exp + C;
+    float *const gs = reinterpret_cast<float *>(smem + plan.small);
+    int *const q_exp = reinterpret_cast<int *>(gs + 2 * kDecayFloats), *const k_exp = q_exp + C, *const k_bad = k_exp + C;
 
     pdl_wait_prev();
     pdl_launch_dependents();
@@ -182,18 +204,24 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
     const float *const qk_of[2] = {l.q + head / (l.n_heads / l.n_qk) * DK, l.k + head / (l.n_heads / l.n_qk) * DK};
     auto load = [&](int64_t row, int buffer) {
         const int64_t x0 = seq * l.n_new + row;
+        const int lo = (int)max((int64_t)0, span.first - row), n = (int)min((int64_t)C, row1 - row) - lo;  // rows that are there
         auto rows = [&](uint32_t dst, int pitch, const float *src, int64_t stride, int width) {
+            src += x0 * stride;
             if (l.vec) {
-                for (int i = tid; i < C * width / 4; i += threads) {
-                    const int r = i / (width / 4), c = i % (width / 4) * 4;
-                    const bool on = row + r >= span.first && row + r < row1;
-                    copy16(dst + (r * pitch + c) * 4, on ? src + (x0 + r) * stride + c : src, on);
+                // a row per warp, 16 bytes a lane
+                if (4 * lane < width) {
+                    const float *at = src + warp * stride + 4 * lane;
+                    dst += (warp * pitch + 4 * lane) * 4;
+                    for (int r = warp; r < C; r += nw, at += nw * stride, dst += nw * pitch * 4) {
+                        const bool on = (uint32_t)(r - lo) < (uint32_t)n;
+                        copy16(dst, on ? at : src + lo * stride, on);
+                    }
                 }
             } else {
                 for (int i = tid; i < C * width; i += threads) {
                     const int r = i / width, c = i % width;
-                    const bool on = row + r >= span.first && row + r < row1;
-                    copy4(dst + (r * pitch + c) * 4, on ? src + (x0 + r) * stride + c : src, on);
+                    const bool on = (uint32_t)(r - lo) < (uint32_t)n;
+                    copy4(dst + (r * pitch + c) * 4, on ? src + r * stride + c : src + lo * stride, on);
                 }
             }
         };
@@ -206,14 +234,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
         const int64_t r = row + lane;
         return r >= span.first && r < row1 ? decay_of(l.decay[(seq * l.n_new + r) * l.decay_stride + head]) : 0.0f;
     };
-
+    // The last warp sums a chunk's decays while the others are at the scores of the chunk before: lane j row
+    // j, log2 of the factors, 64 bits.
+    const bool sums_decays = warp == nw - 1;
     double seg_total = 0.0;
-    if (begin < row1) load(begin, 0);
-    float next_decay = begin < row1 ? load_decay(begin) : 0.0f;
-    int buffer = 0;
-    for (int64_t row = begin; row < row1; row += C, buffer ^= 1) {
-        // sums of decays, lane j row j (log2 of the factors)
-        const float decay = next_decay;
+    auto sum_decays = [&](float decay, int buffer) {
         double total = (double)decay * 1.4426950408889634;
 #pragma unroll
         for (int o = 1; o < C; o <<= 1) {
@@ -221,68 +246,110 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
             if (lane >= o) total += a;
         }
         const double chunk_total = __shfl_sync(~0u, total, C - 1);
-        const float high = (float)total, low = (float)(total - (double)high);
-        const float to_end = exp2f((float)(chunk_total - total));
+        const float high = (float)total;
+        float *const at = gs + buffer * kDecayFloats;
+        at[lane] = high;
+        at[C + lane] = (float)(total - (double)high);
+        at[2 * C + lane] = exp2f((float)total);
+        at[3 * C + lane] = exp2f((float)(chunk_total - total));
+        if (lane == 0) at[4 * C] = exp2f((float)chunk_total);
         seg_total += chunk_total;
+    };
 
+    float next_decay = 0.0f;
+    if (begin < row1) {
+        load(begin, 0);
+        if (sums_decays) {
+            sum_decays(load_decay(begin), 0);
+            next_decay = load_decay(begin + C);
+        }
+    }
+    int buffer = 0;
+    for (int64_t row = begin; row < row1; row += C, buffer ^= 1) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();  // the rows are there, and the chunk before has been used up
-        if (warp == 0) {
-            gh[lane] = high;
-            gl[lane] = low;
-        }
         // q and k as terms, a row per warp
-#pragma unroll 1
-        for (int r = warp + (OUT ? 0 : C); r < 2 * C; r += nw) {
-            const bool is_k = r >= C;
-            const int i = r & (C - 1);
-            constexpr int V = DK / 32;
-            const float *raw = reinterpret_cast<const float *>(smem + (is_k ? plan.raw_k : plan.raw_q)) + i * DK + lane * V;
-            float x[V];
-            uint32_t top = 0;
-            bool bad = false;
+#pragma unroll 2
+        for (int i = warp; i < C; i += nw) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                x[v] = raw[v];
-                // a k that is not finite must not meet the zeros of rows before it: it is taken out here, and
-                // the rows from its own on become NaN
-                if (is_k && exponent_bits(x[v]) == 255) {
-                    bad = true;
-                    x[v] = 0.0f;
+            for (int is_k = OUT ? 0 : 1; is_k < 2; ++is_k) {
+                constexpr int V = DK / 32;
+                const float *raw = reinterpret_cast<const float *>(smem + (is_k ? plan.raw_k : plan.raw_q)) + i * DK + lane * V;
+                float x[V];
+                if constexpr (V == 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(raw);
+                    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+                } else if constexpr (V == 2) {
+                    const float2 f = *reinterpret_cast<const float2 *>(raw);
+                    x[0] = f.x, x[1] = f.y;
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) x[v] = raw[v];
                 }
-                top = max(top, exponent_bits(x[v]));
-            }
-            top = __reduce_max_sync(~0u, top);
-            const int e = exponent_for(top);
-            const float up = pow2(-e);
-            bad = __any_sync(~0u, bad);
-            __half *const hi = reinterpret_cast<__half *>(smem + (is_k ? plan.k16 : plan.q16) + i * PITCH) + lane * V;
-            __half *const lo = hi + plan.term / 2;
+                float most = 0.0f;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float y = x[v] * up;
-                const __half h = __float2half_rn(y);
-                hi[v] = h;
-                lo[v] = __float2half_rn(y - __half2float(h));
-            }
-            if (lane == 0) {
-                (is_k ? k_exp : q_exp)[i] = e;
-                if (is_k) k_bad[i] = bad;
+                for (int v = 0; v < V; ++v) most = top_of(most, x[v]);
+                uint32_t top = __reduce_max_sync(~0u, __float_as_uint(most));
+                if (is_k) {
+                    const bool bad = top >= 0x7F800000u;
+                    if (bad) {
+                        // a k that is not finite must not meet the zeros of rows before it: it is taken out here,
+                        // and the rows from its own on become NaN
+                        most = 0.0f;
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            if (exponent_bits(x[v]) == 255) x[v] = 0.0f;
+                            most = top_of(most, x[v]);
+                        }
+                        top = __reduce_max_sync(~0u, __float_as_uint(most));
+                    }
+                    if (lane == 0) k_bad[i] = bad;
+                }
+                const int e = exponent_for(top >> 23);
+                const float up = up_for(e);
+                if (lane == 0) (is_k ? k_exp : q_exp)[i] = e;
+                uint8_t *const hi = smem + (is_k ? plan.k16 : plan.q16) + i * PITCH + lane * V * 2, *const lo = hi + plan.term;
+                if constexpr (V % 2 == 0) {
+                    uint32_t h[V / 2], r[V / 2];
+#pragma unroll
+                    for (int v = 0; v < V / 2; ++v) split2(x[2 * v] * up, x[2 * v + 1] * up, h[v], r[v]);
+                    if constexpr (V == 4) {
+                        *reinterpret_cast<uint2 *>(hi) = make_uint2(h[0], h[1]);
+                        *reinterpret_cast<uint2 *>(lo) = make_uint2(r[0], r[1]);
+                    } else {
+                        *reinterpret_cast<uint32_t *>(hi) = h[0];
+                        *reinterpret_cast<uint32_t *>(lo) = r[0];
+                    }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float y = x[v] * up;
+                        const __half h = __float2half_rn(y);
+                        reinterpret_cast<__half *>(hi)[v] = h;
+                        reinterpret_cast<__half *>(lo)[v] = __float2half_rn(y - __half2float(h));
+                    }
+                }
             }
         }
         __syncthreads();  // terms are there, raw q and k are free
         if (row + C < row1) {
             load(row + C, buffer ^ 1);
-            next_decay = load_decay(row + C);
+            if (sums_decays) {
+                sum_decays(next_decay, buffer ^ 1);
+                next_decay = load_decay(row + 2 * C);
+            }
         }
+        const float *const gh = gs + buffer * kDecayFloats, *const gl = gh + C, *const from_start = gl + C, *const to_end = from_start + C;
         const int ke = k_exp[lane];
         const int k_top = __reduce_max_sync(~0u, ke);
         // the first row that a k or decay makes NaN
-        const uint32_t bad_rows = __ballot_sync(~0u, k_bad[lane] || decay != decay);
+        const uint32_t bad_rows = __ballot_sync(~0u, k_bad[lane] || gh[lane] != gh[lane]);
         const int bad_from = bad_rows ? __ffs(bad_rows) - 1 : C;
 
         float o[4][4];
+        int se[2];
         if (OUT) {
+            const float k_scale = pow2(ke - k_top - 22);
             // scores: 16 x 8 tiles (the two right of the diagonal are never read)
             for (int i = warp; i < 6; i += nw) {
                 const int mi = i < 2 ? 0 : 1, nj = i < 2 ? i : i - 2;
@@ -300,48 +367,39 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
                     mma(cross, ah, bl[0], bl[1]);
                     mma(main[ks & 1], ah, bh[0], bh[1]);
                 }
+                const int c = nj * 8 + 2 * t;
+                const float2 ch = *reinterpret_cast<const float2 *>(gh + c), cl = *reinterpret_cast<const float2 *>(gl + c);
+                const float k0 = __shfl_sync(~0u, k_scale, c), k1 = __shfl_sync(~0u, k_scale, c + 1);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int r = mi * 16 + 8 * u + g;
                     const float rh = gh[r], rl = gl[r];
-                    float v[2];
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const int c = nj * 8 + 2 * t + w;
-                        const float dot = main[0][2 * u + w] + main[1][2 * u + w] + cross[2 * u + w];
-                        const float d = exp2f((rh - gh[c]) + (rl - gl[c])) * pow2(k_exp[c] - k_top - 22);
-                        v[w] = c <= r ? dot * d : 0.0f;
-                    }
+                    const float dot0 = main[0][2 * u] + main[1][2 * u] + cross[2 * u];
+                    const float dot1 = main[0][2 * u + 1] + main[1][2 * u + 1] + cross[2 * u + 1];
+                    const float v0 = c <= r ? dot0 * (exp2f((rh - ch.x) + (rl - cl.x)) * k0) : 0.0f;
+                    const float v1 = c + 1 <= r ? dot1 * (exp2f((rh - ch.y) + (rl - cl.y)) * k1) : 0.0f;
                     uint32_t hi, lo;
-                    split2(v[0], v[1], hi, lo);
-                    uint8_t *const dst = smem + plan.p16 + r * kPPitch + (nj * 8 + 2 * t) * 2;
+                    split2(v0, v1, hi, lo);
+                    uint8_t *const dst = smem + plan.p16 + r * kPPitch + c * 2;
                     *reinterpret_cast<uint32_t *>(dst) = hi;
                     *reinterpret_cast<uint32_t *>(dst + plan.p_term) = lo;
                 }
             }
 
             // what the state gives: S^T Q^T
-            uint32_t top[2] = {0, 0};
+            float top[2] = {0, 0}, up[2];
 #pragma unroll
             for (int n = 0; n < 2 * KS; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) top[i >> 1] = max(top[i >> 1], exponent_bits(s[n][i]));
-            int se[2];
-            float up[2];
+                for (int i = 0; i < 4; ++i) top[i >> 1] = fmaxf(top[i >> 1], fabsf(s[n][i]));
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                top[u] = max(top[u], __shfl_xor_sync(~0u, top[u], 1));
-                top[u] = max(top[u], __shfl_xor_sync(~0u, top[u], 2));
-                se[u] = exponent_for(top[u]);
-                up[u] = pow2(-se[u]);
+                se[u] = exponent_of(top_over_4(top[u]));
+                up[u] = up_for(se[u]);
             }
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
-#pragma unroll
             for (int k2 = 0; k2 < KS; k2 += 2) {
-                float c[4][4] = {};
+                float c[4][4];
                 uint32_t ah[2][4], al[2][4];
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
@@ -362,82 +420,75 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
                         ldm4(bl[k], qb + np * 16 * PITCH + k * 32 + plan.term);
                     }
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            mma(c[2 * np + h], al[k], bh[k][2 * h], bh[k][2 * h + 1]);
-                            mma(c[2 * np + h], ah[k], bl[k][2 * h], bl[k][2 * h + 1]);
-                        }
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) mma(c[2 * np + h], ah[k], bh[k][2 * h], bh[k][2 * h + 1]);
+                    for (int h = 0; h < 2; ++h) {
+                        float(&d)[4] = c[2 * np + h];
+                        mma_new(d, al[0], bh[0][2 * h], bh[0][2 * h + 1]);
+                        mma(d, ah[0], bl[0][2 * h], bl[0][2 * h + 1]);
+                        mma(d, al[1], bh[1][2 * h], bh[1][2 * h + 1]);
+                        mma(d, ah[1], bl[1][2 * h], bl[1][2 * h + 1]);
+                        mma(d, ah[0], bh[0][2 * h], bh[0][2 * h + 1]);
+                        mma(d, ah[1], bh[1][2 * h], bh[1][2 * h + 1]);
+                    }
                 }
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[n][i] += c[n][i];
+                    for (int i = 0; i < 4; ++i) o[n][i] = k2 ? o[n][i] + c[n][i] : c[n][i];
             }
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int r = 8 * n + 2 * t + w, e = q_exp[r];
-                    const float a = exp2f(gh[r] + gl[r]);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) o[n][2 * u + w] *= a * pow2(e + se[u]);
-                }
             __syncthreads();  // scores are there
         }
 
         // this warp's dims of v: values of rows 16 step + 2t, +1, +8, +9, dims g and g + 8
-        const float *const vp = reinterpret_cast<const float *>(smem + plan.raw_v + buffer * plan.v_bytes) + warp * 16 + g;
+        const float *const vp = reinterpret_cast<const float *>(smem + plan.raw_v + buffer * plan.v_bytes) + 2 * t * (tile_cols + 4) + warp * 16 + g;
         const int v_pitch = tile_cols + 4;
         float v[2][2][4];  // [step][dim][row]
-        uint32_t top[2] = {0, 0};
+        float top[2] = {0, 0};
         int v_bad[2] = {C, C};  // first row of each dim that is not finite
-        bool odd = false;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = 16 * k + 2 * t + (i & 1) + 8 * (i >> 1);
-                    float x = vp[r * v_pitch + 8 * u];
-                    const uint32_t b = exponent_bits(x);
-                    if (b == 255) {
-                        odd = true;
-                        v_bad[u] = min(v_bad[u], r);
-                        x = 0.0f;
-                    } else {
-                        top[u] = max(top[u], b);
-                    }
-                    v[k][u][i] = x;
+                    v[k][u][i] = vp[(16 * k + (i & 1) + 8 * (i >> 1)) * v_pitch + 8 * u];
+                    top[u] = top_of(top[u], v[k][u][i]);
                 }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) top[u] = top_over_4(top[u]);
+        if (__any_sync(~0u, !finite(top[0]) || !finite(top[1]))) {
+            // they must not meet the zeros of rows before them: taken out, and the dim's rows from them on become NaN
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                top[u] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (exponent_bits(v[k][u][i]) == 255) {
+                            v_bad[u] = min(v_bad[u], 16 * k + 2 * t + (i & 1) + 8 * (i >> 1));
+                            v[k][u][i] = 0.0f;
+                        }
+                        top[u] = top_of(top[u], v[k][u][i]);
+                    }
+                top[u] = top_over_4(top[u]);
+                v_bad[u] = min(v_bad[u], __shfl_xor_sync(~0u, v_bad[u], 1));
+                v_bad[u] = min(v_bad[u], __shfl_xor_sync(~0u, v_bad[u], 2));
+            }
+        }
         int ve[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            top[u] = max(top[u], __shfl_xor_sync(~0u, top[u], 1));
-            top[u] = max(top[u], __shfl_xor_sync(~0u, top[u], 2));
-            ve[u] = exponent_for(top[u]);
-            const float up = pow2(-ve[u]);
+            ve[u] = exponent_of(top[u]);
+            const float up = up_for(ve[u]);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[k][u][i] *= up;
         }
-        if (__any_sync(~0u, odd)) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                v_bad[u] = min(v_bad[u], __shfl_xor_sync(~0u, v_bad[u], 1));
-                v_bad[u] = min(v_bad[u], __shfl_xor_sync(~0u, v_bad[u], 2));
-            }
-        }
 
         if (OUT) {
             // what the chunk's own rows give: V^T P^T
-            float c[4][4] = {};
+            float c[4][4];
             uint32_t ah[2][4], al[2][4];
 #pragma unroll
             for (int k = 0; k < 2; ++k)
@@ -453,41 +504,65 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
                     ldm4(bl[k], pb + np * 16 * kPPitch + k * 32 + plan.p_term);
                 }
 #pragma unroll
-                for (int k = 0; k <= np; ++k)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        mma(c[2 * np + h], al[k], bh[k][2 * h], bh[k][2 * h + 1]);
-                        mma(c[2 * np + h], ah[k], bl[k][2 * h], bl[k][2 * h + 1]);
+                for (int h = 0; h < 2; ++h) {
+                    float(&d)[4] = c[2 * np + h];
+                    mma_new(d, al[0], bh[0][2 * h], bh[0][2 * h + 1]);
+                    mma(d, ah[0], bl[0][2 * h], bl[0][2 * h + 1]);
+                    if (np) {
+                        mma(d, al[1], bh[1][2 * h], bh[1][2 * h + 1]);
+                        mma(d, ah[1], bl[1][2 * h], bl[1][2 * h + 1]);
                     }
-#pragma unroll
-                for (int k = 0; k <= np; ++k)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) mma(c[2 * np + h], ah[k], bh[k][2 * h], bh[k][2 * h + 1]);
+                    mma(d, ah[0], bh[0][2 * h], bh[0][2 * h + 1]);
+                    if (np) mma(d, ah[1], bh[1][2 * h], bh[1][2 * h + 1]);
+                }
             }
+            // the larger of the two parts' powers of two is taken out of both
+            float of_state[2], of_chunk[2];
+            int common[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int chunk = k_top + 22 + ve[u];
+                common[u] = max(se[u], chunk);
+                of_state[u] = pow2(se[u] - common[u]);
+                of_chunk[u] = pow2(chunk - common[u]);
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const float2 a = *reinterpret_cast<const float2 *>(from_start + 8 * n + 2 * t);
+                const int2 e = *reinterpret_cast<const int2 *>(q_exp + 8 * n + 2 * t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int u = i >> 1;
+                    const float sum = fmaf(c[n][i], of_chunk[u], o[n][i] * (of_state[u] * (i & 1 ? a.y : a.x)));
+                    o[n][i] = sum * pow2((i & 1 ? e.y : e.x) + common[u]) * l.scale;
+                }
+            }
+            if (__any_sync(~0u, min(bad_from, min(v_bad[0], v_bad[1])) < C)) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (8 * n + 2 * t + (i & 1) >= min(bad_from, v_bad[i >> 1])) o[n][i] = NAN;
+            }
+            const int lo = (int)max((int64_t)0, span.first - row), rows = (int)min((int64_t)C, row1 - row) - lo;
+            float *const out = l.out + (seq * l.n_new + row + 2 * t) * l.out_stride + head * l.dv + mine;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int r = 8 * n + 2 * t + w;
-                    const int64_t x = row + r;
-                    if (x < span.first || x >= row1) continue;
-                    const int e = q_exp[r] + k_top + 22;
-                    float *const dst = l.out + (seq * l.n_new + x) * l.out_stride + head * l.dv + mine;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float y = fmaf(c[n][2 * u + w], pow2(e + ve[u]), o[n][2 * u + w]) * l.scale;
-                        if (r >= min(bad_from, v_bad[u])) y = NAN;
-                        dst[8 * u] = y;
+                for (int w = 0; w < 2; ++w)
+                    if ((uint32_t)(8 * n + 2 * t + w - lo) < (uint32_t)rows) {
+                        float *const dst = out + (8 * n + w) * l.out_stride;
+                        dst[0] = o[n][w];
+                        dst[8] = o[n][2 + w];
                     }
-                }
         }
 
         // the state: S^T e^(G_C) + (V f)^T K, f_j = e^(G_C - G_j) and k_j's power of two
         {
-            const float f = to_end * pow2(ke - k_top);
+            const float f = to_end[lane] * pow2(ke - k_top);
             uint32_t ah[2][4], al[2][4];
             // the products' own largest sets their power of two: an old row's v may be large and forgotten
-            uint32_t most[2] = {0, 0};
+            float most[2] = {0, 0};
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float fr[4];
@@ -498,16 +573,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         v[k][u][i] *= fr[i];
-                        most[u] = max(most[u], exponent_bits(v[k][u][i]));
+                        most[u] = fmaxf(most[u], fabsf(v[k][u][i]));
                     }
             }
             int be[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                most[u] = max(most[u], __shfl_xor_sync(~0u, most[u], 1));
-                most[u] = max(most[u], __shfl_xor_sync(~0u, most[u], 2));
-                be[u] = exponent_for(most[u]);
-                const float up = pow2(-be[u]);
+                be[u] = exponent_of(top_over_4(most[u]));
+                const float up = up_for(be[u]);
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -517,14 +590,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) split2(v[k][i & 1][2 * (i >> 1)], v[k][i & 1][2 * (i >> 1) + 1], ah[k][i], al[k][i]);
-            const float keep = bad_from < C ? NAN : exp2f((float)chunk_total);
+            const float keep = bad_from < C ? NAN : gh[4 * C];
             float gain[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) gain[u] = v_bad[u] < C ? NAN : pow2(k_top + ve[u] + be[u]);
             const uint32_t kb = base + plan.k16 + ((lane & 7) + (((lane >> 3) & 1) << 3)) * PITCH + (lane >> 4) * 16;
 #pragma unroll
             for (int n2 = 0; n2 < KS; ++n2) {
-                float c[2][4] = {};
+                float c[2][4];
                 uint32_t bh[2][4], bl[2][4];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -532,16 +605,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
                     ldm4_trans(bl[k], kb + k * 16 * PITCH + n2 * 32 + plan.term);
                 }
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        mma(c[h], al[k], bh[k][2 * h], bh[k][2 * h + 1]);
-                        mma(c[h], ah[k], bl[k][2 * h], bl[k][2 * h + 1]);
-                    }
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) mma(c[h], ah[k], bh[k][2 * h], bh[k][2 * h + 1]);
+                for (int h = 0; h < 2; ++h) {
+                    mma_new(c[h], al[0], bh[0][2 * h], bh[0][2 * h + 1]);
+                    mma(c[h], ah[0], bl[0][2 * h], bl[0][2 * h + 1]);
+                    mma(c[h], al[1], bh[1][2 * h], bh[1][2 * h + 1]);
+                    mma(c[h], ah[1], bl[1][2 * h], bl[1][2 * h + 1]);
+                    mma(c[h], ah[0], bh[0][2 * h], bh[0][2 * h + 1]);
+                    mma(c[h], ah[1], bh[1][2 * h], bh[1][2 * h + 1]);
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -554,7 +625,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
         if (last) store(l.state_out + which * size);
     } else {
         store(p.starts + ((seg + 1) * states + which) * size);
-        if (tid == 0 && tile == 0) p.seg_decay[(seg + 1) * states + which] = (float)seg_total;
+        if (sums_decays && lane == 0 && tile == 0) p.seg_decay[(seg + 1) * states + which] = (float)seg_total;
     }
 }
 
