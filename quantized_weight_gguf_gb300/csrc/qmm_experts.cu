@@ -1,10 +1,10 @@
 // qmm_experts.cu -- the experts' feed-forward network over packed weights:
 //     y[p] (+)= sum_s w[p][s] Wd_e (act(Wg_e x[p]) * (Wu_e x[p])),  e = ids[p][s].
-// One position takes two launches: the gate and up products with the
-// activation, and the down product over its slots. Several take four: the pairs (position, slot) are sorted
-// by expert while x becomes 16-bit terms (one launch); the gate and up products; the down product, a
-// row per pair; the sum of each position's rows. Each is a programmatic dependent of the one before. This file
-// holds the first and the last of the four, and the host side.
+// Few rows go row by row: x becomes digits (one launch; one position: the next one does it), the gate and up products
+// with the activation, and the down product over each position's slots. More take four launches: the pairs (position,
+// slot) are sorted by expert while x becomes 16-bit terms; the gate and up products; the down product, a row per pair;
+// the sum of each position's rows. Each is a programmatic dependent of the one before. This file holds the first and
+// the last of the four, and the host side.
 #include <algorithm>
 
 #include "qmm_experts.h"
@@ -17,7 +17,7 @@ namespace experts {
 // one translation unit per group of formats
 #define QMM_EXPERTS_FORMAT(FMT) \
     extern template cudaError_t launch_product<FMT>(bool, int, const ProductParams &, int, const DeviceInfo &, cudaStream_t); \
-    extern template cudaError_t launch_single<FMT>(bool, bool, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
+    extern template cudaError_t launch_single<FMT>(bool, const ProductParams &, const DeviceInfo &, cudaStream_t);
 QMM_EXPERTS_FORMAT(F_BF16)
 QMM_EXPERTS_FORMAT(F_F16)
 QMM_EXPERTS_FORMAT(F_Q4_0)
@@ -111,12 +111,17 @@ __device__ void sort_pairs(const PrepareParams &p) {
     }
 }
 
-// Block 0 sorts the pairs, the others turn x into terms (records), a block of 32 values
-// per warp.
+// Block 0 sorts the pairs (row by row: looks at their ids), the others turn x into terms (records), a block of 32
+// values per warp.
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ PrepareParams p) {
     pdl_wait_prev();
     if (blockIdx.x == 0) {
-        sort_pairs(p);
+        if (p.columns > 1) {
+            sort_pairs(p);
+        } else {
+            for (int i = threadIdx.x; i < p.pairs; i += kPrepareThreads)
+                if (p.ids[i] < -1 || p.ids[i] >= p.n_experts) record_error(p.err, DERR_BAD_ID);
+        }
         return;
     }
     const int lane = threadIdx.x & 31;
@@ -199,26 +204,21 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 // Blocks of 32 of a row of terms, padded to the largest chunk.
 int padded_blocks(int k) { return (k + 255) / 256 * 8; }
 
-// One position whose x fits: two launches, and no sorting.
+// One position whose x fits the shared memory: two launches.
 bool is_one(const ExpertsFfn &f) { return f.n_pos == 1 && (f.k + 31) / 32 <= kOneBlocks; }
 
 // Columns of a tile, by the rows that an expert gets when all are chosen equally often. Measured at 64 experts,
 // top 8, 2048 x 768, in us (1 = row by row):
-//   rows              1            2            8             32            64
-//   Q4_K      1:53 8:72    1:89 8:92   8:147 16:142  16:308 32:322  16:551 32:509
-//   Q8_0      1:62 8:72   1:105 8:89   8:139 16:137  16:287 32:306  16:505 32:504
-//   BF16      1:85 8:93  1:144 8:106   8:146 16:154  16:310 32:366  16:542 32:602
-//   Q6_K     1:112 8:97  1:201 8:117   8:190 16:182  16:407 32:338  16:689 32:590
-// Rows of weights that are not made of whole 16 bytes (all of Q6_K among them) are copied in narrow pieces by
-// the row-by-row kernel, which then only pays for one position (Q6_K 23.5 us against 30.8). 16-bit
-// weights, which have no codes to unpack, gain nothing from 32 columns (F16 at 33 rows: 335 us, BF16 with its three
-// terms and 16 columns 312).
+//   rows           1/4           1           3/2             8             32            64
+//   Q4_K    1:20 8:41   1:56 8:73   1:77  8:91  8:147 16:142  16:308 32:322  16:551 32:509
+//   Q8_0    1:23 8:40   1:66 8:74   1:89  8:89  8:139 16:137  16:287 32:306  16:505 32:504
+//   Q6_K    1:31 8:48   1:99 8:97  1:141 8:117  8:190 16:182  16:407 32:338  16:689 32:590
+//   BF16    1:33 8:45   1:93 8:94  1:129 8:106  8:146 16:154  16:310 32:366  16:542 32:602
+// 16-bit weights, which have no codes to unpack, gain nothing from 32 columns.
 int columns_of(const ExpertsFfn &f) {
-    if (is_one(f)) return 1;
     const int64_t pairs = f.n_pos * f.top_k, n = f.n_experts;
-    const bool whole = f.row_bytes % 16 == 0 && f.down_row_bytes % 16 == 0 && f.fmt != F_Q6_K && f.fmt_down != F_Q6_K;
-    const bool wide = f.fmt == F_BF16 || f.fmt == F_F16 || f.fmt_down == F_BF16 || f.fmt_down == F_F16;
-    return pairs <= n && whole ? 1 : pairs <= 8 * n ? 8 : pairs <= 32 * n || wide ? 16 : 32;
+    const bool codes = f.fmt != F_BF16 && f.fmt != F_F16 && f.fmt_down != F_BF16 && f.fmt_down != F_F16;
+    return pairs <= n || is_one(f) ? 1 : pairs <= 8 * n ? 8 : pairs <= 32 * n || !codes ? 16 : 32;
 }
 
 // The most tiles that the ids can make: each expert that is chosen leaves at
@@ -254,12 +254,16 @@ Scratch scratch_of(const ExpertsFfn &f) {
         s.bytes = at;
         return s;
     }
+    s.x = part((size_t)s.x_row_bytes * (size_t)f.n_pos);
+    if (s.columns == 1) {
+        s.bytes = at;
+        return s;
+    }
     s.h_scale = part(sizeof(float) * (size_t)s.h_blocks * pairs);
     s.h_sum = part(sizeof(float) * (size_t)s.h_blocks * pairs);
     s.n_tiles = part(sizeof(int));
     s.tiles = part(sizeof(Tile) * (size_t)max_tiles(f, s.columns));
     s.order = part(sizeof(int) * pairs);
-    s.x = part((size_t)s.x_row_bytes * (size_t)f.n_pos);
     s.x_scale = part(sizeof(float) * (size_t)s.x_blocks * (size_t)f.n_pos);
     s.x_sum = part(sizeof(float) * (size_t)s.x_blocks * (size_t)f.n_pos);
     s.out = part(sizeof(float) * (size_t)f.k * pairs);
@@ -269,7 +273,7 @@ Scratch scratch_of(const ExpertsFfn &f) {
 
 template <int FMT>
 cudaError_t product_of(bool down, int columns, const ProductParams &p, int tiles, const DeviceInfo &dev, cudaStream_t s) {
-    return columns == 1 ? launch_single<FMT>(down, p.x32 != nullptr, p, tiles, dev, s)
+    return columns == 1 ? launch_single<FMT>(down, p, dev, s)
                         : launch_product<FMT>(down, columns, p, tiles, dev, s);
 }
 cudaError_t product(int fmt, bool down, int columns, const ProductParams &p, int tiles, const DeviceInfo &dev,
@@ -349,6 +353,7 @@ cudaError_t launch_experts_ffn(const ExpertsFfn &f, const DeviceInfo &dev, cudaS
     p.h_blocks = l.h_blocks;
     p.h_fmt = f.fmt_down;
     p.act = f.act;
+    p.n_pos = (int)f.n_pos;
     p.x32 = one ? f.x : nullptr;
     p.ids = f.ids;
     p.accumulate = f.accumulate;
@@ -367,9 +372,9 @@ cudaError_t launch_experts_ffn(const ExpertsFfn &f, const DeviceInfo &dev, cudaS
     p.x_sum = p.h_sum;
     p.x_row_bytes = l.h_row_bytes;
     p.x_blocks = l.h_blocks;
-    p.out = one ? f.y : reinterpret_cast<float *>(ws + l.out);
+    p.out = l.columns == 1 ? f.y : reinterpret_cast<float *>(ws + l.out);
     e = product(f.fmt_down, true, l.columns, p, tiles, dev, s);
-    if (e != cudaSuccess || one) return e;
+    if (e != cudaSuccess || l.columns == 1) return e;
 
     SumParams q = {};
     q.rows = p.out;

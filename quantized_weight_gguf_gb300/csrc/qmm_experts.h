@@ -71,10 +71,11 @@ struct ProductParams {
     int h_blocks;            // padded
     int h_fmt, act;
     // second product
-    float *out;              // [pair][rows]; one position: y
-    // single rows (see qmm_experts_rows.cuh)
+    float *out;              // [pair][rows]; row by row: y
+    // row by row (see qmm_experts_rows.cuh)
     int slices;              // set by the launch
-    const float *x32;        // one position: x, ids, and whether y is added to
+    int n_pos;
+    const float *x32;        // one position: x
     const int32_t *ids;
     int n_experts, accumulate;
     unsigned int *err;
@@ -83,9 +84,9 @@ struct ProductParams {
 // columns (activation rows) of a tile: 8, 16 or 32
 template <int FMT>
 cudaError_t launch_product(bool down, int columns, const ProductParams &p, int max_tiles, const DeviceInfo &dev, cudaStream_t s);
-// tiles of one row; one: of a single position
+// row by row
 template <int FMT>
-cudaError_t launch_single(bool down, bool one, const ProductParams &p, int max_columns, const DeviceInfo &dev, cudaStream_t s);
+cudaError_t launch_single(bool down, const ProductParams &p, const DeviceInfo &dev, cudaStream_t s);
 
 }  // namespace experts
 }  // namespace qmm

@@ -4,6 +4,6 @@
 namespace qmm {
 namespace experts {
 template cudaError_t launch_product<F_Q6_K>(bool, int, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
-template cudaError_t launch_single<F_Q6_K>(bool, bool, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
+template cudaError_t launch_single<F_Q6_K>(bool, const ProductParams &, const DeviceInfo &, cudaStream_t);
 }  // namespace experts
 }  // namespace qmm

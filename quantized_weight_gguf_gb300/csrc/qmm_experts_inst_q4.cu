@@ -4,8 +4,8 @@
 namespace qmm {
 namespace experts {
 template cudaError_t launch_product<F_Q4_0>(bool, int, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
-template cudaError_t launch_single<F_Q4_0>(bool, bool, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
+template cudaError_t launch_single<F_Q4_0>(bool, const ProductParams &, const DeviceInfo &, cudaStream_t);
 template cudaError_t launch_product<F_Q5_0>(bool, int, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
-template cudaError_t launch_single<F_Q5_0>(bool, bool, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
+template cudaError_t launch_single<F_Q5_0>(bool, const ProductParams &, const DeviceInfo &, cudaStream_t);
 }  // namespace experts
 }  // namespace qmm

@@ -9,13 +9,13 @@
 // less the codes' zero point times the digits' sum. 24 dp4a and 30 to 45 other instructions a block, half of
 // what fragments for the tensor cores take for so few columns. 16-bit weights: fp32 multiply-adds.
 //
-// A unit of work is 64 rows of W for one activation row: of the first product 32 rows of the gate and the same 32 of
-// the up matrix (one block of the second product's activations), taken by `slices` warps that
-// each multiply every slices-th run. A warp copies what it multiplies into a ring of its own
-// and waits for nobody until the unit's end, where the slices' sums are added up in order.
+// A unit of work of the first product is 32 rows of a pair's gate matrix and the same 32 of its up matrix (one block of
+// the second product's activations); of the second 16 rows of y, over the blocks of the position's slots as one long
+// sum, so that y needs no further pass. `slices` warps take a unit, each every slices-th run. A warp copies what
+// it multiplies into a ring of its own and waits for nobody until the unit's end, where the slices' sums are added up
+// in order. Pairs are taken as they stand: sorted by expert, which took a launch's time, they came from L2 no more often.
 //
-// One position: the first product turns x into digits while its first weights are on their way; the
-// second runs over the blocks of all slots as one long sum, 16 rows a unit, so that y needs no further pass.
+// One position: the first product turns x into digits itself while its first weights are on their way.
 #pragma once
 
 #include "qmm_experts_kernel.cuh"
@@ -26,7 +26,7 @@ namespace experts {
 constexpr int kRowWarps = 8;
 constexpr int kOneBlocks = 160;  // of x that one position's first product holds (k up to 5120)
 // Rows of W in a unit.
-__host__ __device__ constexpr int unit_rows(bool one, bool down) { return one && down ? 16 : 64; }
+__host__ __device__ constexpr int unit_rows(bool down) { return down ? 16 : 64; }
 
 // A record of a block of 32 activations, 144 bytes (8 records apart, lanes' 16-byte loads meet no bank twice): quantised weights: digits [3][32] (element e
 // is sum_i 256^i digit_i[e] times the scale), scale, sum, and per digit the sums of elements 0-15 and 16-31 as
@@ -262,10 +262,9 @@ __host__ __device__ constexpr int run_pieces(int fmt, bool even) {
 struct RowLayout {
     int w_bytes, stage, stages, ring, part_bytes, one_bytes, smem;
 };
-__host__ __device__ constexpr RowLayout row_layout(int fmt, bool one, bool down, bool even) {
+__host__ __device__ constexpr RowLayout row_layout(int fmt, bool held, bool down, bool even) {
     RowLayout l = {};
-    const bool held = one && !down;
-    const int unit = unit_rows(one, down);
+    const int unit = unit_rows(down);
     l.w_bytes = stage_rows(fmt, unit, even) * run_pieces(fmt, even) * 16;
     l.stage = l.w_bytes + (held ? 0 : 8 * kRecord);
     l.part_bytes = kRowWarps * unit * 4;
@@ -277,19 +276,18 @@ __host__ __device__ constexpr RowLayout row_layout(int fmt, bool one, bool down,
     return l;
 }
 
-template <int FMT, bool ONE, bool DOWN, bool EVEN>
+// HELD: the first product of one position.
+template <int FMT, bool HELD, bool DOWN, bool EVEN>
 __global__ void __launch_bounds__(kRowWarps * 32, 2) rows_kernel(const __grid_constant__ ProductParams p) {
-    constexpr RowLayout L = row_layout(FMT, ONE, DOWN, EVEN);
-    constexpr bool HELD = ONE && !DOWN;
-    constexpr int UNIT = unit_rows(ONE, DOWN), W = kRowWarps, NS = L.stages;
+    static_assert(!(HELD && DOWN), "the first product");
+    constexpr RowLayout L = row_layout(FMT, HELD, DOWN, EVEN);
+    constexpr int UNIT = unit_rows(DOWN), W = kRowWarps, NS = L.stages;
     constexpr int SR = stage_rows(FMT, UNIT, EVEN), PARTS = UNIT / SR;
     constexpr int CB = run_bytes(FMT), NP = run_pieces(FMT, EVEN), PITCH = 16 * NP;
     constexpr int PER = block_elems(FMT) == 256 ? 8 : 1;       // blocks that block_times' pointer covers
     constexpr int BB = is_16bit(FMT) ? 64 : block_bytes(FMT);  // its bytes
     constexpr int ROWS = DOWN ? UNIT : 32;                     // of a matrix, per unit
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int slots[kMaxTopK];
-    __shared__ int n_slots;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int l = lane & 7, q = lane >> 3;
     uint8_t *const ring = smem + warp * L.ring;
@@ -298,44 +296,35 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) rows_kernel(const __grid_co
 
     pdl_wait_prev();
 
-    // one position: its slots that name an expert
-    if (ONE) {
-        if (warp == 0) {
-            int n = 0;
-            for (int s0 = 0; s0 < p.top_k; s0 += 32) {
-                const int e = s0 + lane < p.top_k ? p.ids[s0 + lane] : -1;
-                const bool on = e >= 0 && e < p.n_experts;
-                if (!on && e != -1 && blockIdx.x == 0) record_error(p.err, DERR_BAD_ID);
-                const uint32_t mask = __ballot_sync(~0u, on);
-                if (on) slots[n + __popc(mask & ((1u << lane) - 1))] = s0 + lane;
-                n += __popc(mask);
-            }
-            if (lane == 0) n_slots = n;
-        }
-        __syncthreads();
-    }
-    const int columns = ONE ? n_slots : *p.n_tiles;       // several positions: tiles of one pair
     const int slices = p.slices, groups = W / slices;
     const int group = warp / slices, slice = warp % slices;
     const int row_blocks = (p.rows + ROWS - 1) / ROWS;
     const int runs = (p.blocks + 7) / 8;
-    // one position's second product: a unit is a block of rows, over the runs of every slot
-    const int units = ONE && DOWN ? row_blocks : columns * row_blocks;
-    const int items = ONE && DOWN ? columns * runs : runs;
+    const int units = (DOWN ? p.n_pos : p.n_pos * p.top_k) * row_blocks;
+    const int items = DOWN ? p.top_k * runs : runs;  // of a unit: runs, of the slots one after the other
     const int first_unit = blockIdx.x * groups + group, unit_step = gridDim.x * groups;
+    if (HELD && blockIdx.x == 0 && warp == 0)  // (several positions: the launch before has looked)
+        for (int i = lane; i < p.top_k; i += 32)
+            if (p.ids[i] < -1 || p.ids[i] >= p.n_experts) record_error(p.err, DERR_BAD_ID);
 
+    // the experts of a unit's slots (in lanes, 32 at a time), -1: none
     struct Unit {
-        int expert, column, row;
+        int pair, row;  // its first
+        int experts[DOWN ? 2 : 1];
+        __device__ __forceinline__ int expert(int slot) const {
+            return DOWN ? __shfl_sync(~0u, experts[DOWN && slot >= 32], slot & 31) : experts[0];
+        }
     };
     auto unit_of = [&](int unit) {
         Unit u;
-        if (ONE && DOWN) {
-            u.expert = u.column = 0;
-            u.row = unit * ROWS;
-        } else {
-            u.column = unit / row_blocks;
-            u.row = (unit - u.column * row_blocks) * ROWS;
-            u.expert = ONE ? p.ids[slots[u.column]] : p.tiles[u.column].expert;
+        const int at = unit / row_blocks;
+        u.pair = DOWN ? at * p.top_k : at;
+        u.row = (unit - at * row_blocks) * ROWS;
+#pragma unroll
+        for (int i = 0; i < (DOWN ? 2 : 1); ++i) {
+            const int slot = DOWN ? 32 * i + lane : 0;
+            const int e = slot < p.top_k ? p.ids[u.pair + slot] : -1;
+            u.experts[i] = e >= 0 && e < p.n_experts ? e : -1;
         }
         return u;
     };
@@ -344,17 +333,17 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) rows_kernel(const __grid_co
 
     // ---- copies: the unit, run and part that are loaded next ----
     int load_unit = first_unit, load_item = slice, load_run = slice, load_slot = 0, load_part = 0;
-    bool opened = false;
+    bool opened = false, turned = false;
+    int load_expert = -1;
     Unit from = {};
     const uint8_t *records = nullptr, *slice_at[2] = {};
     constexpr int COPIES = (SR * NP + 31) / 32;
-    int piece_at[COPIES];  // of a stage's first row
-    if (!EVEN)
+    int piece_at[COPIES];  // of a stage's first row (EVEN: its row)
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) {
-            const int piece = 32 * i + lane, row = piece / NP;
-            piece_at[i] = row * (int)p.row_bytes + 16 * (piece - row * NP);
-        }
+    for (int i = 0; i < COPIES; ++i) {
+        const int piece = 32 * i + lane, row = piece / NP;
+        piece_at[i] = row * (int)p.row_bytes + (EVEN ? 0 : 16 * (piece - row * NP));
+    }
     auto load = [&](int slot) {
         const uint32_t at = smem_addr(ring) + slot * L.stage;
         const int at_run = load_run * CB, left = (int)p.row_bytes - at_run;
@@ -368,6 +357,20 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) rows_kernel(const __grid_co
             for (int i = 0; i < COPIES; ++i)
                 if ((SR * NP) % 32 == 0 || i + 1 < COPIES || 32 * i + lane < SR * NP)
                     cp_async16(at + 512 * i + 16 * lane, b + piece_at[i], 16);
+        } else if (EVEN && (left >= CB || !is_16bit(FMT)) && from.row + ROWS <= p.rows &&
+                   (int64_t)(from.row + ROWS - 1) * p.row_bytes + at_run + 16 * NP <= p.slice_bytes) {
+            // the whole pieces that a run lies in: what they hold beside it stays unused (a 16-bit block may end
+            // inside the run's last one, and takes the zeros below)
+            const uint8_t *b = (DOWN || u0 < 32 ? slice_at[0] : slice_at[1]) +
+                               (int64_t)(from.row + (DOWN ? u0 : u0 & 31)) * p.row_bytes + at_run;
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i)
+                if ((SR * NP) % 32 == 0 || i + 1 < COPIES || 32 * i + lane < SR * NP) {
+                    const int piece = 32 * i + lane;
+                    const uint8_t *r = b + piece_at[i];
+                    r -= reinterpret_cast<uintptr_t>(r) & 15u;
+                    cp_async16(at + 512 * i + 16 * lane, r + 16 * (piece % NP), 16);
+                }
         } else {
 #pragma unroll 1
             for (int piece = lane; piece < SR * NP; piece += 32) {
@@ -387,36 +390,38 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) rows_kernel(const __grid_co
         }
     };
     auto load_next = [&](int slot) {
-        // on to the next unit that has an item for this warp
-        if (load_item >= items) {
-            load_unit += unit_step;
-            load_item = load_run = slice;
-            load_slot = 0;
-            opened = false;
-        }
-        if (load_unit < units && load_item < items) {
-            bool turned = !opened;
-            if (turned) from = unit_of(load_unit);
-            if (ONE && DOWN)
+        // on to this warp's next item that has an expert
+        while (load_unit < units) {
+            if (!opened) {
+                from = unit_of(load_unit);
+                load_item = load_run = slice;
+                load_slot = 0;
+                opened = turned = true;
+            }
+            if (load_item >= items) {
+                load_unit += unit_step;
+                opened = false;
+                continue;
+            }
+            if (DOWN)
                 while (load_run >= runs) {
                     load_run -= runs;
                     ++load_slot;
                     turned = true;
                 }
             if (turned) {
-                int row = from.column;
-                if (ONE && DOWN) {
-                    from.expert = p.ids[slots[load_slot]];
-                    row = load_slot;
-                } else if (!ONE && !DOWN) {
-                    row = p.order[from.column] / p.top_k;
-                }
-                records = p.x + row * p.x_row_bytes;
-                const int64_t base = from.expert * p.slice_bytes;
+                turned = false;
+                load_expert = from.expert(load_slot);
+                const int64_t base = load_expert * p.slice_bytes;
                 slice_at[0] = p.w[0] + base;
                 slice_at[1] = p.w[1] + base;
-                opened = true;
+                records = p.x + (DOWN ? from.pair + load_slot : from.pair / p.top_k) * p.x_row_bytes;
             }
+            if (load_expert >= 0) break;
+            load_item += slices;
+            load_run += slices;
+        }
+        if (load_unit < units) {
             load(slot);
             if (++load_part == PARTS) {
                 load_part = 0;
@@ -443,20 +448,25 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) rows_kernel(const __grid_co
     float *const sums = part + group * slices * UNIT;
     for (int unit = first_unit; unit < units; unit += unit_step) {
         const Unit here = unit_of(unit);
+        if (!DOWN && here.expert(0) < 0) continue;
         float sum[UNIT / 4];  // rows 4 j + q
 #pragma unroll
         for (int j = 0; j < UNIT / 4; ++j) sum[j] = 0.0f;
-        int run = slice, j0 = 0, expert = here.expert;
-        bool turned = ONE && DOWN;
+        int run = slice, j0 = 0, expert = -1;
+        bool turn = true;
         for (int item = slice; item < items; item += slices) {
-            if (ONE && DOWN)
+            if (DOWN)
                 while (run >= runs) {
                     run -= runs;
                     ++j0;
-                    turned = true;
+                    turn = true;
                 }
-            if (EVEN && turned) expert = p.ids[slots[j0]];
-            turned = false;
+            if (turn) expert = here.expert(j0);
+            turn = false;
+            if (expert < 0) {  // nothing has been loaded for it
+                run += slices;
+                continue;
+            }
             Digits<FMT> x;
             const bool on = run * 8 + l < p.blocks;
 #pragma unroll
@@ -514,16 +524,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) rows_kernel(const __grid_co
         }
         if (slice == 0) {
             if constexpr (DOWN) {
-                float *const out = ONE ? p.out : p.out + (int64_t)p.order[here.column] * p.rows;
-#pragma unroll
-                for (int i = 0; i < (UNIT == 64 ? 2 : 1); ++i) {
-                    const int row = here.row + r + 32 * i;
-                    if (mine && row < p.rows) out[row] = ONE && p.accumulate ? out[row] + s[i] : s[i];
-                }
+                float *const out = p.out + (int64_t)(unit / row_blocks) * p.rows + here.row + r;
+                if (mine && here.row + r < p.rows) *out = p.accumulate ? *out + s[0] : s[0];
             } else {
-                const float w = p.weights[ONE ? slots[here.column] : p.order[here.column]];
+                const float w = p.weights[here.pair];
                 const float h = here.row + r < p.rows ? glu_gate(s[0], glu_arg(p.act, s[0])) * s[1] * w : 0.0f;
-                put_record(h, r, p.h_fmt, p.h + here.column * p.h_row_bytes + (int64_t)(here.row / 32) * kRecord);
+                put_record(h, r, p.h_fmt, p.h + here.pair * p.h_row_bytes + (int64_t)(here.row / 32) * kRecord);
             }
         }
         if (slices > 1) named_barrier(1 + group, slices * 32);  // the sums have been taken
@@ -532,19 +538,19 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2) rows_kernel(const __grid_co
     pdl_launch_dependents();
 }
 
-template <int FMT, bool ONE, bool DOWN, bool EVEN>
-cudaError_t launch_rows_one(const ProductParams &p, int max_columns, const DeviceInfo &dev, cudaStream_t s) {
-    constexpr RowLayout L = row_layout(FMT, ONE, DOWN, EVEN);
+template <int FMT, bool HELD, bool DOWN, bool EVEN>
+cudaError_t launch_rows(const ProductParams &p, const DeviceInfo &dev, cudaStream_t s) {
+    constexpr RowLayout L = row_layout(FMT, HELD, DOWN, EVEN);
     static_assert(L.stages >= 2, "two stages");
     static OncePerDevice once;
-    cudaError_t e = allow_smem(once, rows_kernel<FMT, ONE, DOWN, EVEN>, L.smem);
+    cudaError_t e = allow_smem(once, rows_kernel<FMT, HELD, DOWN, EVEN>, L.smem);
     if (e != cudaSuccess) return e;
-    constexpr int ROWS = DOWN ? unit_rows(ONE, DOWN) : 32;
-    const int64_t units = (ONE && DOWN ? 1 : (int64_t)max_columns) * ((p.rows + ROWS - 1) / ROWS);
+    constexpr int ROWS = DOWN ? unit_rows(DOWN) : 32;
+    const int64_t units = (int64_t)p.n_pos * (DOWN ? 1 : p.top_k) * ((p.rows + ROWS - 1) / ROWS);
     const int64_t wave = (int64_t)dev.sm_count * 2;
     // as few slices as give every warp a unit's share, or two (with fewer, a
     // warp that has two units keeps all others waiting), and no more than there are runs
-    const int runs = (p.blocks + 7) / 8 * (ONE && DOWN ? max_columns : 1);
+    const int runs = (p.blocks + 7) / 8 * (DOWN ? p.top_k : 1);
     ProductParams r = p;
     r.slices = 1;
     while (r.slices < kRowWarps && 2 * r.slices <= runs && units * r.slices < 2 * wave * kRowWarps) r.slices *= 2;
@@ -559,22 +565,25 @@ cudaError_t launch_rows_one(const ProductParams &p, int max_columns, const Devic
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rows_kernel<FMT, ONE, DOWN, EVEN>, r);
+    return cudaLaunchKernelEx(&cfg, rows_kernel<FMT, HELD, DOWN, EVEN>, r);
 }
 
-template <int FMT, bool ONE, bool DOWN>
-cudaError_t launch_rows(const ProductParams &p, int max_columns, const DeviceInfo &dev, cudaStream_t s) {
-    constexpr bool CAN_BE_EVEN = FMT != F_Q4_K && ONE, MUST_BE_EVEN = FMT == F_Q6_K;
-    if constexpr (CAN_BE_EVEN || MUST_BE_EVEN)
-        if (MUST_BE_EVEN || p.row_bytes % 16)
-            return ONE ? launch_rows_one<FMT, true, DOWN, true>(p, max_columns, dev, s) : cudaErrorInvalidValue;
-    if constexpr (!MUST_BE_EVEN) return launch_rows_one<FMT, ONE, DOWN, false>(p, max_columns, dev, s);
+// EVEN: rows that are not made of whole 16 bytes
+template <int FMT, bool HELD, bool DOWN>
+cudaError_t launch_rows(const ProductParams &p, const DeviceInfo &dev, cudaStream_t s) {
+    if constexpr (FMT == F_Q4_K) {
+        return launch_rows<FMT, HELD, DOWN, false>(p, dev, s);
+    } else if constexpr (FMT == F_Q6_K) {
+        return launch_rows<FMT, HELD, DOWN, true>(p, dev, s);
+    } else {
+        return p.row_bytes % 16 ? launch_rows<FMT, HELD, DOWN, true>(p, dev, s) : launch_rows<FMT, HELD, DOWN, false>(p, dev, s);
+    }
 }
 
 template <int FMT>
-cudaError_t launch_single(bool down, bool one, const ProductParams &p, int max_columns, const DeviceInfo &dev, cudaStream_t s) {
-    if (one) return down ? launch_rows<FMT, true, true>(p, max_columns, dev, s) : launch_rows<FMT, true, false>(p, max_columns, dev, s);
-    return down ? launch_rows<FMT, false, true>(p, max_columns, dev, s) : launch_rows<FMT, false, false>(p, max_columns, dev, s);
+cudaError_t launch_single(bool down, const ProductParams &p, const DeviceInfo &dev, cudaStream_t s) {
+    if (down) return launch_rows<FMT, false, true>(p, dev, s);
+    return p.x32 ? launch_rows<FMT, true, false>(p, dev, s) : launch_rows<FMT, false, false>(p, dev, s);
 }
 
 }  // namespace experts
