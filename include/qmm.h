@@ -597,7 +597,7 @@ typedef struct qmm_experts_ffn_args {
  * Weights enter as their integer codes (or 16-bit values). Where experts get more
  * than about a row each, x and the activated products meet them on the tensor cores
  * as sums of 16-bit terms: of a value, 22 bits or 2^-38 of the largest among 32
- * neighbours, whichever is more (BF16 weights: 24 bits). One position, and few
+ * neighbours (of its row, above about 20 rows each), whichever is more (BF16 weights: 24 bits). One position, and few
  * rows, are taken row by row: for quantised weights values are kept to 2^-23 of the
  * largest among 32 neighbours, 16-bit weights are multiplied in fp32. Sums are
  * fp32; the same call gives the same result each time. An Inf or NaN in x

@@ -3,12 +3,13 @@
 // Few rows go row by row: x becomes digits (one launch; one position: the next one does it), the gate and up products
 // with the activation, and the down product over each position's slots. More take four launches: the pairs (position,
 // slot) are sorted by expert while x becomes 16-bit terms; the gate and up products; the down product, a row per pair;
-// the sum of each position's rows. Each is a programmatic dependent of the one before. This file holds the first and
-// the last of the four, and the host side.
+// the sum of each position's rows. Many take a fifth, which makes the gate and up products' results terms once whole
+// rows of them are there. Each is a programmatic dependent of the one before. This file holds all but the
+// products, and the host side.
 #include <algorithm>
 
 #include "qmm_experts.h"
-#include "qmm_experts_rows.cuh"
+#include "qmm_experts_tile.cuh"
 
 namespace qmm {
 
@@ -18,13 +19,17 @@ namespace experts {
 #define QMM_EXPERTS_FORMAT(FMT) \
     extern template cudaError_t launch_product<FMT>(bool, int, const ProductParams &, int, const DeviceInfo &, cudaStream_t); \
     extern template cudaError_t launch_single<FMT>(bool, const ProductParams &, const DeviceInfo &, cudaStream_t);
+#define QMM_EXPERTS_CODES(FMT) \
+    QMM_EXPERTS_FORMAT(FMT) \
+    extern template cudaError_t launch_tile<FMT>(bool, const ProductParams &, int, const DeviceInfo &, cudaStream_t);
 QMM_EXPERTS_FORMAT(F_BF16)
 QMM_EXPERTS_FORMAT(F_F16)
-QMM_EXPERTS_FORMAT(F_Q4_0)
-QMM_EXPERTS_FORMAT(F_Q4_K)
-QMM_EXPERTS_FORMAT(F_Q6_K)
-QMM_EXPERTS_FORMAT(F_Q8_0)
-QMM_EXPERTS_FORMAT(F_Q5_0)
+QMM_EXPERTS_CODES(F_Q4_0)
+QMM_EXPERTS_CODES(F_Q4_K)
+QMM_EXPERTS_CODES(F_Q6_K)
+QMM_EXPERTS_CODES(F_Q8_0)
+QMM_EXPERTS_CODES(F_Q5_0)
+#undef QMM_EXPERTS_CODES
 #undef QMM_EXPERTS_FORMAT
 
 namespace {
@@ -142,6 +147,49 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     }
 }
 
+// Rows of activations as the tile kernels' terms, a row per CTA at a time: each term 32 fp16 of a block,
+// under the power of two that brings the row's largest to [2^14, 2^15) (the scale is its inverse), and the sums
+// of the scaled blocks. With ids, block 0 sorts the pairs. Rows with an Inf or NaN are taken as they are.
+__global__ void __launch_bounds__(kPrepareThreads) tile_terms_kernel(const __grid_constant__ PrepareParams p) {
+    __shared__ uint32_t tops[kPrepareWarps];
+    pdl_wait_prev();
+    const int sorts = p.ids != nullptr;
+    if (sorts && blockIdx.x == 0) {
+        sort_pairs(p);
+        return;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int64_t row = (int64_t)blockIdx.x - sorts; row < p.n_pos; row += gridDim.x - sorts) {
+        const float *const x = p.x + row * p.k;
+        uint32_t top = 0;
+        for (int i = threadIdx.x; i < p.k; i += kPrepareThreads) top = max(top, (__float_as_uint(x[i]) >> 23) & 255u);
+        top = __reduce_max_sync(~0u, top);
+        if (lane == 0) tops[warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPrepareWarps; ++i) top = max(top, tops[i]);
+        __syncthreads();
+        const uint32_t b = top < 15 ? 15 : top;
+        const bool plain = top == 255;
+        const float up = plain ? 1.0f : __uint_as_float((268u - b) << 23);  // 2^(14 + 127 - b)
+        if (threadIdx.x == 0) p.scales[row] = plain ? 1.0f : __uint_as_float((b - 14u) << 23);
+        for (int i = warp; i < p.k / 32; i += kPrepareWarps) {
+            const float v = x[32 * i + lane] * up;
+            const __half hi = __float2half_rn(v);
+            const float f = __half2float(hi);
+            __half *const to = reinterpret_cast<__half *>(p.terms + row * p.x_row_bytes + (int64_t)i * kTermBytes) + tile_place(lane);
+            to[0] = hi;
+            to[32] = __float2half_rn(isfinite(f) ? v - f : 0.0f);
+            if (p.fmt == F_Q4_K) {
+                float sum = v;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+                if (lane == 0) p.sums[row * p.x_blocks + i] = sum;
+            }
+        }
+    }
+}
+
 struct SumParams {
     const float *rows;       // [pairs][k]
     const int32_t *ids;
@@ -207,18 +255,21 @@ int padded_blocks(int k) { return (k + 255) / 256 * 8; }
 // One position whose x fits the shared memory: two launches.
 bool is_one(const ExpertsFfn &f) { return f.n_pos == 1 && (f.k + 31) / 32 <= kOneBlocks; }
 
-// Columns of a tile, by the rows that an expert gets when all are chosen equally often. Measured at 64 experts,
-// top 8, 2048 x 768, in us (1 = row by row):
-//   rows           1/4           1           3/2             8             32            64
-//   Q4_K    1:20 8:41   1:56 8:73   1:77  8:91  8:147 16:142  16:308 32:322  16:551 32:509
-//   Q8_0    1:23 8:40   1:66 8:74   1:89  8:89  8:139 16:137  16:287 32:306  16:505 32:504
-//   Q6_K    1:31 8:48   1:99 8:97  1:141 8:117  8:190 16:182  16:407 32:338  16:689 32:590
-//   BF16    1:33 8:45   1:93 8:94  1:129 8:106  8:146 16:154  16:310 32:366  16:542 32:602
-// 16-bit weights, which have no codes to unpack, gain nothing from 32 columns.
+// How the products are taken, by the rows that an expert gets when all are chosen equally often. Measured at 64 experts,
+// top 8, 2048 x 768, in us: row by row (1), tiles of 8 and 16 columns on mma.sync, and of 48 on tcgen05 (T):
+//   rows           1/4           1           3/2             8             16            24            32            64
+//   Q4_K    1:20 8:41   1:56 8:73   1:77  8:91  8:147 16:142  16:186 T:197  16:276 T:210  16:308 T:219  16:551 T:362
+//   Q8_0    1:23 8:40   1:66 8:74   1:89  8:89  8:139 16:137  16:181 T:244  16:255 T:257  16:287 T:264  16:505 T:478
+//   Q6_K    1:31 8:48   1:99 8:97  1:141 8:117  8:190 16:182  16:237 T:300  16:341 T:314  16:407 T:324  16:689 T:582
+//   BF16    1:33 8:45   1:93 8:94  1:129 8:106  8:146 16:154
+// Tiles on tcgen05 are for codes, whose blocks' sums a scale multiplies on their way out.
+bool is_tile(const ExpertsFfn &f) {
+    const bool codes = f.fmt != F_BF16 && f.fmt != F_F16 && f.fmt_down != F_BF16 && f.fmt_down != F_F16;
+    return codes && !is_one(f) && f.n_pos * f.top_k > 20 * (int64_t)f.n_experts;
+}
 int columns_of(const ExpertsFfn &f) {
     const int64_t pairs = f.n_pos * f.top_k, n = f.n_experts;
-    const bool codes = f.fmt != F_BF16 && f.fmt != F_F16 && f.fmt_down != F_BF16 && f.fmt_down != F_F16;
-    return pairs <= n || is_one(f) ? 1 : pairs <= 8 * n ? 8 : pairs <= 32 * n || !codes ? 16 : 32;
+    return is_tile(f) ? kTileColumns : pairs <= n || is_one(f) ? 1 : pairs <= 8 * n ? 8 : 16;
 }
 
 // The most tiles that the ids can make: each expert that is chosen leaves at
@@ -231,6 +282,8 @@ int64_t max_tiles(const ExpertsFfn &f, int columns) {
 // The parts of the workspace.
 struct Scratch {
     size_t tiles, n_tiles, order, x, x_scale, x_sum, h, h_scale, h_sum, out, bytes;
+    size_t h32;  // tiles: the first product's results
+    bool tile;
     int columns;
     int64_t x_row_bytes, h_row_bytes;
     int x_blocks, h_blocks;
@@ -238,11 +291,12 @@ struct Scratch {
 Scratch scratch_of(const ExpertsFfn &f) {
     Scratch s = {};
     const size_t pairs = (size_t)(f.n_pos * f.top_k);
+    s.tile = is_tile(f);
     s.columns = columns_of(f);
     s.x_blocks = padded_blocks(f.k);
     s.h_blocks = padded_blocks(f.n_ff);
-    s.x_row_bytes = (int64_t)s.x_blocks * (s.columns == 1 ? kRecord : frag_bytes(f.fmt));
-    s.h_row_bytes = (int64_t)s.h_blocks * (s.columns == 1 ? kRecord : frag_bytes(f.fmt_down));
+    s.x_row_bytes = (int64_t)s.x_blocks * (s.columns == 1 ? kRecord : s.tile ? kTermBytes : frag_bytes(f.fmt));
+    s.h_row_bytes = (int64_t)s.h_blocks * (s.columns == 1 ? kRecord : s.tile ? kTermBytes : frag_bytes(f.fmt_down));
     size_t at = 0;
     auto part = [&](size_t bytes) {
         const size_t here = at;
@@ -267,25 +321,28 @@ Scratch scratch_of(const ExpertsFfn &f) {
     s.x_scale = part(sizeof(float) * (size_t)s.x_blocks * (size_t)f.n_pos);
     s.x_sum = part(sizeof(float) * (size_t)s.x_blocks * (size_t)f.n_pos);
     s.out = part(sizeof(float) * (size_t)f.k * pairs);
+    if (s.tile) s.h32 = part(sizeof(float) * (size_t)f.n_ff * pairs);
     s.bytes = at;
     return s;
 }
 
 template <int FMT>
-cudaError_t product_of(bool down, int columns, const ProductParams &p, int tiles, const DeviceInfo &dev, cudaStream_t s) {
+cudaError_t product_of(bool down, bool tile, int columns, const ProductParams &p, int tiles, const DeviceInfo &dev, cudaStream_t s) {
+    if constexpr (FMT != F_BF16 && FMT != F_F16)
+        if (tile) return launch_tile<FMT>(down, p, tiles, dev, s);
     return columns == 1 ? launch_single<FMT>(down, p, dev, s)
                         : launch_product<FMT>(down, columns, p, tiles, dev, s);
 }
-cudaError_t product(int fmt, bool down, int columns, const ProductParams &p, int tiles, const DeviceInfo &dev,
+cudaError_t product(int fmt, bool down, bool tile, int columns, const ProductParams &p, int tiles, const DeviceInfo &dev,
                     cudaStream_t s) {
     switch (fmt) {
-    case F_BF16: return product_of<F_BF16>(down, columns, p, tiles, dev, s);
-    case F_F16: return product_of<F_F16>(down, columns, p, tiles, dev, s);
-    case F_Q4_0: return product_of<F_Q4_0>(down, columns, p, tiles, dev, s);
-    case F_Q4_K: return product_of<F_Q4_K>(down, columns, p, tiles, dev, s);
-    case F_Q6_K: return product_of<F_Q6_K>(down, columns, p, tiles, dev, s);
-    case F_Q8_0: return product_of<F_Q8_0>(down, columns, p, tiles, dev, s);
-    default: return product_of<F_Q5_0>(down, columns, p, tiles, dev, s);
+    case F_BF16: return product_of<F_BF16>(down, tile, columns, p, tiles, dev, s);
+    case F_F16: return product_of<F_F16>(down, tile, columns, p, tiles, dev, s);
+    case F_Q4_0: return product_of<F_Q4_0>(down, tile, columns, p, tiles, dev, s);
+    case F_Q4_K: return product_of<F_Q4_K>(down, tile, columns, p, tiles, dev, s);
+    case F_Q6_K: return product_of<F_Q6_K>(down, tile, columns, p, tiles, dev, s);
+    case F_Q8_0: return product_of<F_Q8_0>(down, tile, columns, p, tiles, dev, s);
+    default: return product_of<F_Q5_0>(down, tile, columns, p, tiles, dev, s);
     }
 }
 
@@ -324,7 +381,8 @@ cudaError_t launch_experts_ffn(const ExpertsFfn &f, const DeviceInfo &dev, cudaS
     const int64_t warps = f.n_pos * l.x_blocks;
     const int64_t blocks = std::min<int64_t>((warps + kPrepareWarps - 1) / kPrepareWarps, (int64_t)dev.sm_count * 8);
     const bool one = is_one(f);
-    if (!one) e = launch_next(prepare_kernel, a, 1 + blocks, kPrepareThreads, s);
+    if (l.tile) e = launch_next(tile_terms_kernel, a, 1 + std::min<int64_t>(f.n_pos, (int64_t)dev.sm_count * 8), kPrepareThreads, s);
+    else if (!one) e = launch_next(prepare_kernel, a, 1 + blocks, kPrepareThreads, s);
     if (e != cudaSuccess) return e;
 
     ProductParams p = {};
@@ -346,7 +404,7 @@ cudaError_t launch_experts_ffn(const ExpertsFfn &f, const DeviceInfo &dev, cudaS
     p.top_k = f.top_k;
     p.n_experts = f.n_experts;
     p.weights = f.weights;
-    p.h = ws + l.h;
+    p.h = ws + (l.tile ? l.h32 : l.h);
     p.h_scale = reinterpret_cast<float *>(ws + l.h_scale);
     p.h_sum = reinterpret_cast<float *>(ws + l.h_sum);
     p.h_row_bytes = l.h_row_bytes;
@@ -358,9 +416,24 @@ cudaError_t launch_experts_ffn(const ExpertsFfn &f, const DeviceInfo &dev, cudaS
     p.ids = f.ids;
     p.accumulate = f.accumulate;
     p.err = dev.err;
-    e = product(f.fmt, false, l.columns, p, tiles, dev, s);
+    e = product(f.fmt, false, l.tile, l.columns, p, tiles, dev, s);
     if (e != cudaSuccess) return e;
 
+    if (l.tile) {
+        a.ids = nullptr;
+        a.x = reinterpret_cast<const float *>(ws + l.h32);
+        a.n_pos = pairs;
+        a.k = f.n_ff;
+        a.x_blocks = l.h_blocks;
+        a.fmt = f.fmt_down;
+        a.terms = ws + l.h;
+        a.scales = p.h_scale;
+        a.sums = p.h_sum;
+        a.x_row_bytes = l.h_row_bytes;
+        e = launch_next(tile_terms_kernel, a, std::min<int64_t>(pairs, (int64_t)dev.sm_count * 8), kPrepareThreads, s);
+        if (e != cudaSuccess) return e;
+        p.h = ws + l.h;
+    }
     p.w[0] = p.w[1] = f.down;
     p.row_bytes = f.down_row_bytes;
     p.slice_bytes = f.down_row_bytes * f.k;
@@ -373,7 +446,7 @@ cudaError_t launch_experts_ffn(const ExpertsFfn &f, const DeviceInfo &dev, cudaS
     p.x_row_bytes = l.h_row_bytes;
     p.x_blocks = l.h_blocks;
     p.out = l.columns == 1 ? f.y : reinterpret_cast<float *>(ws + l.out);
-    e = product(f.fmt_down, true, l.columns, p, tiles, dev, s);
+    e = product(f.fmt_down, true, l.tile, l.columns, p, tiles, dev, s);
     if (e != cudaSuccess || l.columns == 1) return e;
 
     SumParams q = {};

@@ -81,9 +81,12 @@ struct ProductParams {
     unsigned int *err;
 };
 
-// columns (activation rows) of a tile: 8, 16 or 32
+// columns (activation rows) of a tile: 8 or 16
 template <int FMT>
 cudaError_t launch_product(bool down, int columns, const ProductParams &p, int max_tiles, const DeviceInfo &dev, cudaStream_t s);
+// tiles of 48 (see qmm_experts_tile.cuh): x: terms of rows under one power of two each; h: fp32
+template <int FMT>
+cudaError_t launch_tile(bool down, const ProductParams &p, int max_tiles, const DeviceInfo &dev, cudaStream_t s);
 // row by row
 template <int FMT>
 cudaError_t launch_single(bool down, const ProductParams &p, const DeviceInfo &dev, cudaStream_t s);

@@ -13,7 +13,7 @@
 namespace qmm {
 namespace experts {
 
-// How a tile of 8, 16 or 32 activation rows is worked on: by 8 warps of
+// How a tile of 8 or 16 activation rows is worked on: by 8 warps of
 // `m_tiles` tiles of 16 rows each. With 8 columns, where the work is decoding, one tile a warp, so
 // that few registers let many warps hide one another's latencies; of the first product, half of the
 // warps take gate's rows and half the same rows of up. Above, where activations' terms are read
@@ -474,10 +474,7 @@ template <int FMT, bool DOWN>
 cudaError_t launch_columns(int columns, const ProductParams &p, int max_tiles, const DeviceInfo &dev, cudaStream_t s) {
     switch (columns) {
     case 8: return launch_aligned<FMT, 8, DOWN>(p, max_tiles, dev, s);
-    case 16: return launch_aligned<FMT, 16, DOWN>(p, max_tiles, dev, s);
-    default:
-        if constexpr (FMT != F_BF16 && FMT != F_F16) return launch_aligned<FMT, 32, DOWN>(p, max_tiles, dev, s);
-        return cudaErrorInvalidValue;  // 16-bit weights have no 32 columns
+    default: return launch_aligned<FMT, 16, DOWN>(p, max_tiles, dev, s);
     }
 }
 

@@ -22,7 +22,7 @@ def magnitudes(fmt, w, k, n):
 
 def dot_error(x, mag, digits=False):
     """Bound on the error of x . w for rows x [p, k] and weights of sizes mag [n, k]: an x value is kept to 2^-22
-    of itself or 2^-38 of the largest of its block of 32; a block's products are summed by at most 6 tensor-core
+    of itself or 2^-38 of the largest of its block of 32, or of its row; a block's products are summed by at most 6 tensor-core
     steps that cut (2^-23 each, of the sizes summed) and its scales multiplied in fp32 (a few U); at most two
     additions per 16 values follow. With `digits` an x value is kept as three signed digits of 8 bits on one step
     for its block, which is at most 2^-22 of the block's largest: half of it, 2^-23, is lost at most."""
@@ -30,6 +30,8 @@ def dot_error(x, mag, digits=False):
     c = 2.0 ** -22 + (k / 8 + 80) * U
     pad = np.zeros((x.shape[0], -k % 32))
     top = np.abs(np.concatenate((x, pad), 1)).reshape(x.shape[0], -1, 32).max(-1).repeat(32, 1)[:, :k]
+    if not digits:
+        top = np.abs(x).max(1, keepdims=True).repeat(k, 1)
     return c * (np.abs(x) @ mag.T) + 2.0 ** (-23 if digits else -38) * (top @ mag.T)
 
 

@@ -278,3 +278,67 @@ def test_refuses_other_tensors():
                dict(y=torch.empty((2, 32), device=DEV)), dict(x=x.t().contiguous().t())):
         with pytest.raises(ValueError):
             c.call(**kw)
+
+
+# Experts with more than 20 rows each: tiles of up to 48 pairs, whole, partly filled and empty.
+@pytest.mark.parametrize("fmt,fmt_down,k,n_ff", [
+    ("q4_0", "q4_0", 32, 32), ("q4_0", "q5_0", 96, 160), ("q5_0", "q8_0", 288, 96), ("q8_0", "q8_0", 1376, 352),
+    ("q8_0", "q4_0", 32, 1056), ("q6_k", "q6_k", 256, 1280), ("q4_k", "q4_k", 1280, 256), ("q4_k", "q6_k", 512, 768),
+    ("q6_k", "q5_0", 768, 416), ("q5_0", "q4_k", 2080, 512)])
+@pytest.mark.parametrize("n_pos,n_exp,top_k", [(21, 1, 1), (48, 1, 1), (49, 1, 1), (97, 4, 2), (150, 2, 1)])
+def test_many_rows(fmt, fmt_down, k, n_ff, n_pos, n_exp, top_k):
+    Case("geglu" if n_pos == 97 else "swiglu", fmt, fmt_down, n_pos, k, n_ff, n_exp, top_k).check()
+
+
+def test_many_rows_accumulate_in_place_and_leave_slots_empty():
+    c = Case("swiglu", "q4_k", "q8_0", 60, 512, 256, 3, 2)
+    c.check(y0=np.random.default_rng(1).standard_normal((60, c.k)).astype(np.float32))
+    x = _dev(c.x)
+    c.check(y=c.call(x=x, y=x))
+    rng = np.random.default_rng(2)
+    c.ids[rng.random(c.ids.shape) < 0.2] = -1
+    c.ids[7] = -1
+    c.ids[8] = 2
+    c.check()
+    c.ids[:] = 1
+    c.check()
+
+
+def test_many_rows_of_any_size():
+    c = Case("swiglu", "q4_k", "q5_0", 64, 768, 512, 2, 1)
+    c.x *= np.exp2(np.random.default_rng(3).integers(-30, 30, (64, 1))).astype(np.float32)
+    c.x[5] = 0
+    c.check()
+
+
+def test_a_nan_or_inf_among_many_rows_stays_in_its_position():
+    c = Case("swiglu", "q8_0", "q4_k", 70, 512, 512, 2, 1)
+    clean = c.call().cpu().numpy()
+    c.x[3, 100], c.x[11, 7] = np.nan, np.inf
+    got = c.call().cpu().numpy()
+    bad = [3, 11]
+    assert not np.isfinite(got[bad]).any()
+    keep = np.setdiff1d(np.arange(70), bad)
+    assert np.array_equal(got[keep], clean[keep])
+
+
+def test_many_rows_captured_and_on_another_stream():
+    c = Case("swiglu", "q4_k", "q4_k", 130, 512, 256, 4, 2)
+    want = c.call().cpu().numpy()
+    x, y = _dev(c.x), torch.empty(130, c.k, device=DEV)
+    ids, weights = _dev(c.ids), _dev(c.weights)
+    c.call(x=x, ids=ids, weights=weights, y=y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.call(x=x, ids=ids, weights=weights, y=y)
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        y.zero_()
+        g.replay()
+        assert np.array_equal(y.cpu().numpy(), want)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            z = c.call(x=x, ids=ids, weights=weights)
+        s.synchronize()
+        assert np.array_equal(z.cpu().numpy(), want)
