@@ -5,12 +5,19 @@
 // the activations as two fp16 terms under one power of two per row; each block's sums start fresh, and are
 // multiplied by the block's scale in fp32 as they leave the tensor memory, so nothing of W is rounded and no sum in the
 // tensor cores, which cut what they add, is longer than 32 values. With a row of W per lane, as tensor memory has
-// them, a scale is decoded once and multiplies 32 sums, two per packed instruction.
+// them, a scale is decoded once and multiplies up to 48 sums, two per packed instruction.
 //
 // Warps 0 .. 3: a lane takes a row of W; unpacks a block's codes to tensor memory (two stages of A and D), then takes
-// the sums of the block before. Each copies its own rows into a ring of its own. Warp 4: one lane issues the products, four
-// per block (two 16-deep steps, the low term's first). Warp 5: copies the pairs' terms, 4 KB a
-// block, into the 128-byte swizzle that the products read.
+// the sums of the block before. Each copies its own rows into a ring of its own. Warp 4 copies the pairs' terms, 6 KB
+// a block, into the 128-byte swizzle that the products read, and one lane of it issues them: four per block (two
+// 16-deep steps, the low term's first).
+//
+// Bound by the warps that unpack and take, whose time hardly depends on the columns: 1390 instructions a block and CTA of
+// Q4_K, of which about 130 unpack, 190 take the mins and 360 the sums; issue slots 51 to 58 % used, the tensor pipe 11 %.
+// Four CTAs an SM (286 us with three, 259 with four, before the last change of the codes). Measured: 256 positions, Q4_K
+// 2048 x 1024, eight of 64 experts 274 us, of which the first product 178, the second 79 (mma.sync: 395); 128 rows an
+// expert at 2048 x 768 560 us (903). Blocks in pairs per handshake took 300 us instead of 268 (one stage of D, so that a
+// product waits for the sums before it), tiles of 32 columns 272 instead of 251.
 #pragma once
 
 #include "qmm_experts_kernel.cuh"
