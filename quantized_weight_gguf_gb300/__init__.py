@@ -745,6 +745,14 @@ def qmm_experts_ffn_workspace_bytes(args: qmm_experts_ffn_args) -> int:
     return load().qmm_experts_ffn_workspace_bytes(ctypes.byref(args))
 
 
+def _on_current_device(t):
+    """Refuses a tensor of another CUDA device than the current one, on which the kernels would be launched."""
+    torch = _torch()
+    now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # a third of current_device's time
+    if t.is_cuda and t.get_device() != now():
+        raise ValueError(f"the tensors are on {t.device}, which is not the current device")
+
+
 def _on_device(first, t, name, dtype, shape=None):
     """Refuses a tensor that is not contiguous `dtype` (of `shape`) on the CUDA device of `first`."""
     here = t.get_device()
@@ -843,6 +851,7 @@ def route_experts(logits, top_k: int, *, score="softmax", normalize=True, scale=
         weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
     else:
         _on_device(logits, weights, "weights", torch.float32, shape)
+    _on_current_device(logits)
     _call_route(logits.data_ptr(), row if n_pos > 1 else n_experts, n_pos, n_experts, top_k,
                 SCORES[score] if isinstance(score, str) else int(score), bool(normalize), scale, ids.data_ptr(),
                 weights.data_ptr(), _stream_of(stream, logits), 0)
@@ -877,6 +886,7 @@ def experts_ffn(act, fmt, w_gate, w_up, fmt_down, w_down, x, ids, weights, k: in
         _on_device(x, y, "y", torch.float32)
         if y.numel() != n_pos * k:
             raise ValueError(f"y must have x's {n_pos} x {k} values")
+    _on_current_device(x)
     handle = _stream_of(stream, x)
     _call_ffn.with_scratch(
         [ACTS[act] if isinstance(act, str) else int(act), _fmt(fmt), _fmt(fmt_down), w_gate.data_ptr(), w_up.data_ptr(),
@@ -954,6 +964,7 @@ def linear_attend(q, k, v, decay, state, lens=None, *, scale=None, out=None, sta
     out_shape, out_row = _head_rows("out", out, here)
     if out_shape != v_shape:
         raise ValueError("out must have v's shape")
+    _on_current_device(v)
     handle = _stream_of(stream, v)
     _call_linear.with_scratch(
         [q.data_ptr(), k.data_ptr(), v.data_ptr(), q_row, k_row, v_row, decay.data_ptr(), decay_row, state.data_ptr(),

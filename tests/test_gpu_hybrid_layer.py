@@ -107,3 +107,21 @@ def test_replayed_steps_are_the_eager_ones(example):
         graph.replay()
         assert torch.equal(x, y) and torch.equal(eager.state, captured.state)
     assert q.qmm_device_status() == 0
+
+
+def test_refuses_tensors_that_are_not_on_the_current_device(example, monkeypatch):
+    """The kernels go to the current device: with another one current, the calls launch nothing."""
+    layer = example.HybridLayer(seed=1, **SIZES)
+    x = torch.randn(2, 1, 256, device="cuda:0")
+    logits = torch.randn(2, 12, device="cuda:0")
+    ids, weights = q.route_experts(logits, 3)
+    heads = [torch.randn(2, 1, h, 32, device="cuda:0") for h in (2, 2, 4)]
+    decay = torch.zeros(4, device="cuda:0")
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        q.route_experts(logits, 3, ids=ids, weights=weights)
+    with pytest.raises(ValueError, match="current device"):
+        q.experts_ffn("swiglu", "q4_k", layer.w_gate, layer.w_up, "q6_k", layer.w_down, x.view(2, 256), ids, weights,
+                      256, 512, 12, y=torch.empty_like(x.view(2, 256)))
+    with pytest.raises(ValueError, match="current device"):
+        q.linear_attend(*heads, decay, layer.state, out=torch.empty_like(heads[2]))
