@@ -651,17 +651,19 @@ typedef struct qmm_linear_args {
 } qmm_linear_args;
 
 /* Decays are at most 0: greater ones count as 0, and -Inf clears the state
- * before its row (so do decays below -110, whose factor fp32 holds as 0). A NaN decay or a
- * k that is not finite makes the head's rows from its own on, and its state, NaN;
- * a v that is not finite those of its dim; a q that is not finite its row's outputs Inf or NaN.
- * Rows before are not touched by it. Sums and states are fp32 (sums of decays 64 bits). Up to 8 rows are taken one by one in
- * fp32; more in chunks of 32 on the tensor cores, where q, k, v and the state enter as two fp16
- * terms: of a value, 22 bits or 2^-38 of the largest of its row (q, k), of its dim in
- * the chunk (v, and v times its row's largest k as it adds to the state) or of its dim of the state, whichever is
- * more; of a score q . k, 22 bits or 2^-31 of
- * the product of the row's largest q and the chunk's largest k. The same call
- * gives the same result each time. Stream-ordered, no synchronization; scratch
- * as for qmm_matmul_ex (calls that can run concurrently pass their own). */
+ * before its row (so do decays below -110, whose factor fp32 holds as 0). A NaN
+ * decay or a k that is not finite makes the head's rows from its own on Inf or
+ * NaN and spoils its state (up to 8 rows: where that k reaches it); a v that is
+ * not finite does so for its dim; a q that is not finite makes its row's outputs
+ * Inf or NaN. Rows before are not touched by it. Sums and states are fp32 (sums
+ * of decays 64 bits). Up to 8 rows are taken one by one in fp32; more in chunks
+ * of 32 on the tensor cores, where q, k, v and the state enter as two fp16
+ * terms: of a value, 22 bits or 2^-38 of the largest of its row (q, k), of its
+ * dim in the chunk (v, and v times its row's largest k as it adds to the state)
+ * or of its dim of the state, whichever is more; of a score q . k, 22 bits or
+ * 2^-31 of the product of the row's largest q and the chunk's largest k. The
+ * same call gives the same result each time. Stream-ordered, no synchronization;
+ * scratch as for qmm_matmul_ex (calls that can run concurrently pass their own). */
 int qmm_linear_attend(const qmm_linear_args *a);
 
 /* Device scratch bytes qmm_linear_attend needs for *a; 0 when it needs none or

@@ -948,7 +948,10 @@ def linear_attend(q, k, v, decay, state, lens=None, *, scale=None, out=None, sta
         if n_heads > 1 and decay.stride(0) != 1:
             raise ValueError("decay's heads must be adjacent")
     elif d_shape == v_shape[:3]:
-        decay_row = _head_rows("decay", decay.unsqueeze(-1), here)[1]
+        s0, s1, s2 = decay.stride()
+        decay_row = s1 if n_new > 1 else s0 if n_seqs > 1 else n_heads
+        if (n_heads > 1 and s2 != 1) or (n_new > 1 and n_seqs > 1 and s0 != n_new * s1):
+            raise ValueError("decay: the heads of a row must be adjacent and rows equally spaced")
     else:
         raise ValueError(f"decay must be {tuple(v_shape[:3])} or ({n_heads},), got {tuple(d_shape)}")
     shape = (n_seqs, n_heads, dk, dv)

@@ -342,3 +342,37 @@ def test_many_rows_captured_and_on_another_stream():
             z = c.call(x=x, ids=ids, weights=weights)
         s.synchronize()
         assert np.array_equal(z.cpu().numpy(), want)
+
+
+def test_many_rows_on_two_streams_at_once():
+    """Both calls' CTAs share SMs and their tensor memory, also with the tensor-core product of qmm_matmul."""
+    cases = [Case("swiglu", f, f, 200, 1024, 512, 4, 2, seed=i) for i, f in enumerate(("q4_k", "q8_0"))]
+    want = [c.call().cpu().numpy() for c in cases]
+    args = [(_dev(c.x), _dev(c.ids), _dev(c.weights)) for c in cases]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [[torch.empty(200, 1024, device=DEV) for _ in range(6)] for _ in cases]
+    rng = np.random.default_rng(4)
+    w, x = _dev(qmm_synth.gen_weights("q4_k", 1024, 4096, rng)), _dev(rng.standard_normal((256, 1024)).astype(np.float32))
+    dense = q.matmul("q4_k", w, x, 1024, 4096)
+    torch.cuda.synchronize()
+    for i in range(6):
+        for c, a, s, o in zip(cases, args, streams, outs):
+            with torch.cuda.stream(s):
+                c.call(x=a[0], ids=a[1], weights=a[2], y=o[i])
+        with torch.cuda.stream(streams[2]):
+            again = q.matmul("q4_k", w, x, 1024, 4096)
+    torch.cuda.synchronize()
+    q.qmm_device_status()
+    assert torch.equal(again, dense)
+    for o, y in zip(outs, want):
+        assert all(np.array_equal(t.cpu().numpy(), y) for t in o)
+
+
+@pytest.mark.parametrize("n_pos", [30, 64])
+def test_many_rows_without_any_expert(n_pos):
+    c = Case("swiglu", "q4_k", "q4_k", n_pos, 256, 256, 1, 1)
+    c.ids[:] = -1
+    c.check()
+    c.ids[5] = 7                                 # of none
+    c.check(status=11)
+
