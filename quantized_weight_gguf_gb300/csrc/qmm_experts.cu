@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(kPrepareThreads) tile_terms_kernel(const __gri
             const float v = x[32 * i + lane] * up;
             const __half hi = __float2half_rn(v);
             const float f = __half2float(hi);
-            __half *const to = reinterpret_cast<__half *>(p.terms + row * p.x_row_bytes + (int64_t)i * kTermBytes) + tile_place(lane);
+            uint8_t *const block = p.terms + row * p.x_row_bytes + (int64_t)i * kTermBytes;
+            __half *const to = reinterpret_cast<__half *>(block) + tile_place(lane);
             to[0] = hi;
             to[32] = __float2half_rn(isfinite(f) ? v - f : 0.0f);
             if (p.fmt == F_Q4_K) {
@@ -327,7 +328,8 @@ Scratch scratch_of(const ExpertsFfn &f) {
 }
 
 template <int FMT>
-cudaError_t product_of(bool down, bool tile, int columns, const ProductParams &p, int tiles, const DeviceInfo &dev, cudaStream_t s) {
+cudaError_t product_of(bool down, bool tile, int columns, const ProductParams &p, int tiles, const DeviceInfo &dev,
+                       cudaStream_t s) {
     if constexpr (FMT != F_BF16 && FMT != F_F16)
         if (tile) return launch_tile<FMT>(down, p, tiles, dev, s);
     return columns == 1 ? launch_single<FMT>(down, p, dev, s)
@@ -381,7 +383,8 @@ cudaError_t launch_experts_ffn(const ExpertsFfn &f, const DeviceInfo &dev, cudaS
     const int64_t warps = f.n_pos * l.x_blocks;
     const int64_t blocks = std::min<int64_t>((warps + kPrepareWarps - 1) / kPrepareWarps, (int64_t)dev.sm_count * 8);
     const bool one = is_one(f);
-    if (l.tile) e = launch_next(tile_terms_kernel, a, 1 + std::min<int64_t>(f.n_pos, (int64_t)dev.sm_count * 8), kPrepareThreads, s);
+    const int64_t rows_at_once = (int64_t)dev.sm_count * 8;
+    if (l.tile) e = launch_next(tile_terms_kernel, a, 1 + std::min(f.n_pos, rows_at_once), kPrepareThreads, s);
     else if (!one) e = launch_next(prepare_kernel, a, 1 + blocks, kPrepareThreads, s);
     if (e != cudaSuccess) return e;
 
@@ -430,7 +433,7 @@ cudaError_t launch_experts_ffn(const ExpertsFfn &f, const DeviceInfo &dev, cudaS
         a.scales = p.h_scale;
         a.sums = p.h_sum;
         a.x_row_bytes = l.h_row_bytes;
-        e = launch_next(tile_terms_kernel, a, std::min<int64_t>(pairs, (int64_t)dev.sm_count * 8), kPrepareThreads, s);
+        e = launch_next(tile_terms_kernel, a, std::min<int64_t>(pairs, rows_at_once), kPrepareThreads, s);
         if (e != cudaSuccess) return e;
         p.h = ws + l.h;
     }

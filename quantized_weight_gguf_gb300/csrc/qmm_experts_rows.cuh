@@ -33,9 +33,10 @@ constexpr int kOneBlocks = 160;  // of x that one position's first product holds
 // Rows of W in a unit.
 __host__ __device__ constexpr int unit_rows(bool down) { return down ? 16 : 64; }
 
-// A record of a block of 32 activations, 144 bytes (8 records apart, lanes' 16-byte loads meet no bank twice): quantised weights: digits [3][32] (element e
-// is sum_i 256^i digit_i[e] times the scale), scale, sum, and per digit the sums of elements 0-15 and 16-31 as
-// 16-bit halves of a word; 16-bit weights: the values.
+// A record of a block of 32 activations, 144 bytes (eight lanes' 16-byte loads from records that lie one after the
+// other meet no bank twice). Quantised weights: digits [3][32] (element e is sum_i 256^i digit_i[e] times the
+// scale), scale, sum, and per digit the sums of elements 0-15 and 16-31 as 16-bit halves of a word; 16-bit weights:
+// the values.
 constexpr int kRecord = 144;
 __host__ __device__ constexpr bool is_16bit(int fmt) { return fmt == F_BF16 || fmt == F_F16; }
 

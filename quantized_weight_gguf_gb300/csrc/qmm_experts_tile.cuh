@@ -46,7 +46,8 @@ __host__ __device__ constexpr TileLayout tile_layout(int fmt, bool down) {
     const int x = kXSlots * (kXBytes + kTileColumns * 4), h = down ? 0 : kTileColumns * 64 * 4, bars = 256;
     // as many CTAs per SM as tensor memory has room for, if two stages of W fit beside them
     for (l.ctas = 512 / tile_tmem_cols(fmt); l.ctas > 1; --l.ctas) {
-        l.stages = (228 * 1024 / l.ctas - 1024 - 1024 - x - h - bars) / (kTileWarps * l.w_stage);  // 1 KB the system's, 1 KB for alignment
+        // (1 KB is the system's, 1 KB for alignment)
+        l.stages = (228 * 1024 / l.ctas - 1024 - 1024 - x - h - bars) / (kTileWarps * l.w_stage);
         if (l.stages >= 2) break;
     }
     if (l.stages > 4) l.stages = 4;
@@ -58,7 +59,7 @@ __host__ __device__ constexpr TileLayout tile_layout(int fmt, bool down) {
     return l;
 }
 
-// Tests the phase; a hint of how long to suspend the thread, which mbar_try_wait gives, made it sleep past the moment.
+// Tests the phase, and waits for it as long as the hardware does by itself.
 __device__ __forceinline__ bool try_now(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -70,7 +71,8 @@ __device__ __forceinline__ bool try_now(uint32_t bar, uint32_t parity) {
 }
 // Waits for the phase, up to the limit; then, or when another warp has given up, goes on all the same: the
 // results are wrong and reported, and every later wait is short.
-__device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, volatile int *stop, unsigned int *err, unsigned int code) {
+__device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, volatile int *stop, unsigned int *err,
+                                         unsigned int code) {
     if (try_now(bar, parity)) return;
     uint64_t t0 = 0;
     for (uint32_t i = 1; !try_now(bar, parity); ++i) {
@@ -87,7 +89,8 @@ __device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, volatile
 // An arrival by the warp's first lane, for all of it.
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
     __syncwarp();
-    asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar), "r"(lane)
+    asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar),
+                 "r"(lane)
                  : "memory");
 }
 
@@ -201,7 +204,8 @@ struct TileRow<F_Q6_K> {
 };
 
 template <int FMT, bool DOWN>
-__global__ void __launch_bounds__(kTileThreads, tile_layout(FMT, DOWN).ctas) tile_kernel(const __grid_constant__ ProductParams p) {
+__global__ void __launch_bounds__(kTileThreads, tile_layout(FMT, DOWN).ctas)
+    tile_kernel(const __grid_constant__ ProductParams p) {
     constexpr TileLayout L = tile_layout(FMT, DOWN);
     constexpr int KB = chunk_k(FMT) / 32, CB = chunk_bytes(FMT), NP = L.pieces, PITCH = 16 * NP, NS = L.stages;
     constexpr int SUMS = tile_sums(FMT), SC = tile_stage_cols(FMT);
@@ -247,7 +251,8 @@ __global__ void __launch_bounds__(kTileThreads, tile_layout(FMT, DOWN).ctas) til
 
     if (warp == kTileWarps) {
         // ---- the pairs' terms, and the products ----
-        const int64_t blocks = (int)blockIdx.x < units ? (int64_t)((units - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * p.blocks : 0;
+        const int mine = (int)blockIdx.x < units ? (units - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+        const int64_t blocks = (int64_t)mine * p.blocks;
         int load_unit = blockIdx.x, load_block = 0, load_x = 0, x = 0, s = 0;
         uint32_t load_px = 1, px = 0, ps = 0;  // (a fresh barrier: the phase before has completed)
         const uint8_t *from[kTileColumns / 4] = {};
@@ -505,7 +510,8 @@ __global__ void __launch_bounds__(kTileThreads, tile_layout(FMT, DOWN).ctas) til
                 for (int c = 0; c < kTileColumns / 2; ++c) {
                     if (c % 8 == 0 && c / 8 >= groups) break;
                     const int at = 2 * c + matrix;
-                    const float scale_of = __shfl_sync(~0u, x_scale[c / 16], at & 31), w = __shfl_sync(~0u, weight[c / 16], at & 31);
+                    const float scale_of = __shfl_sync(~0u, x_scale[c / 16], at & 31);
+                    const float w = __shfl_sync(~0u, weight[c / 16], at & 31);
                     const float other = across[at * 64] * scale_of, own = half_of(sum[c], matrix) * scale_of;
                     const float gate = matrix == 0 ? own : other, up = matrix == 0 ? other : own;
                     if (at < tile.count && r < p.rows) h[(int64_t)at * p.rows] = glu_gate(gate, glu_arg(p.act, gate)) * up * w;

@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
                 next_decay = load_decay(row + 2 * C);
             }
         }
-        const float *const gh = gs + buffer * kDecayFloats, *const gl = gh + C, *const from_start = gl + C, *const to_end = from_start + C;
+        const float *const gh = gs + buffer * kDecayFloats, *const gl = gh + C;
+        const float *const from_start = gl + C, *const to_end = from_start + C;
         const int ke = k_exp[lane];
         const int k_top = __reduce_max_sync(~0u, ke);
         // the first row that a k or decay makes NaN
@@ -443,8 +444,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
         }
 
         // this warp's dims of v: values of rows 16 step + 2t, +1, +8, +9, dims g and g + 8
-        const float *const vp = reinterpret_cast<const float *>(smem + plan.raw_v + buffer * plan.v_bytes) + 2 * t * (tile_cols + 4) + warp * 16 + g;
         const int v_pitch = tile_cols + 4;
+        const float *const vp =
+            reinterpret_cast<const float *>(smem + plan.raw_v + buffer * plan.v_bytes) + 2 * t * v_pitch + warp * 16 + g;
         float v[2][2][4];  // [step][dim][row]
         float top[2] = {0, 0};
         int v_bad[2] = {C, C};  // first row of each dim that is not finite
