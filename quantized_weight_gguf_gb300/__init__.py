@@ -881,7 +881,8 @@ def experts_ffn(act, fmt, w_gate, w_up, fmt_down, w_down, x, ids, weights, k: in
     if w_up.numel() * w_up.element_size() != w_len:
         raise ValueError("w_gate and w_up must have the same size")
     if y is None:
-        y = (torch.zeros if accumulate else torch.empty)((n_pos, k), dtype=torch.float32, device=x.device)
+        # nothing to add to (zeros would be filled on torch's current stream, which `stream` does not wait for)
+        y, accumulate = torch.empty((n_pos, k), dtype=torch.float32, device=x.device), False
     else:
         _on_device(x, y, "y", torch.float32)
         if y.numel() != n_pos * k:
