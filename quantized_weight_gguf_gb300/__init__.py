@@ -869,6 +869,9 @@ def experts_ffn(act, fmt, w_gate, w_up, fmt_down, w_down, x, ids, weights, k: in
     if x.dim() == 1:
         x = x.unsqueeze(0)
     if ids.dim() == 1:
+        if not weights.is_contiguous():
+            # (a copy would be made on torch's current stream, which `stream` does not wait for)
+            raise ValueError("weights must be contiguous")
         ids, weights = ids.unsqueeze(0), weights.reshape(1, -1)
     n_pos, top_k = ids.shape
     _on_device(x, x, "x", torch.float32, (n_pos, k))

@@ -44,3 +44,14 @@ def test_adding_to_no_y_is_the_sum_alone(n_pos):
     y = call(accumulate=True, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+def test_weights_that_would_have_to_be_copied_are_refused():
+    call, ids, weights = _case(1, top_k=8)
+    want = call()
+    assert torch.equal(call(ids=ids[0], weights=weights[0]), want)
+    assert torch.equal(call(ids=ids[0], weights=weights), want)
+    with pytest.raises(ValueError):
+        call(ids=ids[0], weights=weights.view(4, 2).t())
+    with pytest.raises(ValueError):
+        call(ids=ids[0], weights=weights.repeat(2, 1).t()[:, 0].as_strided((8,), (2,)))
