@@ -657,11 +657,13 @@ typedef struct qmm_linear_args {
  * not finite does so for its dim; a q that is not finite makes its row's outputs
  * Inf or NaN. Rows before are not touched by it. Sums and states are fp32 (sums
  * of decays 64 bits). Up to 8 rows are taken one by one in fp32; more in chunks
- * of 32 on the tensor cores, where q, k, v and the state enter as two fp16
- * terms: of a value, 22 bits or 2^-38 of the largest of its row (q, k), of its
- * dim in the chunk (v, and v times its row's largest k as it adds to the state)
- * or of its dim of the state, whichever is more; of a score q . k, 22 bits or
- * 2^-31 of the product of the row's largest q and the chunk's largest k. The
+ * of 32 on the tensor cores. There q, k and the state enter as two fp16 terms: of a
+ * value, 22 bits or 2^-38 of the largest of its row (q, k) or of its dim of the
+ * state, whichever is more; scores q . k and v as three bf16 terms, all 24 bits.
+ * What a row adds to the state is k times v's products with the row's largest k,
+ * of which 22 bits or 2^-38 of the largest of its dim in the chunk are kept, as
+ * the decays leave them at the chunk's end. A row is so no less exact for
+ * rows after it, or for rows that it has forgotten, be they ever so large. The
  * same call gives the same result each time. Stream-ordered, no synchronization;
  * scratch as for qmm_matmul_ex (calls that can run concurrently pass their own). */
 int qmm_linear_attend(const qmm_linear_args *a);

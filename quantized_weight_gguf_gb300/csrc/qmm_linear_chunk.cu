@@ -9,7 +9,9 @@
 // accumulator fragments of m16n8k16, which are A fragments of S^T Q^T as they
 // stand. The 32 x 32 scores are shared: one 16 x 8 tile a warp. fp32 values enter
 // as two fp16 terms (22 bits) under powers of two per row of q and k and per
-// dim of v and S, three products of terms each; accumulators start fresh after at most
+// dim of S and of what a chunk adds to it, three products of terms each; scores times v, the
+// smallest of the four, as three bf16 terms and six products, which need no power of two: a row's
+// scores are of very different sizes where decays are strong. Accumulators start fresh after at most
 // 32 values of depth and the small products come first, since the
 // tensor cores cut what they add. Sums of decays are formed in 64 bits and kept as
 // two floats, so that differences of long sums stay exact.
@@ -18,7 +20,7 @@
 // first (one product of the four), a scan over the segments, then everything.
 //
 // Bound by instructions at 16 warps an SM, whose states take the registers: 2420 of a warp a chunk at dk = dv = 128, of
-// which 228 are products; the issue slots are half used, the tensor pipe 36 %, shared memory's data path 57 %.
+// which 246 are products; the issue slots are half used, the tensor pipe 36 %, shared memory's data path 57 %.
 // Measured: 12001 rows of 16 heads of 128 / 128 310 us (92 the segments' own states, 210 the second pass), six ragged
 // sequences to 1777 rows of 12 heads of 64 / 96 133 us, against 58 and 17 us that their bytes take. The decays' sums in
 // one warp, terms in vectors and factors read instead of formed took the first from 477 us.
@@ -44,12 +46,13 @@ struct ChunkParams {
 };
 
 // Shared memory, in bytes from its start: q and k as they come, v of two
-// chunks, q and k as terms, the scores as terms, small arrays.
+// chunks, q and k as two terms each, the scores as three, small arrays.
 struct Plan {
     int raw_q, raw_k, raw_v, v_bytes, q16, k16, term, p16, p_term, small, bytes;
 };
 __host__ __device__ constexpr int pitch_of(int dk) { return (dk + 8) * 2; }  // 8 rows of 16 bytes on different banks
 constexpr int kPPitch = (C + 8) * 2;
+constexpr int kScoreUnit = 24;  // scores, at most 2^37 times k's power of two, in units of 2^24: no larger than k
 // Of the sums G_i of a chunk's decays: high and low parts, e^(G_i), e^(G_C - G_i), and (padded) e^(G_C).
 constexpr int kDecayFloats = 4 * C + 4;
 __host__ __device__ constexpr Plan plan_of(int dk, int tile) {
@@ -63,12 +66,13 @@ __host__ __device__ constexpr Plan plan_of(int dk, int tile) {
     p.k16 = p.q16 + 2 * p.term;
     p.p_term = C * kPPitch;
     p.p16 = p.k16 + 2 * p.term;
-    p.small = p.p16 + 2 * p.p_term;
+    p.small = p.p16 + 3 * p.p_term;
     p.bytes = p.small + (2 * kDecayFloats + 3 * C) * 4;
     return p;
 }
 
-#define QMM_MMA "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+#define QMM_MMA_OF(T) "mma.sync.aligned.m16n8k16.row.col.f32." T "." T ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+#define QMM_MMA QMM_MMA_OF("f16")
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm(QMM_MMA "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -80,7 +84,14 @@ __device__ __forceinline__ void mma_new(float (&c)[4], const uint32_t (&a)[4], u
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
+// bf16 operands
+__device__ __forceinline__ void mma_bf(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm(QMM_MMA_OF("bf16") "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 #undef QMM_MMA
+#undef QMM_MMA_OF
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -111,14 +122,24 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&r);
 }
+// Two values as bf16 pairs: three terms that are cut, 8 bits each, so that they hold all 24.
+__device__ __forceinline__ void cut3(float x, float y, uint32_t (&t)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+        t[i] = prmt(a, b, 0x7632u);
+        x -= __uint_as_float(a & 0xFFFF0000u);
+        y -= __uint_as_float(b & 0xFFFF0000u);
+    }
+}
 // The exponent that brings values whose largest has this biased exponent to
 // [2^14, 2^15) is -e; it stays in what 2^e and 2^-e can be as normal numbers.
 __device__ __forceinline__ int exponent_for(uint32_t biased) {
     const int e = (int)biased - 127 - 14;
     return biased == 255 ? 0 : e < -126 ? -126 : e;
 }
-// 2^n, 0 below the normal numbers, Inf above
-__device__ __forceinline__ float pow2(int n) { return __uint_as_float((uint32_t)(min(max(n, -127), 128) + 127) << 23); }
+// 2^n, 0 below the normal numbers, 2^127 above
+__device__ __forceinline__ float pow2(int n) { return __uint_as_float((uint32_t)(min(max(n, -127), 127) + 127) << 23); }
 __device__ __forceinline__ uint32_t exponent_bits(float v) { return (__float_as_uint(v) >> 23) & 255u; }
 // 2^-exponent_for()
 __device__ __forceinline__ float up_for(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
@@ -346,7 +367,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
         const float *const gh = gs + buffer * kDecayFloats, *const gl = gh + C;
         const float *const from_start = gl + C, *const to_end = from_start + C;
         const int ke = k_exp[lane];
-        const int k_top = __reduce_max_sync(~0u, ke);
+        // the largest k's exponent among the rows as they are decayed at the chunk's end
+        const int k_top = __reduce_max_sync(~0u, __float2int_ru((float)ke + (gh[C - 1] - gh[lane])));
         // the first row that a k or decay makes NaN
         const uint32_t bad_rows = __ballot_sync(~0u, k_bad[lane] || gh[lane] != gh[lane]);
         const int bad_from = bad_rows ? __ffs(bad_rows) - 1 : C;
@@ -354,8 +376,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
         float o[4][4];
         int se[2];
         if (OUT) {
-            const float k_scale = pow2(ke - k_top - 22);
-            // scores: 16 x 8 tiles (the two right of the diagonal are never read)
+            // scores: 16 x 8 tiles (the two right of the diagonal are never read), in units of q's power of two and
+            // 2^kScoreUnit. Three bf16 terms hold a score, and one of v, without a power of two of their own: one shared
+            // by rows would be that of the largest, be it after a row or forgotten before it.
+            const float k_scale = pow2(ke);
             for (int i = warp; i < 6; i += nw) {
                 const int mi = i < 2 ? 0 : 1, nj = i < 2 ? i : i - 2;
                 float cross[4] = {0, 0, 0, 0}, main[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
@@ -379,15 +403,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
                 for (int u = 0; u < 2; ++u) {
                     const int r = mi * 16 + 8 * u + g;
                     const float rh = gh[r], rl = gl[r];
-                    const float dot0 = main[0][2 * u] + main[1][2 * u] + cross[2 * u];
-                    const float dot1 = main[0][2 * u + 1] + main[1][2 * u + 1] + cross[2 * u + 1];
-                    const float v0 = c <= r ? dot0 * (exp2f((rh - ch.x) + (rl - cl.x)) * k0) : 0.0f;
-                    const float v1 = c + 1 <= r ? dot1 * (exp2f((rh - ch.y) + (rl - cl.y)) * k1) : 0.0f;
-                    uint32_t hi, lo;
-                    split2(v0, v1, hi, lo);
+                    constexpr float unit = 1.0f / (1 << kScoreUnit);
+                    const float dot0 = (main[0][2 * u] + main[1][2 * u] + cross[2 * u]) * unit;
+                    const float dot1 = (main[0][2 * u + 1] + main[1][2 * u + 1] + cross[2 * u + 1]) * unit;
+                    const float v0 = c <= r ? dot0 * exp2f((rh - ch.x) + (rl - cl.x)) * k0 : 0.0f;
+                    const float v1 = c + 1 <= r ? dot1 * exp2f((rh - ch.y) + (rl - cl.y)) * k1 : 0.0f;
+                    uint32_t terms[3];
+                    cut3(v0, v1, terms);
                     uint8_t *const dst = smem + plan.p16 + r * kPPitch + c * 2;
-                    *reinterpret_cast<uint32_t *>(dst) = hi;
-                    *reinterpret_cast<uint32_t *>(dst + plan.p_term) = lo;
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) *reinterpret_cast<uint32_t *>(dst + x * plan.p_term) = terms[x];
                 }
             }
 
@@ -443,104 +468,87 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
             __syncthreads();  // scores are there
         }
 
-        // this warp's dims of v: values of rows 16 step + 2t, +1, +8, +9, dims g and g + 8
+        // this warp's dims of v, of which each lane has its own: rows 16 k + 2t, +1, +8, +9, dims g and g + 8
         const int v_pitch = tile_cols + 4;
-        const float *const vp =
-            reinterpret_cast<const float *>(smem + plan.raw_v + buffer * plan.v_bytes) + 2 * t * v_pitch + warp * 16 + g;
-        float v[2][2][4];  // [step][dim][row]
-        float top[2] = {0, 0};
+        float *const vp = reinterpret_cast<float *>(smem + plan.raw_v + buffer * plan.v_bytes) + 2 * t * v_pitch + warp * 16 + g;
+        auto v_at = [&](int k, int u, int i) -> float & { return vp[(16 * k + (i & 1) + 8 * (i >> 1)) * v_pitch + 8 * u]; };
         int v_bad[2] = {C, C};  // first row of each dim that is not finite
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[k][u][i] = vp[(16 * k + (i & 1) + 8 * (i >> 1)) * v_pitch + 8 * u];
-                    top[u] = top_of(top[u], v[k][u][i]);
-                }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) top[u] = top_over_4(top[u]);
-        if (__any_sync(~0u, !finite(top[0]) || !finite(top[1]))) {
-            // they must not meet the zeros of rows before them: taken out, and the dim's rows from them on become NaN
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                top[u] = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (exponent_bits(v[k][u][i]) == 255) {
-                            v_bad[u] = min(v_bad[u], 16 * k + 2 * t + (i & 1) + 8 * (i >> 1));
-                            v[k][u][i] = 0.0f;
-                        }
-                        top[u] = top_of(top[u], v[k][u][i]);
-                    }
-                top[u] = top_over_4(top[u]);
-                v_bad[u] = min(v_bad[u], __shfl_xor_sync(~0u, v_bad[u], 1));
-                v_bad[u] = min(v_bad[u], __shfl_xor_sync(~0u, v_bad[u], 2));
-            }
-        }
-        int ve[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            ve[u] = exponent_of(top[u]);
-            const float up = up_for(ve[u]);
+        {
+            float top = 0.0f;
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[k][u][i] *= up;
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = top_of(top, v_at(k, u, i));
+            if (__any_sync(~0u, !finite(top))) {
+                // they must not meet the zeros of rows before them: taken out, and the dim's rows from them on become NaN
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (exponent_bits(v_at(k, u, i)) == 255) {
+                                v_bad[u] = min(v_bad[u], 16 * k + 2 * t + (i & 1) + 8 * (i >> 1));
+                                v_at(k, u, i) = 0.0f;
+                            }
+                    v_bad[u] = min(v_bad[u], __shfl_xor_sync(~0u, v_bad[u], 1));
+                    v_bad[u] = min(v_bad[u], __shfl_xor_sync(~0u, v_bad[u], 2));
+                }
+            }
         }
 
         if (OUT) {
-            // what the chunk's own rows give: V^T P^T
-            float c[4][4];
-            uint32_t ah[2][4], al[2][4];
+            // what the chunk's own rows give: V^T P^T, products of terms down to 2^-16 of the first ones'
+            float c[4][4] = {};
+            uint32_t first[2][4];
+            const uint32_t pb = base + plan.p16 + ((lane & 7) + ((lane >> 4) << 3)) * kPPitch + ((lane >> 3) & 1) * 16;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t a[3][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t terms[3];
+                    cut3(v_at(k, i & 1, 2 * (i >> 1)), v_at(k, i & 1, 2 * (i >> 1) + 1), terms);
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) a[x][i] = terms[x];
+                    first[k][i] = terms[0];
+                }
+#pragma unroll
+                for (int np = k; np < 2; ++np) {
+                    uint32_t b[3][4];
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) ldm4(b[x], pb + np * 16 * kPPitch + k * 32 + x * plan.p_term);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float(&d)[4] = c[2 * np + h];
+                        mma_bf(d, a[2], b[0][2 * h], b[0][2 * h + 1]);
+                        mma_bf(d, a[1], b[1][2 * h], b[1][2 * h + 1]);
+                        mma_bf(d, a[0], b[2][2 * h], b[2][2 * h + 1]);
+                        mma_bf(d, a[1], b[0][2 * h], b[0][2 * h + 1]);
+                        mma_bf(d, a[0], b[1][2 * h], b[1][2 * h + 1]);
+                    }
+                }
+            }
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) split2(v[k][i & 1][2 * (i >> 1)], v[k][i & 1][2 * (i >> 1) + 1], ah[k][i], al[k][i]);
-            const uint32_t pb = base + plan.p16 + ((lane & 7) + ((lane >> 4) << 3)) * kPPitch + ((lane >> 3) & 1) * 16;
+                for (int np = k; np < 2; ++np) {
+                    uint32_t b[4];
+                    ldm4(b, pb + np * 16 * kPPitch + k * 32);
 #pragma unroll
-            for (int np = 0; np < 2; ++np) {
-                uint32_t bh[2][4], bl[2][4];
-#pragma unroll
-                for (int k = 0; k <= np; ++k) {
-                    ldm4(bh[k], pb + np * 16 * kPPitch + k * 32);
-                    ldm4(bl[k], pb + np * 16 * kPPitch + k * 32 + plan.p_term);
+                    for (int h = 0; h < 2; ++h) mma_bf(c[2 * np + h], first[k], b[2 * h], b[2 * h + 1]);
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float(&d)[4] = c[2 * np + h];
-                    mma_new(d, al[0], bh[0][2 * h], bh[0][2 * h + 1]);
-                    mma(d, ah[0], bl[0][2 * h], bl[0][2 * h + 1]);
-                    if (np) {
-                        mma(d, al[1], bh[1][2 * h], bh[1][2 * h + 1]);
-                        mma(d, ah[1], bl[1][2 * h], bl[1][2 * h + 1]);
-                    }
-                    mma(d, ah[0], bh[0][2 * h], bh[0][2 * h + 1]);
-                    if (np) mma(d, ah[1], bh[1][2 * h], bh[1][2 * h + 1]);
-                }
-            }
-            // the larger of the two parts' powers of two is taken out of both
-            float of_state[2], of_chunk[2];
-            int common[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int chunk = k_top + 22 + ve[u];
-                common[u] = max(se[u], chunk);
-                of_state[u] = pow2(se[u] - common[u]);
-                of_chunk[u] = pow2(chunk - common[u]);
-            }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const float2 a = *reinterpret_cast<const float2 *>(from_start + 8 * n + 2 * t);
                 const int2 e = *reinterpret_cast<const int2 *>(q_exp + 8 * n + 2 * t);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int u = i >> 1;
-                    const float sum = fmaf(c[n][i], of_chunk[u], o[n][i] * (of_state[u] * (i & 1 ? a.y : a.x)));
-                    o[n][i] = sum * pow2((i & 1 ? e.y : e.x) + common[u]) * l.scale;
+                    const int row_e = i & 1 ? e.y : e.x;
+                    const float of_state = o[n][i] * ((i & 1 ? a.y : a.x) * pow2(row_e + se[i >> 1]));
+                    o[n][i] = fmaf(c[n][i], pow2(row_e + kScoreUnit), of_state) * l.scale;
                 }
             }
             if (__any_sync(~0u, min(bad_from, min(v_bad[0], v_bad[1])) < C)) {
@@ -568,6 +576,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
             const float f = to_end[lane] * pow2(ke - k_top);
             uint32_t ah[2][4], al[2][4];
             // the products' own largest sets their power of two: an old row's v may be large and forgotten
+            float v[2][2][4];  // [step][dim][row]
             float most[2] = {0, 0};
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -578,7 +587,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        v[k][u][i] *= fr[i];
+                        v[k][u][i] = v_at(k, u, i) * fr[i];
                         most[u] = fmaxf(most[u], fabsf(v[k][u][i]));
                     }
             }
@@ -599,7 +608,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
             const float keep = bad_from < C ? NAN : gh[4 * C];
             float gain[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) gain[u] = v_bad[u] < C ? NAN : pow2(k_top + ve[u] + be[u]);
+            for (int u = 0; u < 2; ++u) gain[u] = v_bad[u] < C ? NAN : pow2(k_top + be[u]);
             const uint32_t kb = base + plan.k16 + ((lane & 7) + (((lane >> 3) & 1) << 3)) * PITCH + (lane >> 4) * 16;
 #pragma unroll
             for (int n2 = 0; n2 < KS; ++n2) {
