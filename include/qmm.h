@@ -659,11 +659,14 @@ typedef struct qmm_linear_args {
  * of decays 64 bits). Up to 8 rows are taken one by one in fp32; more in chunks
  * of 32 on the tensor cores. There q, k and the state enter as two fp16 terms: of a
  * value, 22 bits or 2^-38 of the largest of its row (q, k) or of its dim of the
- * state, whichever is more; scores q . k and v as three bf16 terms, all 24 bits.
+ * state, whichever is more; scores q . k and v as three bf16 terms: 24 bits, or
+ * 2^-123 of the row's largest q (scores) and 2^-133 (v), whichever is more.
  * What a row adds to the state is k times v's products with the row's largest k,
  * of which 22 bits or 2^-38 of the largest of its dim in the chunk are kept, as
  * the decays leave them at the chunk's end. A row is so no less exact for
  * rows after it, or for rows that it has forgotten, be they ever so large. The
+ * factors of decays over several rows are fp32 numbers: below 2^-126 they have fewer
+ * bits, below 2^-149 they are 0. What passes fp32's largest number is Inf or NaN. The
  * same call gives the same result each time. Stream-ordered, no synchronization;
  * scratch as for qmm_matmul_ex (calls that can run concurrently pass their own). */
 int qmm_linear_attend(const qmm_linear_args *a);

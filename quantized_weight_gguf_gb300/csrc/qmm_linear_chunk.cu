@@ -27,6 +27,8 @@
 #include "qmm_device.cuh"
 #include "qmm_linear.h"
 
+#include <type_traits>
+
 #include <cuda_fp16.h>
 
 namespace qmm {
@@ -52,7 +54,12 @@ struct Plan {
 };
 __host__ __device__ constexpr int pitch_of(int dk) { return (dk + 8) * 2; }  // 8 rows of 16 bytes on different banks
 constexpr int kPPitch = (C + 8) * 2;
-constexpr int kScoreUnit = 24;  // scores, at most 2^37 times k's power of two, in units of 2^24: no larger than k
+// Scores, at most 2^37 times q's and k's powers of two, in units of 2^24: no larger than k.
+constexpr int kScoreUnit = 24;
+// bf16 terms end at 2^-133: where all of a chunk's k have powers of two below this one they are multiplied up to it,
+// and dims of v below 2^-64 by 2^64.
+constexpr int kTinyK = -40, kTinyUp = 64;
+constexpr uint32_t kTinyBits = 0x1F800000;  // 2^-64
 // Of the sums G_i of a chunk's decays: high and low parts, e^(G_i), e^(G_C - G_i), and (padded) e^(G_C).
 constexpr int kDecayFloats = 4 * C + 4;
 __host__ __device__ constexpr Plan plan_of(int dk, int tile) {
@@ -138,9 +145,17 @@ __device__ __forceinline__ int exponent_for(uint32_t biased) {
     const int e = (int)biased - 127 - 14;
     return biased == 255 ? 0 : e < -126 ? -126 : e;
 }
+// 2^n, of the normal numbers
+__device__ __forceinline__ float pow2_of(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }
+__device__ __forceinline__ bool is_normal(int n) { return (uint32_t)(n + 126) <= 253u; }
 // 2^n, 0 below the normal numbers, 2^127 above
 __device__ __forceinline__ float pow2(int n) { return __uint_as_float((uint32_t)(min(max(n, -127), 127) + 127) << 23); }
 __device__ __forceinline__ uint32_t exponent_bits(float v) { return (__float_as_uint(v) >> 23) & 255u; }
+// 2^n times v, for n to twice what a float's exponent can be
+__device__ __forceinline__ float times_pow2(float v, int n) {
+    const int m = min(max(n, -126), 127);
+    return v * pow2(n - m) * pow2_of(m);
+}
 // 2^-exponent_for()
 __device__ __forceinline__ float up_for(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
 // max(top, |v|), NaN if v is
@@ -330,7 +345,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
                     }
                     if (lane == 0) k_bad[i] = bad;
                 }
-                const int e = exponent_for(top >> 23);
+                const int e = is_k || top ? exponent_for(top >> 23) : 0;
                 const float up = up_for(e);
                 if (lane == 0) (is_k ? k_exp : q_exp)[i] = e;
                 uint8_t *const hi = smem + (is_k ? plan.k16 : plan.q16) + i * PITCH + lane * V * 2, *const lo = hi + plan.term;
@@ -369,17 +384,20 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
         const int ke = k_exp[lane];
         // the largest k's exponent among the rows as they are decayed at the chunk's end
         const int k_top = __reduce_max_sync(~0u, __float2int_ru((float)ke + (gh[C - 1] - gh[lane])));
+        const int k_up = max(0, kTinyK - __reduce_max_sync(~0u, ke));
         // the first row that a k or decay makes NaN
         const uint32_t bad_rows = __ballot_sync(~0u, k_bad[lane] || gh[lane] != gh[lane]);
         const int bad_from = bad_rows ? __ffs(bad_rows) - 1 : C;
 
         float o[4][4];
         int se[2];
+        bool wide = false;  // the outputs' parts have powers of two that are not normal numbers: applied in two factors
+        const int c_exp = kScoreUnit - k_up;
         if (OUT) {
             // scores: 16 x 8 tiles (the two right of the diagonal are never read), in units of q's power of two and
-            // 2^kScoreUnit. Three bf16 terms hold a score, and one of v, without a power of two of their own: one shared
-            // by rows would be that of the largest, be it after a row or forgotten before it.
-            const float k_scale = pow2(ke);
+            // 2^kScoreUnit. Three bf16 terms hold a score, and one of v, without a power of two that rows share: it
+            // would be that of the largest, be it after a row or forgotten before it.
+            const float k_scale = pow2(ke + k_up);
             for (int i = warp; i < 6; i += nw) {
                 const int mi = i < 2 ? 0 : 1, nj = i < 2 ? i : i - 2;
                 float cross[4] = {0, 0, 0, 0}, main[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
@@ -427,6 +445,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
                 se[u] = exponent_of(top_over_4(top[u]));
                 up[u] = up_for(se[u]);
             }
+            const int q_e = q_exp[lane], q_low = __reduce_min_sync(~0u, q_e), q_high = __reduce_max_sync(~0u, q_e);
+            wide = __any_sync(~0u, q_low + min(c_exp, min(se[0], se[1])) < -126 || q_high + max(c_exp, max(se[0], se[1])) > 127);
 #pragma unroll
             for (int k2 = 0; k2 < KS; k2 += 2) {
                 float c[4][4];
@@ -473,18 +493,22 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
         float *const vp = reinterpret_cast<float *>(smem + plan.raw_v + buffer * plan.v_bytes) + 2 * t * v_pitch + warp * 16 + g;
         auto v_at = [&](int k, int u, int i) -> float & { return vp[(16 * k + (i & 1) + 8 * (i >> 1)) * v_pitch + 8 * u]; };
         int v_bad[2] = {C, C};  // first row of each dim that is not finite
+        int v_up[2] = {0, 0};
         {
-            float top = 0.0f;
+            float v_top[2] = {0, 0};
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) top = top_of(top, v_at(k, u, i));
-            if (__any_sync(~0u, !finite(top))) {
-                // they must not meet the zeros of rows before them: taken out, and the dim's rows from them on become NaN
+                    for (int i = 0; i < 4; ++i) v_top[u] = top_of(v_top[u], v_at(k, u, i));
+            auto plain = [](float top) { return __float_as_uint(top) - kTinyBits < 0x7F800000u - kTinyBits; };  // neither tiny nor not finite
+            if (__any_sync(~0u, !plain(v_top[0]) || !plain(v_top[1]))) {
+                // tiny ones are multiplied up; those that are not finite must not meet the zeros of rows before them: they
+                // are taken out, and the dim's rows from them on become NaN
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
+                    if (__float_as_uint(top_over_4(v_top[u])) < kTinyBits) v_up[u] = kTinyUp;
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -503,6 +527,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
             // what the chunk's own rows give: V^T P^T, products of terms down to 2^-16 of the first ones'
             float c[4][4] = {};
             uint32_t first[2][4];
+            const float v_scale[2] = {pow2_of(v_up[0]), pow2_of(v_up[1])};
             const uint32_t pb = base + plan.p16 + ((lane & 7) + ((lane >> 4) << 3)) * kPPitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -510,7 +535,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t terms[3];
-                    cut3(v_at(k, i & 1, 2 * (i >> 1)), v_at(k, i & 1, 2 * (i >> 1) + 1), terms);
+                    cut3(v_at(k, i & 1, 2 * (i >> 1)) * v_scale[i & 1], v_at(k, i & 1, 2 * (i >> 1) + 1) * v_scale[i & 1], terms);
 #pragma unroll
                     for (int x = 0; x < 3; ++x) a[x][i] = terms[x];
                     first[k][i] = terms[0];
@@ -540,17 +565,24 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
 #pragma unroll
                     for (int h = 0; h < 2; ++h) mma_bf(c[2 * np + h], first[k], b[2 * h], b[2 * h + 1]);
                 }
+            const bool in_two = wide || __any_sync(~0u, v_up[0] + v_up[1]);
+            auto join = [&](auto two) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const float2 a = *reinterpret_cast<const float2 *>(from_start + 8 * n + 2 * t);
-                const int2 e = *reinterpret_cast<const int2 *>(q_exp + 8 * n + 2 * t);
+                for (int n = 0; n < 4; ++n) {
+                    const float2 a = *reinterpret_cast<const float2 *>(from_start + 8 * n + 2 * t);
+                    const int2 e = *reinterpret_cast<const int2 *>(q_exp + 8 * n + 2 * t);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row_e = i & 1 ? e.y : e.x;
-                    const float of_state = o[n][i] * ((i & 1 ? a.y : a.x) * pow2(row_e + se[i >> 1]));
-                    o[n][i] = fmaf(c[n][i], pow2(row_e + kScoreUnit), of_state) * l.scale;
+                    for (int i = 0; i < 4; ++i) {
+                        const int of_state = (i & 1 ? e.y : e.x) + se[i >> 1], of_chunk = (i & 1 ? e.y : e.x) + c_exp;
+                        const float x = o[n][i] * (i & 1 ? a.y : a.x);
+                        if constexpr (two) o[n][i] = times_pow2(x, of_state) + times_pow2(c[n][i], of_chunk - v_up[i >> 1]);
+                        else o[n][i] = fmaf(c[n][i], pow2_of(of_chunk), x * pow2_of(of_state));
+                        o[n][i] *= l.scale;
+                    }
                 }
-            }
+            };
+            if (in_two) join(std::true_type{});
+            else join(std::false_type{});
             if (__any_sync(~0u, min(bad_from, min(v_bad[0], v_bad[1])) < C)) {
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
@@ -608,7 +640,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
             const float keep = bad_from < C ? NAN : gh[4 * C];
             float gain[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) gain[u] = v_bad[u] < C ? NAN : pow2(k_top + be[u]);
+            for (int u = 0; u < 2; ++u) gain[u] = v_bad[u] < C ? NAN : pow2_of(min(max(k_top + be[u], -126), 127));
+            // (as above; a loop of its own for this costs more registers than the branches in this one)
+            const bool wide = __any_sync(~0u, !is_normal(k_top + be[0]) || !is_normal(k_top + be[1]));
             const uint32_t kb = base + plan.k16 + ((lane & 7) + (((lane >> 3) & 1) << 3)) * PITCH + (lane >> 4) * 16;
 #pragma unroll
             for (int n2 = 0; n2 < KS; ++n2) {
@@ -627,6 +661,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) chunk_kernel(const __grid_c
                     mma(c[h], ah[1], bl[1][2 * h], bl[1][2 * h + 1]);
                     mma(c[h], ah[0], bh[0][2 * h], bh[0][2 * h + 1]);
                     mma(c[h], ah[1], bh[1][2 * h], bh[1][2 * h + 1]);
+                }
+                if (wide) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = k_top + be[i >> 1];
+                            c[h][i] *= pow2(e - min(max(e, -126), 127));
+                        }
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)

@@ -80,3 +80,48 @@ def test_rows_that_fade_as_fast_as_they_shrink(n_new, what):
     getattr(c, what)[:] *= (2.0 ** (60.0 - at * 1.26))[None, :, None, None].astype(np.float32)
     c.decay[:] = -2.0
     c.check()
+
+
+# powers of two that q, k, v and the state are multiplied by: what they give, and the products on the way there, are
+# numbers that fp32 holds
+RANGES = [(0, 0, -106, -106), (0, -106, 0, -106), (-83, -17, -17, -34), (-110, 0, 0, 0), (100, -60, -40, -100),
+          (60, -100, 40, -60), (-100, 60, 40, 100), (-90, 100, 15, 115), (110, -52, -53, -105), (-20, 118, -118, 0),
+          (0, -100, 118, 18), (118, -110, -5, -115), (4, 56, 56, 112), (-8, 2, 112, 114)]
+
+
+@pytest.mark.parametrize("n_new", [5, 9, 40, 70, 400])
+@pytest.mark.parametrize("powers", RANGES)
+def test_sizes_whose_products_fp32_holds(n_new, powers):
+    c = Case(n_new)
+    for name, n in zip("qkv", powers):
+        a = getattr(c, name)
+        a *= np.float32(2.0 ** n)
+    c.state *= np.float32(2.0 ** powers[3])
+    c.check()
+
+
+@pytest.mark.parametrize("n_new", [5, 9, 70, 400])
+def test_large_values_that_meet_zeros_give_zeros(n_new):
+    """q at one dim, k and the state's rows at others: every output is exactly zero, and the state what k v give."""
+    c = Case(n_new)
+    c.q[:], c.k[:] = 0, 0
+    c.q[..., 3], c.k[..., 5] = 2.0 ** 100, 2.0 ** 60
+    c.state *= np.float32(2.0 ** 60)
+    c.state[:, :, 3] = 0
+    out, _ = c.call()
+    assert (out == 0).all()
+    c.check()
+
+
+@pytest.mark.parametrize("n_new", [5, 40, 400])
+def test_rows_of_zeros_among_small_and_large_ones(n_new):
+    for power in (-100, 0, 100):
+        c = Case(n_new)
+        c.q *= np.float32(2.0 ** -power)
+        c.v *= np.float32(2.0 ** power)
+        c.state *= np.float32(2.0 ** power)
+        for a in (c.q, c.k, c.v):
+            a[:, ::3] = 0
+        c.check()
+        c.v[:] = 0
+        c.check()
