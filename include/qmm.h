@@ -599,7 +599,7 @@ typedef struct qmm_experts_ffn_args {
  * as sums of 16-bit terms: of a value, 22 bits or 2^-38 of the largest among 32
  * neighbours (of its row, above about 20 rows each), whichever is more (BF16 weights: 24 bits). One position, and few
  * rows, are taken row by row: for quantised weights values are kept to 2^-23 of the
- * largest among 32 neighbours, 16-bit weights are multiplied in fp32. Sums are
+ * largest among 32 neighbours or 2^-126, whichever is more, 16-bit weights are multiplied in fp32. Sums are
  * fp32; the same call gives the same result each time. An Inf or NaN in x
  * makes that position's outputs Inf or NaN. Stream-ordered, no
  * synchronization; scratch as for qmm_matmul_ex (calls that can run
