@@ -128,7 +128,7 @@ Split split_of(const Linear &l, const DeviceInfo &dev) {
 
 }  // namespace linear
 
-bool linear_supports(int dk, int dv) {
+bool linear_supports(int64_t dk, int64_t dv) {
     return dk >= 32 && dk <= 128 && dk % 32 == 0 && dv >= 32 && dv <= 256 && dv % 32 == 0;
 }
 
@@ -143,7 +143,8 @@ cudaError_t launch_linear(const Linear &l, const DeviceInfo &dev, cudaStream_t s
     case 32: return linear::launch_step<32>(l, s);
     case 64: return linear::launch_step<64>(l, s);
     case 96: return linear::launch_step<96>(l, s);
-    default: return linear::launch_step<128>(l, s);
+    case 128: return linear::launch_step<128>(l, s);
+    default: return cudaErrorInvalidValue;
     }
 }
 

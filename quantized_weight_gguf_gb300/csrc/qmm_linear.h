@@ -20,7 +20,7 @@ struct Linear {
     void *workspace;
 };
 // dims that the kernels take: dk 32, 64, 96 or 128, dv a multiple of 32 up to 256
-bool linear_supports(int dk, int dv);
+bool linear_supports(int64_t dk, int64_t dv);
 size_t linear_workspace_bytes(const Linear &l, const DeviceInfo &dev);
 cudaError_t launch_linear(const Linear &l, const DeviceInfo &dev, cudaStream_t s);
 

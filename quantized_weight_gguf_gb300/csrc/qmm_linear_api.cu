@@ -24,10 +24,9 @@ int check_rows(const char *name, const float *p, int64_t stride, int64_t width) 
 int check_linear(const qmm_linear_args *a, qmm::Linear *l, bool *empty, bool pointers) {
     if (!a) return set_error(QMM_ERR_NULL, "args is NULL");
     if (a->n_new < 1) return set_error(QMM_ERR_SHAPE, "n_new %lld < 1", (long long)a->n_new);
-    if (a->dk < 32 || a->dk > 128 || a->dk % 32)
-        return set_error(QMM_ERR_SHAPE, "dk %lld must be 32, 64, 96 or 128", (long long)a->dk);
-    if (a->dv < 32 || a->dv > 256 || a->dv % 32)
-        return set_error(QMM_ERR_SHAPE, "dv %lld must be a multiple of 32 up to 256", (long long)a->dv);
+    if (!qmm::linear_supports(a->dk, a->dv))
+        return set_error(QMM_ERR_SHAPE, "dk %lld must be 32, 64, 96 or 128, and dv %lld a multiple of 32 up to 256",
+                         (long long)a->dk, (long long)a->dv);
     if (a->n_heads < 1 || a->n_heads > 65536 || a->n_qk_heads < 1 || a->n_heads % a->n_qk_heads)
         return set_error(QMM_ERR_SHAPE, "n_heads %lld must be a multiple of n_qk_heads %lld up to 65536",
                          (long long)a->n_heads, (long long)a->n_qk_heads);

@@ -778,7 +778,8 @@ cudaError_t launch_chunks(const Linear &l, const Split &split, const DeviceInfo 
     case 32: return launch_dk<32>(p, s);
     case 64: return launch_dk<64>(p, s);
     case 96: return launch_dk<96>(p, s);
-    default: return launch_dk<128>(p, s);
+    case 128: return launch_dk<128>(p, s);
+    default: return cudaErrorInvalidValue;
     }
 }
 
