@@ -763,6 +763,9 @@ def _on_device(first, t, name, dtype, shape=None):
                          f"got {t.dtype} {tuple(t.shape)}")
 
 
+_KEPT_BYTES = 1 << 28
+
+
 class _Call:
     """A C call whose arguments' structure is packed from Python numbers in one go (a ctypes structure costs
     2 to 3 us to fill), with its scratch as the structure's fields `workspace` and `workspace_bytes`."""
@@ -791,7 +794,8 @@ class _Call:
 
     def with_scratch(self, values, workspace, first, stream, handle):
         """Calls with `workspace`, or (as attend does) the kept scratch of torch's current stream, or a
-        new tensor."""
+        new tensor. More than _KEPT_BYTES is not kept: the call goes on for long after it has been launched, and
+        torch's allocator has the memory again for others in the meantime."""
         if self.call is None:
             self._bind()
         at, ws = self.scratch_at, None
@@ -809,7 +813,7 @@ class _Call:
                         return
                     values[at] = values[at + 1] = 0
             need = self.need(self.pack(*values))
-            if need and keep:
+            if need and keep and need <= _KEPT_BYTES:
                 workspace = _scratch_of_stream(need, first.device, handle)
             elif need:
                 ws = workspace = torch.empty(need, dtype=torch.uint8, device=first.device)
