@@ -612,10 +612,11 @@ size_t qmm_experts_ffn_workspace_bytes(const qmm_experts_ffn_args *a);
 
 /* ---- Linear attention ----------------------------------------------------
  *
- * Attention whose memory is one matrix per head, with a decay for each head
- * (moeflux tests/graph_diff_oracle.rs, GatedDeltaNetStep and its chunked form,
- * without their delta rule): the layers that stand beside those of qmm_attend in
- * hybrid models. One call serves prompts and single tokens:
+ * Attention whose memory is one matrix per head, with a decay for each head: the
+ * layers that stand beside those of qmm_attend in hybrid models. (The gated delta
+ * step of moeflux tests/graph_diff_oracle.rs, GatedDeltaNetStep, is another
+ * operator: it takes out what the state holds for k before it adds to it.) One
+ * call serves prompts and single tokens:
  *     S_t = e^(g_t) S_(t-1) + k_t v_t^T,    o_t = scale * S_t^T q_t
  * for every sequence and head, rows t in order. Heads share q and k in groups:
  * head h takes those of q / k head h / (n_heads / n_qk_heads).
@@ -650,8 +651,9 @@ typedef struct qmm_linear_args {
     int flags;                 /* 0 */
 } qmm_linear_args;
 
-/* Decays are at most 0: greater ones count as 0, and -Inf clears the state
- * before its row (so do decays below -110, whose factor fp32 holds as 0). A NaN
+/* Decays are at most 0: greater ones count as 0, and -Inf clears a state of
+ * numbers before its row (so do decays below -110, whose factor fp32 holds as 0);
+ * a state that is not finite stays so, until a sequence begins anew. A NaN
  * decay or a k that is not finite makes the head's rows from its own on Inf or
  * NaN and spoils its state (up to 8 rows: where that k reaches it); a v that is
  * not finite does so for its dim; a q that is not finite makes its row's outputs

@@ -8,7 +8,7 @@ functions carry the C names (``qmm_matmul``, ``qmm_matmul_ex``,
 tensors; ``matmul``, ``dequant``, ``matmul_backward_input``,
 ``matmul_experts``, ``matmul_affine``, ``dequant_affine`` and ``matmul_glu``
 are tensor-level conveniences over them, and so are ``KvCache``,
-``kv_append``, ``kv_read`` and ``attend`` over the paged key-value cache, 
+``kv_append``, ``kv_read`` and ``attend`` over the paged key-value cache,
 ``route_experts`` and ``experts_ffn`` of mixture-of-experts layers, and
 ``linear_attend``.
 If ``libqmm.so`` has not been built, every call raises: there is no fallback.
@@ -866,9 +866,10 @@ def experts_ffn(act, fmt, w_gate, w_up, fmt_down, w_down, x, ids, weights, k: in
                 y=None, accumulate=False, workspace=None, stream=None):
     """The gated feed-forward network ("swiglu" / "geglu") of the experts that ids (int32 [n_pos,
     top_k], -1: none) name, weighted and summed: x float32 [n_pos, k] to y float32 [n_pos, k] (the
-    given y when passed, which may be x; added to with `accumulate`). w_gate and w_up hold n_experts
-    slices of n_ff rows of k weights in `fmt`, w_down of k rows of n_ff weights in `fmt_down`, uint8.
-    Scratch is `workspace` (uint8) when given; else as for attend."""
+    given y when passed, which may be x; added to with `accumulate`, which without y changes nothing).
+    w_gate and w_up hold n_experts slices of n_ff rows of k weights in `fmt`, w_down of k rows of n_ff
+    weights in `fmt_down`, uint8.
+    Scratch is `workspace` (uint8) when given; else as for attend, but no more than 256 MB is kept."""
     torch = _torch()
     if x.dim() == 1:
         x = x.unsqueeze(0)
@@ -938,8 +939,8 @@ def linear_attend(q, k, v, decay, state, lens=None, *, scale=None, out=None, sta
     [n_seqs, n_new, n_heads] (rows may be strided) or [n_heads], state [n_seqs, n_heads, dk, dv], scale
     1 / sqrt(dk) unless given. With `lens` (int32 [n_seqs], the new rows counted) rows are each sequence's last
     positions, and a sequence that begins among them begins at a state of zeros. Returns out, shaped like v (the
-    given one when passed); the states after the last row go to state_out, by default over `state`. Scratch is
-    `workspace` (uint8) when given; else as for attend."""
+    given one when passed, which overlaps no input); the states after the last row go to state_out, by default over
+    `state`. Scratch is `workspace` (uint8) when given; else as for attend, but no more than 256 MB is kept."""
     torch = _torch()
     here = v.get_device()
     (q_shape, q_row), (k_shape, k_row), (v_shape, v_row) = (_head_rows(*t, here) for t in (("q", q), ("k", k), ("v", v)))

@@ -263,6 +263,7 @@ bool is_one(const ExpertsFfn &f) { return f.n_pos == 1 && (f.k + 31) / 32 <= kOn
 //   Q8_0    1:23 8:40   1:66 8:74   1:89  8:89  8:139 16:137  16:181 T:244  16:255 T:257  16:287 T:264  16:505 T:478
 //   Q6_K    1:31 8:48   1:99 8:97  1:141 8:117  8:190 16:182  16:237 T:300  16:341 T:314  16:407 T:324  16:689 T:582
 //   BF16    1:33 8:45   1:93 8:94  1:129 8:106  8:146 16:154
+// One set of borders for all formats: at the sizes above it gives away up to 15 % (Q4_K at 3/2 rows), and 2 to 4 % at 8.
 // Tiles on tcgen05 are for codes, whose blocks' sums a scale multiplies on their way out.
 bool is_tile(const ExpertsFfn &f) {
     const bool codes = f.fmt != F_BF16 && f.fmt != F_F16 && f.fmt_down != F_BF16 && f.fmt_down != F_F16;

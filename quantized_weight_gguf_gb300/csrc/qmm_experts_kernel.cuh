@@ -6,8 +6,8 @@
 // and the CTA's warps share the activations' terms, both by cp.async into a
 // later stage than the one being multiplied, also across units.
 //
-// Bound by unpacking and scales, 135 instructions per 16 x 16 x 32 of Q4_K, of which 8 are products (issue slots 60 %
-// used, tensor pipe 28 %); BF16 weights by their three terms and DRAM. Measured: 24 positions of 1536 x 640, six of 40,
+// Bound by unpacking and scales, about 130 instructions per 16 x 16 x 32 of Q4_K, of which 8 are products (issue slots 58
+// to 68 % used, tensor pipe 17 to 29 %); BF16 weights by their three terms and DRAM. Measured: 24 positions of 1536 x 640, six of 40,
 // BF16 56 us (0.61 of the copy rate); Q4_K 2048 x 768, eight of 64, 8 rows an expert 147 us, 16 rows 186 us.
 #pragma once
 

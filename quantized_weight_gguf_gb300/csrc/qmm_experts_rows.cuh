@@ -6,8 +6,9 @@
 // integers: an activation is split into three signed digits of 8 bits under a power of two per block (24 bits,
 // to 2^-23 of the block's largest), codes are unpacked to bytes, and four products are one dp4a. A block's integer sums
 // are exact; they become floats without a conversion, since they start from the bit pattern of 1.5 * 2^23,
-// less the codes' zero point times the digits' sum. 24 dp4a and 30 to 45 other instructions a block, half of
-// what fragments for the tensor cores take for so few columns. 16-bit weights: fp32 multiply-adds.
+// less the codes' zero point times the digits' sum. 24 dp4a of 95 to 106 instructions a warp for 32 blocks (Q4_0, Q8_0; copies
+// and sums among them); tiles for the tensor cores take 74 instead of 66 us at one row per expert of Q8_0. 16-bit weights:
+// fp32 multiply-adds.
 //
 // A unit of work of the first product is 32 rows of a pair's gate matrix and the same 32 of its up matrix (one block of
 // the second product's activations); of the second 16 rows of y, over the blocks of the position's slots as one long
@@ -17,10 +18,10 @@
 //
 // One position: the first product turns x into digits itself while its first weights are on their way.
 //
-// Bound by instructions and their latency (issue slots 48 to 58 % used at the sizes where all SMs are busy) on one side, by
-// fixed steps on the other. Measured: 4096 x 14336, two of 8 experts, Q4_0 59.7 us (0.49 of the copy rate); eight
-// positions, Q8_0 64 us (0.48); 2048 x 768, eight of 64, Q4_K / Q6_K 17.5 us, of which about 8 are the first and last
-// loads' latency; five positions of 1376 x 352, Q5_0 / Q8_0 20.4 us.
+// Bound by the latency that 12 to 16 warps an SM do not hide (111 to 128 registers; issue slots 47 to 58 % used and DRAM
+// half where all SMs are busy), and by fixed steps where the work is small. Measured: 4096 x 14336, two of 8 experts, Q4_0
+// 59.8 us (0.49 of the copy rate); eight positions, Q8_0 64 us (0.48); 2048 x 768, eight of 64, Q4_K / Q6_K 17.5 us,
+// BF16 17.2 us; five positions of 1376 x 352, Q5_0 / Q8_0 20.5 us.
 #pragma once
 
 #include "qmm_experts_kernel.cuh"

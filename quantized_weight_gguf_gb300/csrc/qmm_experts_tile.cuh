@@ -12,8 +12,9 @@
 // a block, into the 128-byte swizzle that the products read, and one lane of it issues them: four per block (two
 // 16-deep steps, the low term's first).
 //
-// Bound by the warps that unpack and take, whose time hardly depends on the columns: 1390 instructions a block and CTA of
-// Q4_K, of which about 130 unpack, 190 take the mins and 360 the sums; issue slots 51 to 58 % used, the tensor pipe 11 %.
+// Bound by the warps that unpack and take, whose time hardly depends on the columns: about 1450 instructions a block and
+// CTA of Q4_K against four products (98.2 M of warps in the first product below), at 20 warps an SM, held there by registers
+// and tensor memory; issue slots 51 to 58 % used, the tensor pipe 11 %.
 // Four CTAs an SM (286 us with three, 259 with four, before the last change of the codes). Measured: 256 positions, Q4_K
 // 2048 x 1024, eight of 64 experts 274 us, of which the first product 178, the second 79 (mma.sync: 395); 128 rows an
 // expert at 2048 x 768 560 us (903). Blocks in pairs per handshake took 300 us instead of 268 (one stage of D, so that a

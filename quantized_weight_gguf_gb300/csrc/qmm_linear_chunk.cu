@@ -19,11 +19,12 @@
 // A prompt too short of sequences and heads to fill the GPU is cut into segments: their own end states
 // first (one product of the four), a scan over the segments, then everything.
 //
-// Bound by instructions at 16 warps an SM, whose states take the registers: 2420 of a warp a chunk at dk = dv = 128, of
-// which 246 are products; the issue slots are half used, the tensor pipe 36 %, shared memory's data path 57 %.
-// Measured: 12001 rows of 16 heads of 128 / 128 310 us (92 the segments' own states, 210 the second pass), six ragged
-// sequences to 1777 rows of 12 heads of 64 / 96 133 us, against 58 and 17 us that their bytes take. The decays' sums in
-// one warp, terms in vectors and factors read instead of formed took the first from 477 us.
+// Bound by instructions and the latency that 16 warps an SM, whose states take the registers, do not hide: 2540 a warp and
+// chunk at dk = dv = 128, of which 246 are products (1080 in the segments' own states); issue slots 48 % used, tensor pipe
+// 37 %. Measured: 12001 rows of 16 heads of 128 / 128 325 us (91 the segments' own states, 227 the second pass), six ragged
+// sequences to 1777 rows of 12 heads of 64 / 96 141 us, against 58 and 17 us that their bytes take. The decays' sums in
+// one warp, terms in vectors and factors read instead of formed took the first from 477 us to 310; three terms of scores
+// and v, and powers of two beyond fp32's exponents, cost 15 us of that.
 #include "qmm_device.cuh"
 #include "qmm_linear.h"
 
