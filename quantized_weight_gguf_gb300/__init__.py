@@ -204,13 +204,16 @@ def _keep_until_done(buf, stream):
     """A per-call scratch tensor allocated on torch's current stream but used
     by kernels on another stream: tell the caching allocator, so the memory
     is not handed out again before that stream's work is done."""
-    if buf is None or stream is None or stream == 0:
+    if buf is None or stream is None:
         return
     import torch
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
-        int(getattr(stream, "cuda_stream", stream)), device=buf.device)
-    if s.cuda_stream != torch.cuda.current_stream(buf.device).cuda_stream:
-        buf.record_stream(s)
+    handle = int(getattr(stream, "cuda_stream", stream))
+    if handle == torch.cuda.current_stream(buf.device).cuda_stream:
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.default_stream(buf.device) if handle == 0 else \
+            torch.cuda.ExternalStream(handle, device=buf.device)
+    buf.record_stream(stream)
 
 
 def _stream(stream):

@@ -55,3 +55,20 @@ def test_weights_that_would_have_to_be_copied_are_refused():
         call(ids=ids[0], weights=weights.view(4, 2).t())
     with pytest.raises(ValueError):
         call(ids=ids[0], weights=weights.repeat(2, 1).t()[:, 0].as_strided((8,), (2,)))
+
+
+@pytest.mark.parametrize("n_pos", [1, 6])
+def test_scratch_of_a_call_on_the_default_stream_stays_its_own(n_pos):
+    """Its memory is not handed out on the current stream while the default one, which is busy, has yet to use it."""
+    call, _, _ = _case(n_pos)
+    want = call()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        y = torch.empty_like(want)
+        with torch.cuda.stream(torch.cuda.default_stream()):
+            torch.cuda._sleep(100_000_000)
+        call(y=y, stream=0)
+        others = [torch.full((size,), 255, dtype=torch.uint8, device=DEV) for size in (1 << 12, 1 << 14, 1 << 16, 1 << 18)]
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and all((o == 255).all() for o in others)
